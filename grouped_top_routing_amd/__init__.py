@@ -18,4 +18,8 @@ from ._lib import (  # noqa: F401
     layer_forward_noalloc, lib, make_config,
     pack_weights, permute, quantize_fp8, route, route_replay, status_string, workspace_bytes,
     LIB_CHECKED_PATH, CHECK_BITS, check_flags, use_library,
+    DTYPE_BF16, DTYPE_FP32, ENTRY_ROUTE_BACKWARD,
+)
+from ._train import (  # noqa: F401
+    AdamW, RouterTrainer, combine_backward, dispatch, dispatch_backward, route_backward,
 )

@@ -36,10 +36,14 @@ ENTRY_LAYER = 3
 ENTRY_EXPERT_STAGE = 4
 ENTRY_EXPERT_FFN_LORA = 5
 ENTRY_LAYER_LORA = 6
+ENTRY_ROUTE_BACKWARD = 8
 
 LAYOUT_ROW_MAJOR = 0
 LAYOUT_PACKED = 1
 LAYOUT_FP8_PACKED = 2
+
+DTYPE_BF16 = 0
+DTYPE_FP32 = 1
 
 #: Every symbol include/beam_moe.h declares.
 EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_route_replay", "moe_permute",
@@ -47,7 +51,9 @@ EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_route_replay", "moe_permute"
            "moe_layer_forward", "moe_pack_weights", "moe_quantize_fp8", "moe_expert_ffn_fp8",
            "moe_expert_gate_up_fp8", "moe_expert_down_fp8", "moe_layer_forward_fp8",
            "moe_expert_ffn_lora", "moe_layer_forward_lora", "moe_layer_forward_noalloc",
-           "moe_debug_check_flags", "moe_status_string")
+           "moe_debug_check_flags", "moe_status_string", "moe_route_logits", "moe_dispatch",
+           "moe_dispatch_backward", "moe_combine_rows", "moe_combine_backward",
+           "moe_route_backward", "moe_adamw_step")
 
 
 class MoeConfig(ctypes.Structure):
@@ -73,6 +79,38 @@ class MoeLora(ctypes.Structure):
         ("b_down", ctypes.c_void_p),
         ("rank", ctypes.c_int32),
         ("scale", ctypes.c_float),
+    ]
+
+
+class MoeAdamwTensor(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("master", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("param_dtype", ctypes.c_int32),
+        ("grad_dtype", ctypes.c_int32),
+        ("state_bits", ctypes.c_int32),
+    ]
+
+
+class MoeAdamw(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("weight_decay", ctypes.c_double),
+        ("grad_scale", ctypes.c_double),
+        ("step", ctypes.c_int64),
+        ("step_dev", ctypes.c_void_p),
+        ("lr_dev", ctypes.c_void_p),
+        ("grad_scale_dev", ctypes.c_void_p),
+        ("seed", ctypes.c_uint32),
     ]
 
 
@@ -121,6 +159,13 @@ def load(path: str) -> ctypes.CDLL:
     LP = ctypes.POINTER(MoeLora)
     L.moe_expert_ffn_lora.argtypes = [CP, P, P, P, P, P, LP, P, P, Z, P]
     L.moe_layer_forward_lora.argtypes = [CP, P, P, P, P, P, LP, P, P, P, P, Z, P]
+    L.moe_route_logits.argtypes = [CP, P, P, P, I, P, P, P, P, Z, P]
+    L.moe_dispatch.argtypes = [CP, I, P, P, P, P, P]
+    L.moe_dispatch_backward.argtypes = [CP, I, P, P, P, P, P, P, P]
+    L.moe_combine_rows.argtypes = [CP, I, P, P, P, P, P]
+    L.moe_combine_backward.argtypes = [CP, I, P, P, P, P, P, P, P]
+    L.moe_route_backward.argtypes = [CP, P, P, P, P, P, P, P, P, I, P, P, P, Z, P]
+    L.moe_adamw_step.argtypes = [ctypes.POINTER(MoeAdamw), ctypes.POINTER(MoeAdamwTensor), I, P]
     L.moe_debug_check_flags.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
     L.moe_status_string.argtypes = [I]
     L.moe_status_string.restype = ctypes.c_char_p
@@ -238,8 +283,10 @@ def _call(name, code):
 
 
 def route(x, w_router, *, sel_bias=None, num_groups=8, topk_groups=4, topk=8, renormalize=True,
-          workspace=None):
-    """Router: returns (topk_ids int32 [T, k], topk_w fp32 [T, k])."""
+          return_logits=False, workspace=None):
+    """Router: returns (topk_ids int32 [T, k], topk_w fp32 [T, k]), and with
+    return_logits the chosen experts' router logits too (fp32 [T, k], what
+    route_backward starts from)."""
     T, H = x.shape
     E = w_router.shape[0]
     _check(x, "x", torch.bfloat16)
@@ -252,13 +299,20 @@ def route(x, w_router, *, sel_bias=None, num_groups=8, topk_groups=4, topk=8, re
     w = torch.empty(T, topk, dtype=torch.float32, device=x.device)
     nb = workspace_bytes(cfg, ENTRY_ROUTE)
     ws = _ws(workspace, x.device).get(nb, x.device)
+    if return_logits:
+        z = torch.empty(T, topk, dtype=torch.float32, device=x.device)
+        _call("moe_route_logits", lib().moe_route_logits(
+            ctypes.byref(cfg), _ptr(x), _ptr(w_router), _ptr(sel_bias), 0, _ptr(ids), _ptr(w),
+            _ptr(z), _ptr(ws), nb, _stream(x.device)))
+        return ids, w, z
     _call("moe_route", lib().moe_route(ctypes.byref(cfg), _ptr(x), _ptr(w_router), _ptr(sel_bias),
                                        _ptr(ids), _ptr(w), _ptr(ws), nb, _stream(x.device)))
     return ids, w
 
 
-def route_replay(x, w_router, topk_ids, *, renormalize=True, workspace=None):
-    """Combine weights for caller-supplied expert ids: fp32 [T, k]."""
+def route_replay(x, w_router, topk_ids, *, renormalize=True, return_logits=False, workspace=None):
+    """Combine weights for caller-supplied expert ids: fp32 [T, k]; with
+    return_logits (weights, router logits), both fp32 [T, k]."""
     T, H = x.shape
     E = w_router.shape[0]
     k = topk_ids.shape[1]
@@ -270,6 +324,12 @@ def route_replay(x, w_router, topk_ids, *, renormalize=True, workspace=None):
     w = torch.empty(T, k, dtype=torch.float32, device=x.device)
     nb = workspace_bytes(cfg, ENTRY_ROUTE)
     ws = _ws(workspace, x.device).get(nb, x.device)
+    if return_logits:
+        z = torch.empty(T, k, dtype=torch.float32, device=x.device)
+        _call("moe_route_logits", lib().moe_route_logits(
+            ctypes.byref(cfg), _ptr(x), _ptr(w_router), None, 1, _ptr(topk_ids), _ptr(w),
+            _ptr(z), _ptr(ws), nb, _stream(x.device)))
+        return w, z
     _call("moe_route_replay", lib().moe_route_replay(ctypes.byref(cfg), _ptr(x), _ptr(w_router),
                                                      _ptr(topk_ids), _ptr(w), _ptr(ws), nb,
                                                      _stream(x.device)))
@@ -357,9 +417,11 @@ def expert_down(h, offsets, w_down, *, topk=8, weight_layout=LAYOUT_ROW_MAJOR, w
 
 
 def combine(y_perm, perm_dst, topk_w, *, routed_scaling=2.5):
-    """Weighted un-permute: out bf16 [T, H]."""
+    """Weighted un-permute: out [T, H], bf16 or fp32 as y_perm."""
     T, k = topk_w.shape
     H = y_perm.shape[1]
+    if y_perm.dtype == torch.float32 or H % 256:
+        return _combine_rows(y_perm, perm_dst, topk_w, routed_scaling)
     _check(y_perm, "y_perm", torch.bfloat16)
     _check(perm_dst, "perm_dst", torch.int32, (T * k,), y_perm.device)
     _check(topk_w, "topk_w", torch.float32, (T, k), y_perm.device)
@@ -368,6 +430,24 @@ def combine(y_perm, perm_dst, topk_w, *, routed_scaling=2.5):
     out = torch.empty(T, H, dtype=torch.bfloat16, device=y_perm.device)
     _call("moe_combine", lib().moe_combine(ctypes.byref(cfg), _ptr(y_perm), _ptr(perm_dst),
                                            _ptr(topk_w), _ptr(out), _stream(y_perm.device)))
+    return out
+
+
+def _combine_rows(y_perm, perm_dst, topk_w, routed_scaling):
+    """combine for fp32 rows and for widths that are no multiple of 256."""
+    T, k = topk_w.shape
+    H = y_perm.shape[1]
+    dt = y_perm.dtype if y_perm.dtype == torch.float32 else torch.bfloat16
+    _check(y_perm, "y_perm", dt, (T * k, H))
+    _check(perm_dst, "perm_dst", torch.int32, (T * k,), y_perm.device)
+    _check(topk_w, "topk_w", torch.float32, (T, k), y_perm.device)
+    cfg = make_config(T, H, 128, num_groups=1, topk_groups=1, topk=k,
+                      routed_scaling=routed_scaling)
+    out = torch.empty(T, H, dtype=dt, device=y_perm.device)
+    if T:
+        _call("moe_combine_rows", lib().moe_combine_rows(
+            ctypes.byref(cfg), DTYPE_FP32 if dt == torch.float32 else DTYPE_BF16, _ptr(y_perm),
+            _ptr(perm_dst), _ptr(topk_w), _ptr(out), _stream(y_perm.device)))
     return out
 
 

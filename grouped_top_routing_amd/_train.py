@@ -1,0 +1,411 @@
+"""ctypes binding of the training calls: rows sorted by expert and back with
+their gradients, the router's gradient, AdamW, and the router's training loop
+made of them.
+
+As in the rest of the binding, every step runs in the library's HIP kernels on
+the current stream of the tensors' device; nothing falls back to torch.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from . import _lib
+from ._lib import (DTYPE_BF16, DTYPE_FP32, ENTRY_ROUTE_BACKWARD, LAYOUT_ROW_MAJOR, Fp8Weights,
+                   MoeAdamw, MoeAdamwTensor, _call, _check, _ws, make_config, workspace_bytes)
+
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_of(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+_NOTHING = contextlib.nullcontext()
+
+
+def _on(device):
+    """Launches go to the tensors' device, whichever is current."""
+    if device.index == torch.cuda.current_device():
+        return _NOTHING
+    return torch.cuda.device(device)
+
+
+def _scratch(nbytes, device, workspace):
+    """The call's workspace.  Under graph capture a buffer of the graph's own
+    pool, so that no other graph or eager call shares it."""
+    if workspace is None and torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _ws(workspace, device).get(nbytes, device)
+
+
+def _check_rows(t, name, shape, dtype=None, device=None):
+    """Row tensors are bf16 or fp32, one type in a call."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    _check(t, name, dtype or t.dtype, shape, device)
+
+
+def _tokens_of(perm_dst, topk):
+    """T of perm_dst [T*topk]."""
+    if not isinstance(perm_dst, torch.Tensor):
+        raise TypeError("perm_dst must be a torch.Tensor")
+    if perm_dst.dim() != 1 or topk < 1 or perm_dst.numel() % topk:
+        raise ValueError(f"perm_dst must have shape (T * {topk},), got {tuple(perm_dst.shape)}")
+    return perm_dst.numel() // topk
+
+
+def _rows_config(T, H, topk, scale=1.0):
+    return make_config(T, H, 128, num_groups=1, topk_groups=1, topk=topk, routed_scaling=scale)
+
+
+def dispatch(x, perm_dst, *, topk=8, topk_w=None, out=None):
+    """Tokens sorted by expert: x_perm [T*k, H] with x_perm[perm_dst[t*k + j]] =
+    x[t], times topk_w[t, j] (fp32 [T, k]) where that is given.  x is bf16 or
+    fp32, of any width.
+
+    Rows that no pair names (as many as perm_dst has entries of -1, the last
+    ones of moe_permute's order) are left as ``out`` holds them; without
+    ``out`` they are not initialised."""
+    T = _tokens_of(perm_dst, topk)
+    _check_rows(x, "x", None)
+    H = x.shape[-1]
+    _check(x, "x", x.dtype, (T, H))
+    _check(perm_dst, "perm_dst", torch.int32, (T * topk,), x.device)
+    if topk_w is not None:
+        _check(topk_w, "topk_w", torch.float32, (T, topk), x.device)
+    if out is None:
+        out = torch.empty(T * topk, H, dtype=x.dtype, device=x.device)
+    else:
+        _check(out, "out", x.dtype, (T * topk, H), x.device)
+    if T:
+        cfg = _rows_config(T, H, topk)
+        with _on(x.device):
+            _call("moe_dispatch", _lib.lib().moe_dispatch(
+                ctypes.byref(cfg), _DTYPES[x.dtype], _at(x), _at(perm_dst), _at(topk_w), _at(out),
+                _stream_of(x.device)))
+    return out
+
+
+def dispatch_backward(grad_x_perm, perm_dst, *, topk=8, x=None, topk_w=None):
+    """Gradient of dispatch: grad_x [T, H], the (weighted) sum of each token's
+    rows of grad_x_perm [T*k, H].  With x and topk_w given, (grad_x,
+    grad_topk_w fp32 [T, k]); with topk_w alone, grad_x."""
+    T = _tokens_of(perm_dst, topk)
+    _check_rows(grad_x_perm, "grad_x_perm", None)
+    H, dt, dev = grad_x_perm.shape[-1], grad_x_perm.dtype, grad_x_perm.device
+    _check(grad_x_perm, "grad_x_perm", dt, (T * topk, H))
+    _check(perm_dst, "perm_dst", torch.int32, (T * topk,), dev)
+    if topk_w is not None:
+        _check(topk_w, "topk_w", torch.float32, (T, topk), dev)
+    if x is not None:
+        if topk_w is None:
+            raise ValueError("x is for the gradient of topk_w: pass topk_w too")
+        _check(x, "x", dt, (T, H), dev)
+    grad_x = torch.empty(T, H, dtype=dt, device=dev)
+    grad_w = None if x is None else torch.empty(T, topk, dtype=torch.float32, device=dev)
+    if T:
+        cfg = _rows_config(T, H, topk)
+        with _on(dev):
+            _call("moe_dispatch_backward", _lib.lib().moe_dispatch_backward(
+                ctypes.byref(cfg), _DTYPES[dt], _at(grad_x_perm), _at(perm_dst), _at(topk_w),
+                _at(x), _at(grad_x), _at(grad_w), _stream_of(dev)))
+    return grad_x if x is None else (grad_x, grad_w)
+
+
+def combine_backward(grad_out, y_perm, perm_dst, topk_w, *, routed_scaling=2.5, need_grad_y=True,
+                     need_grad_w=True, out=None):
+    """Gradient of combine: (grad_y_perm [T*k, H], grad_topk_w fp32 [T, k]);
+    None in the place of one that is not needed.  y_perm may be None without
+    need_grad_w.  Rows of grad_y_perm that no pair names are left as ``out``
+    holds them (without ``out``: not initialised)."""
+    if not (need_grad_y or need_grad_w):
+        raise ValueError("combine_backward: no gradient asked for")
+    if not isinstance(topk_w, torch.Tensor) or topk_w.dim() != 2:
+        raise TypeError("topk_w must be a torch.Tensor [T, k]")
+    T, k = topk_w.shape
+    _check_rows(grad_out, "grad_out", None)
+    H, dt, dev = grad_out.shape[-1], grad_out.dtype, grad_out.device
+    _check(grad_out, "grad_out", dt, (T, H))
+    _check(perm_dst, "perm_dst", torch.int32, (T * k,), dev)
+    _check(topk_w, "topk_w", torch.float32, (T, k), dev)
+    if y_perm is not None:
+        _check(y_perm, "y_perm", dt, (T * k, H), dev)
+    elif need_grad_w:
+        raise ValueError("the gradient of topk_w needs y_perm")
+    grad_y = grad_w = None
+    if need_grad_y:
+        if out is None:
+            grad_y = torch.empty(T * k, H, dtype=dt, device=dev)
+        else:
+            _check(out, "out", dt, (T * k, H), dev)
+            grad_y = out
+    if need_grad_w:
+        grad_w = torch.empty(T, k, dtype=torch.float32, device=dev)
+    if T:
+        cfg = _rows_config(T, H, k, routed_scaling)
+        with _on(dev):
+            _call("moe_combine_backward", _lib.lib().moe_combine_backward(
+                ctypes.byref(cfg), _DTYPES[dt], _at(grad_out), _at(y_perm), _at(perm_dst),
+                _at(topk_w), _at(grad_y), _at(grad_w), _stream_of(dev)))
+    return grad_y, grad_w
+
+
+def route_backward(x, w_router, topk_ids, topk_logits, grad_topk_w, perm_src, offsets, *,
+                   renormalize=True, grad_x_add=None, need_grad_x=True, grad_w_router=None,
+                   workspace=None):
+    """Gradient of route / route_replay: (grad_w_router fp32 [E, H], grad_x bf16
+    [T, H] or None), from the gradient of the combine weights.
+
+    topk_logits is what route(..., return_logits=True) returned; perm_src and
+    offsets are permute's for the same ids.  ``grad_x_add`` (bf16 [T, H], the
+    hidden state's gradient through the experts) is added into grad_x before
+    its one rounding.  A ``grad_w_router`` passed in is added to (gradients of
+    several micro-batches) and returned."""
+    _check(x, "x", torch.bfloat16)
+    if x.dim() != 2:
+        raise ValueError(f"x must have shape (T, H), got {tuple(x.shape)}")
+    T, H = x.shape
+    dev = x.device
+    if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2:
+        raise TypeError("topk_ids must be a torch.Tensor [T, k]")
+    k = topk_ids.shape[1]
+    E = w_router.shape[0]
+    _check(w_router, "w_router", torch.float32, (E, H), dev)
+    _check(topk_ids, "topk_ids", torch.int32, (T, k), dev)
+    _check(topk_logits, "topk_logits", torch.float32, (T, k), dev)
+    _check(grad_topk_w, "grad_topk_w", torch.float32, (T, k), dev)
+    _check(perm_src, "perm_src", torch.int32, (T * k,), dev)
+    _check(offsets, "offsets", torch.int32, (E + 1,), dev)
+    if grad_x_add is not None:
+        if not need_grad_x:
+            raise ValueError("grad_x_add without need_grad_x")
+        _check(grad_x_add, "grad_x_add", torch.bfloat16, (T, H), dev)
+    accumulate = grad_w_router is not None
+    if accumulate:
+        _check(grad_w_router, "grad_w_router", torch.float32, (E, H), dev)
+    cfg = make_config(T, H, 128, num_experts=E, num_groups=1, topk_groups=1, topk=k,
+                      renormalize=renormalize)
+    nb = workspace_bytes(cfg, ENTRY_ROUTE_BACKWARD)
+    grad_x = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if need_grad_x else None
+    if T == 0:
+        return (grad_w_router if accumulate else torch.zeros_like(w_router)), grad_x
+    if not accumulate:
+        grad_w_router = torch.empty(E, H, dtype=torch.float32, device=dev)
+    with _on(dev):
+        ws = _scratch(nb, dev, workspace)
+        _call("moe_route_backward", _lib.lib().moe_route_backward(
+            ctypes.byref(cfg), _at(x), _at(w_router), _at(topk_ids), _at(topk_logits),
+            _at(grad_topk_w), _at(perm_src), _at(offsets), _at(grad_x_add), int(accumulate),
+            _at(grad_w_router), _at(grad_x), _at(ws), nb, _stream_of(dev)))
+    return grad_w_router, grad_x
+
+
+# ---------------------------------------------------------------------------
+# AdamW
+class AdamW:
+    """AdamW (decoupled weight decay) over a list of tensors, all updated by one
+    call (a launch per 40 tensors).
+
+    params: fp32 tensors, or bf16 ones, which get an fp32 master copy that the
+    update works on; contiguous, 16-byte aligned, on one device, updated in
+    place.  state_bits: 32, or 8 for states in E4M3 codes with a power-of-two
+    scale per 32 elements (2.06 bytes per element instead of 8), rounded
+    stochastically from ``seed``.
+
+    ``state`` is a dict of lists, one entry per parameter: ``exp_avg``,
+    ``exp_avg_sq`` (with 8 bits the codes of its square root), with 8 bits
+    ``exp_avg_scale`` and ``exp_avg_sq_scale``, and ``master`` (None for fp32
+    parameters).  Pass one in, with ``step_count``, to continue from a
+    checkpoint; its tensors are used, not copied.
+
+    ``capturable`` keeps the step number on the device, so that a captured
+    step counts on in each replay."""
+
+    def __init__(self, params, *, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2,
+                 state_bits=32, seed=0, state=None, step_count=0, capturable=False):
+        self.params = tuple(params)
+        if not self.params:
+            raise ValueError("AdamW: no parameters")
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
+        if step_count < 0:
+            raise ValueError("step_count must not be negative")
+        for i, p in enumerate(self.params):
+            _check_rows(p, f"params[{i}]", None, None, getattr(self.params[0], "device", None))
+        self.device = self.params[0].device
+        self.lr, self.betas, self.eps = lr, tuple(betas), eps
+        self.weight_decay, self.state_bits, self.seed = weight_decay, state_bits, seed
+        self.step_count = step_count
+        self._step_dev = None
+        if capturable:
+            self._step_dev = torch.full((1,), step_count, dtype=torch.int64, device=self.device)
+        self.state = self._new_state() if state is None else self._taken(state)
+        self._list = (MoeAdamwTensor * len(self.params))()
+        for i, p in enumerate(self.params):
+            d, s = self._list[i], {k: v[i] for k, v in self.state.items()}
+            d.master, d.m, d.v = _at(s["master"]), _at(s["exp_avg"]), _at(s["exp_avg_sq"])
+            if state_bits == 8:
+                d.m_scale, d.v_scale = _at(s["exp_avg_scale"]), _at(s["exp_avg_sq_scale"])
+            d.param_dtype, d.state_bits = _DTYPES[p.dtype], state_bits
+
+    def _kinds(self):
+        """The state's lists and their element types."""
+        if self.state_bits == 32:
+            return {"exp_avg": torch.float32, "exp_avg_sq": torch.float32}
+        return {"exp_avg": torch.float8_e4m3fn, "exp_avg_sq": torch.float8_e4m3fn,
+                "exp_avg_scale": torch.float8_e8m0fnu, "exp_avg_sq_scale": torch.float8_e8m0fnu}
+
+    def _new_state(self):
+        state = {"master": tuple(p.float() if p.dtype == torch.bfloat16 else None
+                                 for p in self.params)}
+        for k, dt in self._kinds().items():
+            state[k] = tuple(
+                torch.zeros((p.numel() + 31) // 32 if k.endswith("scale") else p.shape,
+                            dtype=torch.uint8 if dt.itemsize == 1 else dt,
+                            device=self.device).view(dt) for p in self.params)
+        return state
+
+    def _taken(self, state):
+        state = dict(state)
+        if "master" not in state and all(p.dtype == torch.float32 for p in self.params):
+            state["master"] = [None] * len(self.params)
+        want = set(self._kinds()) | {"master"}
+        if set(state) != want:
+            raise ValueError(f"state must hold {sorted(want)}, got {sorted(state)}")
+        for k, v in state.items():
+            if len(v) != len(self.params):
+                raise ValueError(f"state[{k!r}] must have {len(self.params)} entries, got {len(v)}")
+            for i, (p, t) in enumerate(zip(self.params, v)):
+                name = f"state[{k!r}][{i}]"
+                if k == "master" and p.dtype == torch.float32:
+                    if t is not None:
+                        raise ValueError(f"{name} must be None: its parameter is fp32")
+                    continue
+                _check(t, name, self._kinds().get(k, torch.float32), None, self.device)
+                n = (p.numel() + 31) // 32 if k.endswith("scale") else p.numel()
+                if t.numel() != n:
+                    raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+        return {k: tuple(v) for k, v in state.items()}
+
+    def _scalar(self, v, name):
+        """(host value, device pointer) of a number or a one-element fp32 tensor."""
+        if isinstance(v, torch.Tensor):
+            _check(v, name, torch.float32, None, self.device)
+            if v.numel() != 1:
+                raise ValueError(f"{name} must have one element, got {v.numel()}")
+            return None, v.data_ptr()
+        return float(v), None
+
+    def step(self, grads, *, lr=None, grad_scale=1.0):
+        """One step.  grads: one tensor (bf16 or fp32, the parameter's shape)
+        per parameter, or None to leave that parameter and its state alone.
+        lr (default: the constructor's) and grad_scale, a factor on every
+        gradient, are numbers or one-element fp32 device tensors."""
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(self.params)} gradients expected, got {len(grads)}")
+        for i, (p, g, d) in enumerate(zip(self.params, grads, self._list)):
+            if g is None:
+                d.n = 0
+                continue
+            _check_rows(g, f"grads[{i}]", p.shape, None, self.device)
+            d.param, d.grad, d.n = p.data_ptr(), g.data_ptr(), p.numel()
+            d.grad_dtype = _DTYPES[g.dtype]
+        rate, rate_dev = self._scalar(self.lr if lr is None else lr, "lr")
+        scale, scale_dev = self._scalar(grad_scale, "grad_scale")
+        capturing = torch.cuda.is_current_stream_capturing()
+        if capturing and self._step_dev is None:
+            raise RuntimeError("AdamW.step under graph capture needs capturable=True")
+        opt = MoeAdamw(0.0 if rate is None else rate, self.betas[0], self.betas[1], self.eps,
+                       self.weight_decay, 1.0 if scale is None else scale, self.step_count + 1,
+                       _at(self._step_dev), rate_dev, scale_dev, self.seed & 0xFFFFFFFF)
+        with _on(self.device):
+            if self._step_dev is not None:
+                self._step_dev.add_(1)
+            _call("moe_adamw_step", _lib.lib().moe_adamw_step(
+                ctypes.byref(opt), self._list, len(self.params), _stream_of(self.device)))
+        if not capturing:
+            self.step_count += 1
+
+
+# ---------------------------------------------------------------------------
+# training the router
+class RouterTrainer:
+    """Trains a block's router on frozen experts.
+
+    ``forward`` runs the block (route or replay, permute, expert MLPs,
+    combine) and keeps what the gradient needs, ``backward`` adds the router's
+    gradient of that forward pass to ``grad``, ``step`` is one AdamW step on
+    ``w_router`` (fp32 [E, H], in place) and clears ``grad``::
+
+        trainer = RouterTrainer(w_router, w_gate_up, w_down, lr=1e-4)
+        for x, target in batches:
+            out = trainer.forward(x)
+            trainer.backward(loss_gradient(out, target))
+            trainer.step()
+
+    Experts are bf16 (w_gate_up, w_down in weight_layout), or Fp8Weights in
+    the place of w_gate_up with w_down None.  The hidden state's gradient is
+    not computed: it would need the experts' own."""
+
+    def __init__(self, w_router, w_gate_up, w_down=None, *, sel_bias=None, num_groups=8,
+                 topk_groups=4, topk=8, renormalize=True, routed_scaling=2.5,
+                 weight_layout=LAYOUT_ROW_MAJOR, lr=1e-4, betas=(0.9, 0.999), eps=1e-8,
+                 weight_decay=0.0, state_bits=32, seed=0):
+        self.w_router, self.w_gate_up, self.w_down = w_router, w_gate_up, w_down
+        self.sel_bias, self.weight_layout = sel_bias, weight_layout
+        self.num_groups, self.topk_groups, self.topk = num_groups, topk_groups, topk
+        self.renormalize, self.routed_scaling = renormalize, routed_scaling
+        self.optimizer = AdamW([w_router], lr=lr, betas=betas, eps=eps, weight_decay=weight_decay,
+                               state_bits=state_bits, seed=seed)
+        self.grad = None
+        self._saved = None
+
+    def forward(self, x, topk_ids=None):
+        """The block's output bf16 [T, H]; topk_ids replays recorded routing."""
+        if topk_ids is None:
+            ids, w, z = _lib.route(x, self.w_router, sel_bias=self.sel_bias,
+                                   num_groups=self.num_groups, topk_groups=self.topk_groups,
+                                   topk=self.topk, renormalize=self.renormalize,
+                                   return_logits=True)
+        else:
+            ids = topk_ids
+            w, z = _lib.route_replay(x, self.w_router, ids, renormalize=self.renormalize,
+                                     return_logits=True)
+        _, offsets, src, dst = _lib.permute(ids, num_experts=self.w_router.shape[0])
+        if isinstance(self.w_gate_up, Fp8Weights):
+            y = _lib.expert_ffn_fp8(x, src, offsets, self.w_gate_up, topk=ids.shape[1])
+        else:
+            y = _lib.expert_ffn(x, src, offsets, self.w_gate_up, self.w_down, topk=ids.shape[1],
+                                weight_layout=self.weight_layout)
+        self._saved = (x, ids, w, z, offsets, src, dst, y)
+        return _lib.combine(y, dst, w, routed_scaling=self.routed_scaling)
+
+    def backward(self, grad_out):
+        """Adds the router's gradient for the last forward pass to ``grad``,
+        given the gradient of its output (bf16 [T, H])."""
+        if self._saved is None:
+            raise RuntimeError("RouterTrainer.backward: no forward pass to go back through")
+        x, ids, w, z, offsets, src, dst, y = self._saved
+        _, grad_w = combine_backward(grad_out, y, dst, w, routed_scaling=self.routed_scaling,
+                                     need_grad_y=False)
+        self.grad, _ = route_backward(x, self.w_router, ids, z, grad_w, src, offsets,
+                                      renormalize=self.renormalize, need_grad_x=False,
+                                      grad_w_router=self.grad)
+        self._saved = None
+        return self.grad
+
+    def step(self, *, lr=None, grad_scale=1.0):
+        """One AdamW step on the accumulated gradient, which is then cleared."""
+        if self.grad is None:
+            raise RuntimeError("RouterTrainer.step: no gradient")
+        self.optimizer.step([self.grad], lr=lr, grad_scale=grad_scale)
+        self.grad = None

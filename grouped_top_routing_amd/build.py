@@ -29,7 +29,8 @@ def clang_rt_dir() -> str:
     if not hits:
         raise RuntimeError("clang's AddressSanitizer runtime was not found under /opt/rocm")
     return os.path.dirname(hits[-1])
-SOURCES = ["capi.hip", "route.hip", "permute.hip", "ffn.hip", "ffn_fp8.hip", "lora.hip", "combine.hip"]
+SOURCES = ["capi.hip", "route.hip", "permute.hip", "ffn.hip", "ffn_fp8.hip", "lora.hip", "combine.hip",
+           "rows.hip", "route_grad.hip", "adamw.hip", "capi_train.hip"]
 ARCH = "gfx950"
 
 

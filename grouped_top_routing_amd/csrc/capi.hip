@@ -8,48 +8,13 @@
 
 #include "../../include/beam_moe.h"
 #include "../../include/beam_moe_debug.h"
+#include "capi_common.h"
 #include "common.h"
 #include "kernels.h"
 
 namespace {
 
 using namespace beam;
-
-constexpr size_t kAlign = 256;
-
-size_t align_up(size_t v) { return (v + kAlign - 1) & ~(kAlign - 1); }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-// Weight layouts an entry point accepts (bit i = layout i).
-constexpr int kBf16Layouts = (1 << MOE_LAYOUT_ROW_MAJOR) | (1 << MOE_LAYOUT_PACKED);
-constexpr int kFp8Layouts = 1 << MOE_LAYOUT_FP8_PACKED;
-constexpr int kAnyLayout = kBf16Layouts | kFp8Layouts;
-
-int validate(const moe_config_t* c, int layouts = kBf16Layouts) {
-  if (!c) return MOE_ERR_INVALID_ARG;
-  if (c->num_tokens < 0 || c->hidden <= 0 || c->intermediate <= 0 || c->num_experts <= 0 ||
-      c->num_groups <= 0 || c->topk_groups <= 0 || c->topk <= 0)
-    return MOE_ERR_INVALID_ARG;
-  if (c->renormalize != 0 && c->renormalize != 1) return MOE_ERR_INVALID_ARG;
-  if (!std::isfinite(c->routed_scaling)) return MOE_ERR_INVALID_ARG;
-  if (c->num_experts % c->num_groups != 0) return MOE_ERR_INVALID_ARG;
-  if (c->weight_layout < 0 || c->weight_layout > 2 || !((layouts >> c->weight_layout) & 1))
-    return MOE_ERR_INVALID_ARG;
-  if (c->topk_groups > c->num_groups) return MOE_ERR_INVALID_ARG;
-  if ((int64_t)c->topk > (int64_t)c->topk_groups * (c->num_experts / c->num_groups))
-    return MOE_ERR_INVALID_ARG;
-  // shapes the gfx950 kernels are built for
-  if (c->num_experts != 256) return MOE_ERR_UNSUPPORTED;
-  if (c->num_groups > 64 || (c->num_groups & (c->num_groups - 1)) != 0) return MOE_ERR_UNSUPPORTED;
-  if (c->topk > 8) return MOE_ERR_UNSUPPORTED;
-  if (c->hidden % 256 != 0 || c->intermediate % 128 != 0) return MOE_ERR_UNSUPPORTED;
-  if (c->num_tokens * (int64_t)c->topk >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
-  return MOE_OK;
-}
-
-int64_t pairs(const moe_config_t* c) { return c->num_tokens * (int64_t)c->topk; }
 
 int mb_for(const moe_config_t* c) { return ffn_choose_mb(pairs(c), c->num_experts); }
 int mb_for_fp8(const moe_config_t* c) { return ffn_fp8_choose_mb(pairs(c), c->num_experts); }
@@ -111,30 +76,27 @@ LayerLayout layer_layout(const moe_config_t* c, bool lora = false) {
   return L;
 }
 
-int check_ws(void* ws, size_t have, size_t need) {
-  if (need == 0) return MOE_OK;
-  if (!ws || have < need) return MOE_ERR_WORKSPACE;
-  if (!aligned16(ws)) return MOE_ERR_INVALID_ARG;
-  return MOE_OK;
-}
-
-int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
-
-int device_ready() {
-  int dev = -1;
-  return hipGetDevice(&dev) == hipSuccess ? MOE_OK : MOE_ERR_HIP;
-}
-
 // ---- internal steps (arguments already validated) ----
 int do_route(const moe_config_t* c, const uint16_t* x, const float* wr, const float* bias,
-             int32_t* ids, float* w, void* scratch, hipStream_t s) {
+             int32_t* ids, float* w, void* scratch, hipStream_t s, float* logits = nullptr) {
   const int T = (int)c->num_tokens;
   float* part = static_cast<float*>(scratch);
   const int splits = router_splits(T, c->hidden);
   int st = hip_status(launch_router_logits(x, wr, part, T, c->hidden, splits, s));
   if (st) return st;
-  return hip_status(launch_select(part, splits, bias, ids, w, T, c->num_groups, c->topk_groups,
-                                  c->topk, c->renormalize, s));
+  return hip_status(launch_select(part, splits, bias, ids, w, logits, T, c->num_groups,
+                                  c->topk_groups, c->topk, c->renormalize, s));
+}
+
+int do_replay(const moe_config_t* c, const uint16_t* x, const float* wr, const int32_t* ids,
+              float* w, void* scratch, hipStream_t s, float* logits = nullptr) {
+  const int T = (int)c->num_tokens;
+  float* part = static_cast<float*>(scratch);
+  const int splits = router_splits(T, c->hidden);
+  int st = hip_status(launch_router_logits(x, wr, part, T, c->hidden, splits, s));
+  if (st) return st;
+  return hip_status(launch_replay(part, splits, ids, w, logits, T, c->num_experts, c->topk,
+                                  c->renormalize, s));
 }
 
 int do_permute(const moe_config_t* c, const int32_t* ids, int32_t* counts, int32_t* offsets,
@@ -374,6 +336,7 @@ int moe_workspace_bytes(const moe_config_t* cfg, int entry, size_t* bytes) {
     case MOE_ENTRY_EXPERT_STAGE: *bytes = plan_bytes(cfg); break;
     case MOE_ENTRY_EXPERT_FFN_LORA: *bytes = ffn_lora_ws(cfg); break;
     case MOE_ENTRY_LAYER_LORA: *bytes = layer_layout(cfg, true).total; break;
+    case MOE_ENTRY_ROUTE_BACKWARD: *bytes = route_backward_ws(cfg); break;
     default: return MOE_ERR_INVALID_ARG;
   }
   return MOE_OK;
@@ -406,14 +369,27 @@ int moe_route_replay(const moe_config_t* cfg, const uint16_t* x, const float* w_
   if ((st = check_ws(workspace, workspace_bytes, route_ws(cfg)))) return st;
   if (cfg->num_tokens == 0) return MOE_OK;
   if ((st = device_ready())) return st;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  float* part = static_cast<float*>(workspace);
-  const int T = (int)cfg->num_tokens;
-  const int splits = router_splits(T, cfg->hidden);
-  st = hip_status(launch_router_logits(x, w_router, part, T, cfg->hidden, splits, s));
+  return do_replay(cfg, x, w_router, topk_ids, topk_w, workspace,
+                   static_cast<hipStream_t>(stream));
+}
+
+int moe_route_logits(const moe_config_t* cfg, const uint16_t* x, const float* w_router,
+                     const float* sel_bias, int replay, int32_t* topk_ids, float* topk_w,
+                     float* topk_logits, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = validate(cfg, kAnyLayout);
   if (st) return st;
-  return hip_status(launch_replay(part, splits, topk_ids, topk_w, T, cfg->num_experts, cfg->topk,
-                                  cfg->renormalize, s));
+  if (!x || !w_router || !topk_ids || !topk_w || !topk_logits || (replay != 0 && replay != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w_router) || !aligned4(topk_ids) || !aligned4(topk_w) ||
+      !aligned4(topk_logits) || (sel_bias && !aligned4(sel_bias)))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_ws(workspace, workspace_bytes, route_ws(cfg)))) return st;
+  if (cfg->num_tokens == 0) return MOE_OK;
+  if ((st = device_ready())) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (replay)
+    return do_replay(cfg, x, w_router, topk_ids, topk_w, workspace, s, topk_logits);
+  return do_route(cfg, x, w_router, sel_bias, topk_ids, topk_w, workspace, s, topk_logits);
 }
 
 int moe_permute(const moe_config_t* cfg, const int32_t* topk_ids, int32_t* counts,

@@ -19,10 +19,11 @@ int router_splits(int64_t T, int H);
 hipError_t launch_router_logits(const uint16_t* x, const float* wr, float* part, int T, int H,
                                 int splits, hipStream_t stream);
 hipError_t launch_select(const float* part, int splits, const float* sel_bias, int32_t* ids,
-                         float* w, int T, int G, int topk_groups, int topk, int renormalize,
+                         float* w, float* logits, int T, int G, int topk_groups, int topk,
+                         int renormalize, hipStream_t stream);
+hipError_t launch_replay(const float* part, int splits, const int32_t* ids, float* w,
+                         float* logits, int T, int E, int topk, int renormalize,
                          hipStream_t stream);
-hipError_t launch_replay(const float* part, int splits, const int32_t* ids, float* w, int T,
-                         int E, int topk, int renormalize, hipStream_t stream);
 
 hipError_t launch_permute(const int32_t* ids, int64_t n, int E, int32_t* counts, int32_t* offsets,
                           int32_t* perm_src, int32_t* perm_dst, int32_t* chunk_hist,
@@ -96,5 +97,66 @@ uint32_t check_flags_combine();
 
 hipError_t launch_combine(const uint16_t* y, const int32_t* perm_dst, const float* w,
                           uint16_t* out, int T, int H, int topk, float scale, hipStream_t stream);
+
+// Rows between token order and expert-major order (rows.hip); fp32: the rows
+// are fp32, else bf16.  Null w: weights of one; null grad_w / grad_y: not
+// wanted (one of the two is).
+hipError_t launch_dispatch(bool fp32, const void* x, const int32_t* perm_dst, const float* w,
+                           void* out, int64_t T, int H, int topk, hipStream_t stream);
+hipError_t launch_dispatch_backward(bool fp32, const void* grad, const int32_t* perm_dst,
+                                    const float* w, const void* x, void* grad_x, float* grad_w,
+                                    int64_t T, int H, int topk, hipStream_t stream);
+hipError_t launch_combine_rows(bool fp32, const void* y, const int32_t* perm_dst, const float* w,
+                               void* out, int64_t T, int H, int topk, float scale,
+                               hipStream_t stream);
+hipError_t launch_combine_backward(bool fp32, const void* grad_out, const void* y,
+                                   const int32_t* perm_dst, const float* w, void* grad_y,
+                                   float* grad_w, int64_t T, int H, int topk, float scale,
+                                   hipStream_t stream);
+
+// Router gradient (route_grad.hip).
+constexpr int kRouteChunk = 256;  // sorted rows per partial sum of the router weights' gradient
+struct RouteGradWs {
+  size_t dz, plan, part;  // bytes
+};
+RouteGradWs route_grad_ws(int64_t T, int H, int topk);
+// whether the launch's grid holds the batch
+bool route_grad_fits(int64_t T, int H, int topk);
+hipError_t launch_route_backward(const uint16_t* x, const float* wr, const int32_t* ids,
+                                 const float* logits, const float* grad_topk_w,
+                                 const int32_t* perm_src, const int32_t* offsets,
+                                 const uint16_t* add, float* grad_w, int accumulate,
+                                 uint16_t* grad_x, int64_t T, int H, int topk, int renormalize,
+                                 float* dz, int32_t* plan, float* part, hipStream_t stream);
+
+// AdamW (adamw.hip).
+constexpr int kAdamTensors = 40;  // tensors per launch: their list is the kernel's argument
+struct AdamTensor {
+  void* param;
+  float* master;
+  const void* grad;
+  void* m;
+  void* v;
+  uint8_t* m_scale;
+  uint8_t* v_scale;
+  int64_t n;
+  int32_t kind;  // bit 0: fp32 parameter (else bf16 with a master); bit 1: fp32 gradient;
+                 // bit 2: 32-bit states
+  int32_t place; // in the caller's list
+};
+struct AdamArgs {
+  AdamTensor tensor[kAdamTensors];
+  int64_t first[kAdamTensors];  // first span (workgroup) of each tensor
+  double lr, beta1, beta2, eps, weight_decay, grad_scale;
+  int64_t step;
+  const int64_t* step_dev;
+  const float* lr_dev;
+  const float* grad_scale_dev;
+  uint32_t seed;
+  int32_t count;  // tensors of this launch
+};
+static_assert(sizeof(AdamArgs) <= 4096, "kernel arguments hold 4 KB");
+int64_t adamw_spans(int64_t n);
+hipError_t launch_adamw(const AdamArgs& a, int64_t spans, hipStream_t stream);
 
 }  // namespace beam

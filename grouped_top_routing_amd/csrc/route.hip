@@ -16,7 +16,8 @@
 //                         group top-two sums
 //                         by butterfly shuffles, group ranking, then topk
 //                         rounds of a wavefront-wide arg-max; writes ids and
-//                         combine weights.
+//                         combine weights (and, where asked, the chosen
+//                         experts' logits, which the router's gradient needs).
 #include "common.h"
 #include "kernels.h"
 
@@ -213,8 +214,8 @@ __device__ __forceinline__ void gather_logits(const float* __restrict__ part, in
 template <int G>
 __global__ __launch_bounds__(256) void select_kernel(
     const float* __restrict__ part, int splits, const float* __restrict__ sel_bias,
-    int32_t* __restrict__ ids, float* __restrict__ wout, int T, int topk_groups, int topk,
-    int renormalize) {
+    int32_t* __restrict__ ids, float* __restrict__ wout, float* __restrict__ zout, int T,
+    int topk_groups, int topk, int renormalize) {
   constexpr int LPG = kWave / G;  // lanes per group (group = 4 * LPG experts)
   const int lane = threadIdx.x & 63;
   const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -262,7 +263,7 @@ __global__ __launch_bounds__(256) void select_kernel(
   for (int i = 0; i < 4; ++i) cand[i] = keep ? sel[i] : -INFINITY;
 
   int my_id = 0;
-  float my_s = 0.f, ssum = 0.f;
+  float my_s = 0.f, my_z = 0.f, ssum = 0.f;
   for (int j = 0; j < topk; ++j) {
     float bv = cand[0];
     int bi = 4 * lane;
@@ -283,11 +284,16 @@ __global__ __launch_bounds__(256) void select_kernel(
     }
     const float sw = __shfl(pick4(s, slot), owner);
     if (lane == j) { my_id = bi; my_s = sw; }
+    if (zout) {
+      const float zw = __shfl(pick4(lg, slot), owner);
+      if (lane == j) my_z = zw;
+    }
     ssum += sw;
   }
   if (lane < topk) {
     ids[(size_t)t * topk + lane] = my_id;
     wout[(size_t)t * topk + lane] = renormalize ? my_s / ssum : my_s;
+    if (zout) zout[(size_t)t * topk + lane] = my_z;
   }
 }
 
@@ -297,23 +303,25 @@ __global__ __launch_bounds__(256) void select_kernel(
 // dropped gets weights 0).
 __global__ __launch_bounds__(256) void replay_kernel(
     const float* __restrict__ part, int splits, const int32_t* __restrict__ ids,
-    float* __restrict__ wout, int T, int E, int topk, int renormalize) {
+    float* __restrict__ wout, float* __restrict__ zout, int T, int E, int topk, int renormalize) {
   const int lane = threadIdx.x & 63;
   const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= T) return;
-  float my_s = 0.f;
+  float my_s = 0.f, my_z = 0.f;
   if (lane < topk) {
     const int e = ids[(size_t)t * topk + lane];
     if (e >= 0 && e < E) {
       float lg = 0.f;
       for (int s = 0; s < splits; ++s) lg += part[((size_t)s * T + t) * E + e];
       my_s = sigmoidf_(lg);
+      my_z = lg;
     }
   }
   float ssum = 0.f;
   for (int j = 0; j < topk; ++j) ssum += __shfl(my_s, j);
   if (lane < topk)
     wout[(size_t)t * topk + lane] = renormalize ? (ssum > 0.f ? my_s / ssum : 0.f) : my_s;
+  if (zout && lane < topk) zout[(size_t)t * topk + lane] = my_z;
 }
 
 // ---------------------------------------------------------------------------
@@ -330,13 +338,13 @@ hipError_t launch_router_logits(const uint16_t* x, const float* wr, float* part,
 }
 
 hipError_t launch_select(const float* part, int splits, const float* sel_bias, int32_t* ids,
-                         float* w, int T, int G, int topk_groups, int topk, int renormalize,
-                         hipStream_t stream) {
+                         float* w, float* logits, int T, int G, int topk_groups, int topk,
+                         int renormalize, hipStream_t stream) {
   dim3 grid((T + 3) / 4);
 #define BEAM_SELECT_CASE(GV)                                                                   \
   case GV:                                                                                     \
     hipLaunchKernelGGL(select_kernel<GV>, grid, dim3(256), 0, stream, part, splits, sel_bias,  \
-                       ids, w, T, topk_groups, topk, renormalize);                            \
+                       ids, w, logits, T, topk_groups, topk, renormalize);                    \
     break;
   switch (G) {
     BEAM_SELECT_CASE(1)
@@ -353,10 +361,11 @@ hipError_t launch_select(const float* part, int splits, const float* sel_bias, i
   return hipGetLastError();
 }
 
-hipError_t launch_replay(const float* part, int splits, const int32_t* ids, float* w, int T,
-                         int E, int topk, int renormalize, hipStream_t stream) {
+hipError_t launch_replay(const float* part, int splits, const int32_t* ids, float* w,
+                         float* logits, int T, int E, int topk, int renormalize,
+                         hipStream_t stream) {
   hipLaunchKernelGGL(replay_kernel, dim3((T + 3) / 4), dim3(256), 0, stream, part, splits, ids, w,
-                     T, E, topk, renormalize);
+                     logits, T, E, topk, renormalize);
   return hipGetLastError();
 }
 

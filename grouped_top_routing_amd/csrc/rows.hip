@@ -1,0 +1,333 @@
+// Rows moved between token order and expert-major order, and the gradients of
+// both directions (gfx950).
+//
+// Pair p = t*topk + j (slot j of token t) has row r = perm_dst[p] of the
+// sorted order; a perm_dst outside [0, T*topk) (-1 from the permutation) names
+// no row and the pair is dropped.  With a the token rows, b the sorted rows:
+//   dispatch            b[r] = w[p] * a[t]                 (w = 1 without weights)
+//   dispatch, backward  grad a[t] = sum_j w[p] * grad b[r],  grad w[p] = <a[t], grad b[r]>
+//   combine             out[t] = c * sum_j w[p] * b[r]
+//   combine, backward   grad b[r] = c * w[p] * grad out[t],  grad w[p] = c * <grad out[t], b[r]>
+// (c the routed scaling).  bf16 rows of a multiple of 256 elements are combined
+// by combine.hip; the combine here takes fp32 rows and other widths.
+//
+// All of it is bound by HBM: per token one row of the token order and topk
+// rows of the sorted order move once.  Both kernels are therefore laid out by
+// token: the token's row is read once and held in registers while its topk
+// rows are written (or read), and the indices are wave-uniform scalar loads.
+// Sums are fp32 in slot order, each result is rounded once, and there are no
+// atomics: a row of the sorted order has one writer.
+#include "common.h"
+#include "kernels.h"
+
+namespace beam {
+
+namespace {
+
+// 16 bytes at any element's alignment: gfx950 reads and writes unaligned
+// global memory in one instruction, so rows of odd length take the same path.
+__device__ __forceinline__ uint4 ld16u(const void* p) {
+  uint4 v;
+  __builtin_memcpy(&v, p, 16);
+  return v;
+}
+__device__ __forceinline__ void st16u(void* p, uint4 v) { __builtin_memcpy(p, &v, 16); }
+
+// The row types: storage S, elements per 16 bytes, conversions.
+struct Bf16Rows {
+  using S = uint16_t;
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void widen(uint4 q, float (&f)[8]) {
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      f[2 * c] = bf16_to_f32(u[c] & 0xffffu);
+      f[2 * c + 1] = __uint_as_float(u[c] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 round(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+  }
+  static __device__ __forceinline__ float get(const S* p) { return bf16_to_f32(*p); }
+  static __device__ __forceinline__ void put(S* p, float v) { *p = (S)(pack_bf16x2(v, 0.f)); }
+};
+struct F32Rows {
+  using S = float;
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void widen(uint4 q, float (&f)[4]) {
+    f[0] = __uint_as_float(q.x); f[1] = __uint_as_float(q.y);
+    f[2] = __uint_as_float(q.z); f[3] = __uint_as_float(q.w);
+  }
+  static __device__ __forceinline__ uint4 round(const float (&f)[4]) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+  }
+  static __device__ __forceinline__ float get(const S* p) { return *p; }
+  static __device__ __forceinline__ void put(S* p, float v) { *p = v; }
+};
+
+// A row's pieces: H / N of 16 bytes, then one of the H % N elements left.
+__host__ __device__ constexpr int pieces(int H, int N) { return (H + N - 1) / N; }
+
+// Rows of the token's slots, -1 where a slot names none.
+template <int K>
+__device__ __forceinline__ void slot_rows(const int32_t* __restrict__ perm_dst, int64_t t,
+                                          int topk, int64_t n, int64_t (&rows)[K]) {
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    const int64_t r = j < topk ? perm_dst[t * topk + j] : -1;
+    rows[j] = r >= 0 && r < n ? r : -1;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dispatch: thread (x, y) of a workgroup handles one piece of item
+// blockIdx.x * blockDim.y + y, an item being (token, slice of blockDim.x
+// pieces).  blockDim.x is a multiple of 64, so a wave has one token.
+template <class R, bool WEIGHTED>
+__global__ __launch_bounds__(256) void dispatch_kernel(
+    const typename R::S* __restrict__ x, const int32_t* __restrict__ perm_dst,
+    const float* __restrict__ w, typename R::S* __restrict__ out, int64_t T, int64_t n, int H,
+    int topk, int slices) {
+  constexpr int N = R::N;
+  const int64_t item = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t t = __builtin_amdgcn_readfirstlane((int)(item / slices));
+  const int v = (int)(item - t * slices) * blockDim.x + threadIdx.x;
+  if (t >= T || v * N >= H) return;
+  int64_t rows[8];
+  slot_rows(perm_dst, t, topk, n, rows);
+  const typename R::S* src = x + t * H + v * N;
+  if ((v + 1) * N <= H) {
+    const uint4 q = ld16u(src);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (rows[j] < 0) continue;
+      uint4 o = q;
+      if constexpr (WEIGHTED) {
+        const float wt = w[t * topk + j];
+        float f[N];
+        R::widen(q, f);
+#pragma unroll
+        for (int c = 0; c < N; ++c) f[c] *= wt;
+        o = R::round(f);
+      }
+      st16u(out + rows[j] * H + v * N, o);
+    }
+  } else {
+    for (int c = 0; c < H - v * N; ++c) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (rows[j] < 0) continue;
+        if constexpr (WEIGHTED)
+          R::put(out + rows[j] * H + v * N + c, w[t * topk + j] * R::get(src + c));
+        else
+          out[rows[j] * H + v * N + c] = src[c];
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// SCATTER: b[r] = (c*w) * a[t] (the combine's gradient); otherwise a[t] =
+// c * sum_j w * b[r] (the dispatch's gradient with c = 1, and the combine).
+// DOT: grad w[p] = c * <a[t], b[r]>.
+// Threads (.., y) of a workgroup share one token; for DOT blockDim.x threads
+// cover the whole row and its waves' sums meet in LDS.
+template <class R, bool SCATTER, bool DOT, bool WRITE>
+__global__ __launch_bounds__(1024) void row_grad_kernel(
+    const typename R::S* __restrict__ a, const typename R::S* __restrict__ b,
+    const int32_t* __restrict__ perm_dst, const float* __restrict__ w,
+    typename R::S* __restrict__ out, float* __restrict__ grad_w, int64_t T, int64_t n, int H,
+    int topk, float scale) {
+  constexpr int N = R::N;
+  __shared__ float part[16][8];  // 16 waves of at most 1024 threads
+  const int64_t t =
+      __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (int64_t)blockDim.y + threadIdx.y));
+  int64_t rows[8];
+  float wt[8], dot[8];
+  if (t < T) slot_rows(perm_dst, t, topk, n, rows);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (t >= T) rows[j] = -1;
+    wt[j] = w && j < topk && t < T ? (SCATTER ? scale * w[t * topk + j] : w[t * topk + j]) : 1.f;
+    dot[j] = 0.f;
+  }
+  const int nv = t < T ? pieces(H, N) : 0;
+  for (int v = threadIdx.x; v < nv; v += blockDim.x) {
+    const int64_t at = t * H + v * N;
+    if ((v + 1) * N <= H) {
+      uint4 qb[8];
+      if constexpr (DOT || !SCATTER) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          qb[j] = rows[j] >= 0 ? ld16u(b + rows[j] * H + v * N) : make_uint4(0u, 0u, 0u, 0u);
+      }
+      float fa[N];
+      if constexpr (DOT || SCATTER) R::widen(ld16u(a + at), fa);
+      float acc[N];
+#pragma unroll
+      for (int c = 0; c < N; ++c) acc[c] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (rows[j] < 0) continue;
+        if constexpr (DOT || !SCATTER) {
+          float fb[N];
+          R::widen(qb[j], fb);
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            if constexpr (DOT) dot[j] += fa[c] * fb[c];
+            if constexpr (!SCATTER) acc[c] += wt[j] * fb[c];
+          }
+        }
+        if constexpr (SCATTER && WRITE) {
+          float o[N];
+#pragma unroll
+          for (int c = 0; c < N; ++c) o[c] = wt[j] * fa[c];
+          st16u(out + rows[j] * H + v * N, R::round(o));
+        }
+      }
+      if constexpr (!SCATTER) {
+#pragma unroll
+        for (int c = 0; c < N; ++c) acc[c] *= scale;
+        st16u(out + at, R::round(acc));
+      }
+    } else {
+      for (int c = 0; c < H - v * N; ++c) {
+        float acc = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (rows[j] < 0) continue;
+          const int64_t bt = rows[j] * H + v * N + c;
+          if constexpr (DOT) dot[j] += R::get(a + at + c) * R::get(b + bt);
+          if constexpr (!SCATTER) acc += wt[j] * R::get(b + bt);
+          if constexpr (SCATTER && WRITE) R::put(out + bt, wt[j] * R::get(a + at + c));
+        }
+        if constexpr (!SCATTER) R::put(out + at + c, scale * acc);
+      }
+    }
+  }
+  if constexpr (DOT) {
+    const int waves = blockDim.x / kWave;  // of one token
+    const int wave = (threadIdx.y * blockDim.x + threadIdx.x) / kWave;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int off = 32; off >= 1; off >>= 1) dot[j] += __shfl_xor(dot[j], off);
+    if (threadIdx.x % kWave == 0)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) part[wave][j] = dot[j];
+    __syncthreads();
+    if (t < T && (int)threadIdx.x < topk) {
+      float s = 0.f;
+      for (int i = 0; i < waves; ++i) s += part[threadIdx.y * waves + i][threadIdx.x];
+      grad_w[t * topk + threadIdx.x] = scale * s;
+    }
+  }
+}
+
+// A grid holds fewer than 2^32 threads: batches past half of that go in
+// several launches over ranges of tokens.
+constexpr int64_t kLaunchThreads = (int64_t)1 << 31;
+
+template <class R>
+hipError_t dispatch(const void* x, const int32_t* perm_dst, const float* w, void* out, int64_t T,
+                    int H, int topk, hipStream_t stream) {
+  using S = typename R::S;
+  const int nv = pieces(H, R::N);
+  // threads per item: of 256, 128 and 64, the one with the fewest idle lanes
+  int tx = 64;
+  for (int c = 128; c <= 256; c *= 2)
+    if ((nv + c - 1) / c * c <= (nv + tx - 1) / tx * tx) tx = c;
+  const int slices = (nv + tx - 1) / tx, ty = 256 / tx;
+  const int64_t n = T * topk;
+  int64_t most = kLaunchThreads / ((int64_t)slices * tx);
+  if (most < 1) most = 1;
+  for (int64_t t0 = 0; t0 < T; t0 += most) {
+    const int64_t nt = T - t0 < most ? T - t0 : most;
+    const dim3 grid((unsigned)((nt * slices + ty - 1) / ty)), block(tx, ty);
+    const S* xs = static_cast<const S*>(x) + t0 * H;
+    S* o = static_cast<S*>(out);
+    if (w)
+      hipLaunchKernelGGL((dispatch_kernel<R, true>), grid, block, 0, stream, xs,
+                         perm_dst + t0 * topk, w + t0 * topk, o, nt, n, H, topk, slices);
+    else
+      hipLaunchKernelGGL((dispatch_kernel<R, false>), grid, block, 0, stream, xs,
+                         perm_dst + t0 * topk, w, o, nt, n, H, topk, slices);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <class R, bool SCATTER, bool DOT, bool WRITE>
+hipError_t row_grad(const void* a, const void* b, const int32_t* perm_dst, const float* w,
+                    void* out, float* grad_w, int64_t T, int H, int topk, float scale,
+                    hipStream_t stream) {
+  using S = typename R::S;
+  const int waves = (pieces(H, R::N) + kWave - 1) / kWave;
+  // one round of at most 1024 threads over the row, or equal rounds
+  const int rounds = (waves + 15) / 16;
+  const int tx = kWave * ((waves + rounds - 1) / rounds);
+  const int ty = tx >= 256 ? 1 : 256 / tx;
+  const int64_t n = T * topk, most = kLaunchThreads / tx;
+  for (int64_t t0 = 0; t0 < T; t0 += most) {
+    const int64_t nt = T - t0 < most ? T - t0 : most;
+    const S* as = static_cast<const S*>(a);
+    S* o = static_cast<S*>(out);
+    hipLaunchKernelGGL((row_grad_kernel<R, SCATTER, DOT, WRITE>),
+                       dim3((unsigned)((nt + ty - 1) / ty)), dim3(tx, ty), 0, stream,
+                       as ? as + t0 * H : nullptr, static_cast<const S*>(b),
+                       perm_dst + t0 * topk, w ? w + t0 * topk : nullptr,
+                       SCATTER ? o : o + t0 * H, grad_w ? grad_w + t0 * topk : nullptr, nt, n, H,
+                       topk, scale);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_dispatch(bool fp32, const void* x, const int32_t* perm_dst, const float* w,
+                           void* out, int64_t T, int H, int topk, hipStream_t stream) {
+  return fp32 ? dispatch<F32Rows>(x, perm_dst, w, out, T, H, topk, stream)
+              : dispatch<Bf16Rows>(x, perm_dst, w, out, T, H, topk, stream);
+}
+
+hipError_t launch_dispatch_backward(bool fp32, const void* grad, const int32_t* perm_dst,
+                                    const float* w, const void* x, void* grad_x, float* grad_w,
+                                    int64_t T, int H, int topk, hipStream_t stream) {
+#define BEAM_GRAD(R, DOT)                                                                     \
+  row_grad<R, false, DOT, true>(x, grad, perm_dst, w, grad_x, grad_w, T, H, topk, 1.f, stream)
+  if (fp32) return grad_w ? BEAM_GRAD(F32Rows, true) : BEAM_GRAD(F32Rows, false);
+  return grad_w ? BEAM_GRAD(Bf16Rows, true) : BEAM_GRAD(Bf16Rows, false);
+#undef BEAM_GRAD
+}
+
+hipError_t launch_combine_rows(bool fp32, const void* y, const int32_t* perm_dst, const float* w,
+                               void* out, int64_t T, int H, int topk, float scale,
+                               hipStream_t stream) {
+  return fp32 ? row_grad<F32Rows, false, false, true>(nullptr, y, perm_dst, w, out, nullptr, T, H,
+                                                      topk, scale, stream)
+              : row_grad<Bf16Rows, false, false, true>(nullptr, y, perm_dst, w, out, nullptr, T,
+                                                       H, topk, scale, stream);
+}
+
+hipError_t launch_combine_backward(bool fp32, const void* grad_out, const void* y,
+                                   const int32_t* perm_dst, const float* w, void* grad_y,
+                                   float* grad_w, int64_t T, int H, int topk, float scale,
+                                   hipStream_t stream) {
+#define BEAM_GRAD(R, DOT, WRITE)                                                             \
+  row_grad<R, true, DOT, WRITE>(grad_out, y, perm_dst, w, grad_y, grad_w, T, H, topk, scale, \
+                                stream)
+  if (fp32) {
+    if (!grad_y) return BEAM_GRAD(F32Rows, true, false);
+    return grad_w ? BEAM_GRAD(F32Rows, true, true) : BEAM_GRAD(F32Rows, false, true);
+  }
+  if (!grad_y) return BEAM_GRAD(Bf16Rows, true, false);
+  return grad_w ? BEAM_GRAD(Bf16Rows, true, true) : BEAM_GRAD(Bf16Rows, false, true);
+#undef BEAM_GRAD
+}
+
+}  // namespace beam

@@ -69,7 +69,8 @@ enum moe_entry {
   MOE_ENTRY_LAYER = 3,
   MOE_ENTRY_EXPERT_STAGE = 4,  /* moe_expert_gate_up or moe_expert_down */
   MOE_ENTRY_EXPERT_FFN_LORA = 5,
-  MOE_ENTRY_LAYER_LORA = 6
+  MOE_ENTRY_LAYER_LORA = 6,
+  MOE_ENTRY_ROUTE_BACKWARD = 8  /* 7 names no entry */
 };
 
 typedef struct moe_config {
@@ -321,6 +322,160 @@ int moe_layer_forward_lora(const moe_config_t* cfg, const uint16_t* x, const flo
                            const uint16_t* w_down, const moe_lora_t* lora, uint16_t* out,
                            int32_t* topk_ids_out, float* topk_w_out,
                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Training: the gradients of the block around its experts, and the optimizer.
+ *
+ * The chain of one router training step on frozen experts is
+ *   moe_route_logits, moe_permute, moe_expert_ffn (or _fp8, _lora), moe_combine,
+ *   <loss>, moe_combine_backward, moe_route_backward, moe_adamw_step;
+ * experts of the caller's own go between moe_dispatch and moe_combine, and
+ * their gradients between moe_combine_backward and moe_dispatch_backward.
+ *
+ * moe_dispatch, moe_dispatch_backward, moe_combine_rows and
+ * moe_combine_backward move rows of `dtype` (moe_dtype) and read num_tokens, hidden, topk (and routed_scaling)
+ * of cfg only: any hidden >= 1, 1 <= topk <= 8, num_tokens * topk < 2^31.
+ * Rows are dense; row pointers must be 16-byte aligned, though rows of odd
+ * length within a tensor need not be.  perm_dst is moe_permute's (or any
+ * injective map of pairs to rows); an entry outside [0, num_tokens * topk)
+ * drops its pair.  Sorted rows that no pair names are neither read nor written.
+ * Inputs and outputs must not overlap.
+ */
+enum moe_dtype { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP32 = 1 };
+
+/*
+ * moe_route (replay == 0) or moe_route_replay (replay == 1, topk_ids an input,
+ * sel_bias unused) with one more output:
+ *   topk_logits  [T, topk] fp32 out: the router logit of each chosen expert
+ *                (0 for a replayed id that names no expert)
+ * The other outputs are those calls' bit for bit; workspace MOE_ENTRY_ROUTE.
+ */
+int moe_route_logits(const moe_config_t* cfg, const uint16_t* x, const float* w_router,
+                     const float* sel_bias, int replay, int32_t* topk_ids, float* topk_w,
+                     float* topk_logits, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Tokens sorted by expert: x_perm[perm_dst[p]] = topk_w[p] * x[t] for every
+ * pair p = t*topk + j, in fp32 rounded once (topk_w NULL: a copy).
+ *   x       [T, H] rows;  x_perm  [T*topk, H] rows out
+ *   topk_w  [T, topk] fp32 or NULL
+ */
+int moe_dispatch(const moe_config_t* cfg, int dtype, const void* x, const int32_t* perm_dst,
+                 const float* topk_w, void* x_perm, void* stream);
+
+/*
+ * Gradient of moe_dispatch, sums in fp32 in slot order:
+ *   grad_x[t]       = sum_j topk_w[p] * grad_x_perm[perm_dst[p]]   [T, H] rows out
+ *   grad_topk_w[p]  = <x[t], grad_x_perm[perm_dst[p]]>             [T, topk] fp32 out
+ * (0 for a dropped pair).  topk_w NULL: weights of one.  x and grad_topk_w are
+ * both given or both NULL, and only with topk_w.
+ */
+int moe_dispatch_backward(const moe_config_t* cfg, int dtype, const void* grad_x_perm,
+                          const int32_t* perm_dst, const float* topk_w, const void* x,
+                          void* grad_x, float* grad_topk_w, void* stream);
+
+/*
+ * moe_combine for rows of either type and any width (moe_combine takes bf16
+ * rows of a multiple of 256 elements).
+ *   y_perm [T*topk, H] rows, topk_w [T, topk] fp32, out [T, H] rows out
+ */
+int moe_combine_rows(const moe_config_t* cfg, int dtype, const void* y_perm,
+                     const int32_t* perm_dst, const float* topk_w, void* out, void* stream);
+
+/*
+ * Gradient of moe_combine and moe_combine_rows (out[t] = routed_scaling * sum_j topk_w[p] *
+ * y_perm[perm_dst[p]]):
+ *   grad_y_perm[perm_dst[p]] = routed_scaling * topk_w[p] * grad_out[t]
+ *                                                     [T*topk, H] rows out, or NULL
+ *   grad_topk_w[p] = routed_scaling * <grad_out[t], y_perm[perm_dst[p]]>
+ *                                                     [T, topk] fp32 out, or NULL
+ * (0 for a dropped pair).  At least one output is wanted; y_perm is read for
+ * grad_topk_w, topk_w for grad_y_perm, and either may be NULL without it.
+ */
+int moe_combine_backward(const moe_config_t* cfg, int dtype, const void* grad_out,
+                         const void* y_perm, const int32_t* perm_dst, const float* topk_w,
+                         void* grad_y_perm, float* grad_topk_w, void* stream);
+
+/*
+ * Gradient of moe_route / moe_route_replay from that of the combine weights
+ * (cfg as in the forward call: shapes and renormalize).  With s = sigmoid of
+ * the chosen logits and g = grad_topk_w,
+ *   renormalize:  w_j = s_j / sum_i s_i,  dz_j = w_j (1 - s_j) (g_j - sum_i g_i w_i)
+ *   otherwise:    dz_j = s_j (1 - s_j) g_j
+ *   grad_w_router[e] = sum over the pairs of e of dz[p] * x[t]     [E, H] fp32 out
+ *   grad_x[t] = grad_x_add[t] + sum_j dz[p] * w_router[e_j]        [T, H] bf16 out
+ * Ids outside [0, E) have no part in it.  The selection (and sel_bias) has no
+ * gradient.
+ *   topk_ids, topk_logits    [T, topk], of moe_route_logits
+ *   grad_topk_w              [T, topk] fp32
+ *   perm_src, offsets        of moe_permute on the same topk_ids
+ *   accumulate               1: grad_w_router is added to, 0: overwritten
+ *   grad_x_add               [T, H] bf16 or NULL: the hidden state's gradient from
+ *                            elsewhere (the experts); may be grad_x itself
+ *   grad_x                   NULL: not wanted (then grad_x_add is NULL too)
+ * Sums are fp32 in a fixed order.  With no tokens nothing is written,
+ * grad_w_router included.  Workspace MOE_ENTRY_ROUTE_BACKWARD; batches whose
+ * grids exceed 2^32 threads (num_tokens * hidden around 2^37) return
+ * MOE_ERR_UNSUPPORTED.
+ */
+int moe_route_backward(const moe_config_t* cfg, const uint16_t* x, const float* w_router,
+                       const int32_t* topk_ids, const float* topk_logits,
+                       const float* grad_topk_w, const int32_t* perm_src, const int32_t* offsets,
+                       const uint16_t* grad_x_add, int accumulate, float* grad_w_router,
+                       uint16_t* grad_x, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One AdamW step (decoupled weight decay) over a list of tensors.  With
+ * g = grad_scale * grad and t the step:
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = p - lr weight_decay p - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32, p being the parameter, or the fp32 master of a bf16 one (which is
+ * then rounded to nearest into the parameter).
+ *
+ * 32-bit states: m and v [n] fp32.  8-bit states: m and sqrt(v) as E4M3FN codes
+ * [n], with one E8M0 scale (2^(code - 127)) per block of 32 consecutive
+ * elements [ceil(n / 32)]; the scale is the least power of two, at least
+ * 2^-126, by which the block's largest finite magnitude is at most 448.  Codes
+ * are rounded stochastically, by a hash of (seed, step, place in the list,
+ * element): 16 random bits against the remainder, so that the state's mean
+ * follows changes far below a code step.  A sqrt(v) above zero keeps at least
+ * the smallest code.  The update itself uses m and v before rounding.
+ *
+ * A gradient that is not finite reaches its own element alone (in 8 bits as
+ * NaN).  All tensor pointers are 16-byte aligned except the scales; n may be
+ * any number, 0 included.  State memory of zeros is a valid start.
+ */
+typedef struct moe_adamw_tensor {
+  void* param;         /* [n] fp32, or bf16 with `master`                      */
+  float* master;       /* [n] fp32 for a bf16 param, NULL for an fp32 one      */
+  const void* grad;    /* [n] of grad_dtype                                    */
+  void* m;             /* [n] fp32 or E4M3FN codes                             */
+  void* v;             /* [n] fp32, or E4M3FN codes of sqrt(v)                 */
+  uint8_t* m_scale;    /* [ceil(n/32)] E8M0, NULL with 32-bit states           */
+  uint8_t* v_scale;
+  int64_t n;           /* below 2^34                                           */
+  int32_t param_dtype; /* moe_dtype                                            */
+  int32_t grad_dtype;  /* moe_dtype                                            */
+  int32_t state_bits;  /* 32 or 8                                              */
+} moe_adamw_tensor_t;
+
+typedef struct moe_adamw {
+  double lr, beta1, beta2, eps, weight_decay; /* betas in [0, 1), the others >= 0 */
+  double grad_scale;           /* factor on every gradient (clipping, loss scaling) */
+  int64_t step;                /* t >= 1 of this step                          */
+  /* Device scalars for steps replayed from a captured graph, each NULL or read
+   * when the step runs: the step number in place of `step` (>= 1), the rate in
+   * place of `lr`, and a further factor on the gradients. */
+  const int64_t* step_dev;
+  const float* lr_dev;
+  const float* grad_scale_dev;
+  uint32_t seed;               /* of the 8-bit states' rounding                */
+} moe_adamw_t;
+
+/* `tensors`: host array, read during the call.  Tensors must not overlap. */
+int moe_adamw_step(const moe_adamw_t* opt, const moe_adamw_tensor_t* tensors, int num_tensors,
+                   void* stream);
 
 /* Static description of a status code; never NULL. */
 const char* moe_status_string(int status);
