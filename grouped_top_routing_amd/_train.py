@@ -9,22 +9,49 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import torch
 
 from . import _lib
 from ._lib import (DTYPE_BF16, DTYPE_FP32, ENTRY_ROUTE_BACKWARD, LAYOUT_ROW_MAJOR, Fp8Weights,
-                   MoeAdamw, MoeAdamwTensor, _call, _check, _ws, make_config, workspace_bytes)
+                   MoeAdamw, MoeAdamwTensor, _call, _check, make_config, workspace_bytes)
 
 _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
+
+# A call of these on a small batch takes the GPU less time than the host needs
+# for it, so the checks that pass cost as little as they can: one expression
+# per tensor, whose failure hands the tensor to _check for the error.
 
 
 def _at(t):
     return None if t is None else t.data_ptr()
 
 
+def _need(t, name, dtype, shape, device):
+    """t is a dense tensor of this type and shape on `device`."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.is_cuda and t.device == device and t.is_contiguous()):
+        _check(t, name, dtype, shape, device)
+
+
+def _need_rows(t, name, rows=None):
+    """(width, type, device) of a dense [rows, H] tensor, bf16 or fp32."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous():
+        _check(t, name, t.dtype)
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows):
+        want = "T" if rows is None else rows
+        raise ValueError(f"{name} must have shape ({want}, H), got {tuple(shape)}")
+    return shape[1], t.dtype, t.device
+
+
 def _stream_of(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 _NOTHING = contextlib.nullcontext()
@@ -38,20 +65,12 @@ def _on(device):
 
 
 def _scratch(nbytes, device, workspace):
-    """The call's workspace.  Under graph capture a buffer of the graph's own
-    pool, so that no other graph or eager call shares it."""
-    if workspace is None and torch.cuda.is_current_stream_capturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return _ws(workspace, device).get(nbytes, device)
-
-
-def _check_rows(t, name, shape, dtype=None, device=None):
-    """Row tensors are bf16 or fp32, one type in a call."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _DTYPES:
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
-    _check(t, name, dtype or t.dtype, shape, device)
+    """The call's workspace: the caller's, or memory of torch's allocator that
+    is given back when the call returns (its next use follows on the stream;
+    under capture it is of the graph's own pool)."""
+    if workspace is not None:
+        return workspace.get(nbytes, device)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def _tokens_of(perm_dst, topk):
@@ -63,8 +82,18 @@ def _tokens_of(perm_dst, topk):
     return perm_dst.numel() // topk
 
 
+# Configurations are values: one object per distinct set of numbers.
+@functools.lru_cache(maxsize=256)
 def _rows_config(T, H, topk, scale=1.0):
-    return make_config(T, H, 128, num_groups=1, topk_groups=1, topk=topk, routed_scaling=scale)
+    return ctypes.byref(make_config(T, H, 128, num_groups=1, topk_groups=1, topk=topk,
+                                    routed_scaling=scale))
+
+
+@functools.lru_cache(maxsize=256)
+def _route_config(T, H, E, topk, renormalize):
+    cfg = make_config(T, H, 128, num_experts=E, num_groups=1, topk_groups=1, topk=topk,
+                      renormalize=renormalize)
+    return ctypes.byref(cfg), workspace_bytes(cfg, ENTRY_ROUTE_BACKWARD)
 
 
 def dispatch(x, perm_dst, *, topk=8, topk_w=None, out=None):
@@ -76,22 +105,19 @@ def dispatch(x, perm_dst, *, topk=8, topk_w=None, out=None):
     ones of moe_permute's order) are left as ``out`` holds them; without
     ``out`` they are not initialised."""
     T = _tokens_of(perm_dst, topk)
-    _check_rows(x, "x", None)
-    H = x.shape[-1]
-    _check(x, "x", x.dtype, (T, H))
-    _check(perm_dst, "perm_dst", torch.int32, (T * topk,), x.device)
+    H, dt, dev = _need_rows(x, "x", T)
+    _need(perm_dst, "perm_dst", torch.int32, (T * topk,), dev)
     if topk_w is not None:
-        _check(topk_w, "topk_w", torch.float32, (T, topk), x.device)
+        _need(topk_w, "topk_w", torch.float32, (T, topk), dev)
     if out is None:
-        out = torch.empty(T * topk, H, dtype=x.dtype, device=x.device)
+        out = torch.empty(T * topk, H, dtype=dt, device=dev)
     else:
-        _check(out, "out", x.dtype, (T * topk, H), x.device)
+        _need(out, "out", dt, (T * topk, H), dev)
     if T:
-        cfg = _rows_config(T, H, topk)
-        with _on(x.device):
+        with _on(dev):
             _call("moe_dispatch", _lib.lib().moe_dispatch(
-                ctypes.byref(cfg), _DTYPES[x.dtype], _at(x), _at(perm_dst), _at(topk_w), _at(out),
-                _stream_of(x.device)))
+                _rows_config(T, H, topk), _DTYPES[dt], x.data_ptr(), perm_dst.data_ptr(),
+                _at(topk_w), out.data_ptr(), _stream_of(dev)))
     return out
 
 
@@ -100,24 +126,22 @@ def dispatch_backward(grad_x_perm, perm_dst, *, topk=8, x=None, topk_w=None):
     rows of grad_x_perm [T*k, H].  With x and topk_w given, (grad_x,
     grad_topk_w fp32 [T, k]); with topk_w alone, grad_x."""
     T = _tokens_of(perm_dst, topk)
-    _check_rows(grad_x_perm, "grad_x_perm", None)
-    H, dt, dev = grad_x_perm.shape[-1], grad_x_perm.dtype, grad_x_perm.device
-    _check(grad_x_perm, "grad_x_perm", dt, (T * topk, H))
-    _check(perm_dst, "perm_dst", torch.int32, (T * topk,), dev)
+    H, dt, dev = _need_rows(grad_x_perm, "grad_x_perm", T * topk)
+    _need(perm_dst, "perm_dst", torch.int32, (T * topk,), dev)
     if topk_w is not None:
-        _check(topk_w, "topk_w", torch.float32, (T, topk), dev)
+        _need(topk_w, "topk_w", torch.float32, (T, topk), dev)
     if x is not None:
         if topk_w is None:
             raise ValueError("x is for the gradient of topk_w: pass topk_w too")
-        _check(x, "x", dt, (T, H), dev)
+        _need(x, "x", dt, (T, H), dev)
     grad_x = torch.empty(T, H, dtype=dt, device=dev)
     grad_w = None if x is None else torch.empty(T, topk, dtype=torch.float32, device=dev)
     if T:
-        cfg = _rows_config(T, H, topk)
         with _on(dev):
             _call("moe_dispatch_backward", _lib.lib().moe_dispatch_backward(
-                ctypes.byref(cfg), _DTYPES[dt], _at(grad_x_perm), _at(perm_dst), _at(topk_w),
-                _at(x), _at(grad_x), _at(grad_w), _stream_of(dev)))
+                _rows_config(T, H, topk), _DTYPES[dt], grad_x_perm.data_ptr(),
+                perm_dst.data_ptr(), _at(topk_w), _at(x), grad_x.data_ptr(), _at(grad_w),
+                _stream_of(dev)))
     return grad_x if x is None else (grad_x, grad_w)
 
 
@@ -132,13 +156,11 @@ def combine_backward(grad_out, y_perm, perm_dst, topk_w, *, routed_scaling=2.5, 
     if not isinstance(topk_w, torch.Tensor) or topk_w.dim() != 2:
         raise TypeError("topk_w must be a torch.Tensor [T, k]")
     T, k = topk_w.shape
-    _check_rows(grad_out, "grad_out", None)
-    H, dt, dev = grad_out.shape[-1], grad_out.dtype, grad_out.device
-    _check(grad_out, "grad_out", dt, (T, H))
-    _check(perm_dst, "perm_dst", torch.int32, (T * k,), dev)
-    _check(topk_w, "topk_w", torch.float32, (T, k), dev)
+    H, dt, dev = _need_rows(grad_out, "grad_out", T)
+    _need(perm_dst, "perm_dst", torch.int32, (T * k,), dev)
+    _need(topk_w, "topk_w", torch.float32, (T, k), dev)
     if y_perm is not None:
-        _check(y_perm, "y_perm", dt, (T * k, H), dev)
+        _need(y_perm, "y_perm", dt, (T * k, H), dev)
     elif need_grad_w:
         raise ValueError("the gradient of topk_w needs y_perm")
     grad_y = grad_w = None
@@ -146,16 +168,16 @@ def combine_backward(grad_out, y_perm, perm_dst, topk_w, *, routed_scaling=2.5, 
         if out is None:
             grad_y = torch.empty(T * k, H, dtype=dt, device=dev)
         else:
-            _check(out, "out", dt, (T * k, H), dev)
+            _need(out, "out", dt, (T * k, H), dev)
             grad_y = out
     if need_grad_w:
         grad_w = torch.empty(T, k, dtype=torch.float32, device=dev)
     if T:
-        cfg = _rows_config(T, H, k, routed_scaling)
         with _on(dev):
             _call("moe_combine_backward", _lib.lib().moe_combine_backward(
-                ctypes.byref(cfg), _DTYPES[dt], _at(grad_out), _at(y_perm), _at(perm_dst),
-                _at(topk_w), _at(grad_y), _at(grad_w), _stream_of(dev)))
+                _rows_config(T, H, k, float(routed_scaling)), _DTYPES[dt], grad_out.data_ptr(),
+                _at(y_perm), perm_dst.data_ptr(), topk_w.data_ptr(), _at(grad_y), _at(grad_w),
+                _stream_of(dev)))
     return grad_y, grad_w
 
 
@@ -170,42 +192,41 @@ def route_backward(x, w_router, topk_ids, topk_logits, grad_topk_w, perm_src, of
     hidden state's gradient through the experts) is added into grad_x before
     its one rounding.  A ``grad_w_router`` passed in is added to (gradients of
     several micro-batches) and returned."""
-    _check(x, "x", torch.bfloat16)
-    if x.dim() != 2:
-        raise ValueError(f"x must have shape (T, H), got {tuple(x.shape)}")
-    T, H = x.shape
-    dev = x.device
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise TypeError("x must be a torch.Tensor [T, H]")
     if not isinstance(topk_ids, torch.Tensor) or topk_ids.dim() != 2:
         raise TypeError("topk_ids must be a torch.Tensor [T, k]")
-    k = topk_ids.shape[1]
-    E = w_router.shape[0]
-    _check(w_router, "w_router", torch.float32, (E, H), dev)
-    _check(topk_ids, "topk_ids", torch.int32, (T, k), dev)
-    _check(topk_logits, "topk_logits", torch.float32, (T, k), dev)
-    _check(grad_topk_w, "grad_topk_w", torch.float32, (T, k), dev)
-    _check(perm_src, "perm_src", torch.int32, (T * k,), dev)
-    _check(offsets, "offsets", torch.int32, (E + 1,), dev)
+    if not isinstance(w_router, torch.Tensor) or w_router.dim() != 2:
+        raise TypeError("w_router must be a torch.Tensor [E, H]")
+    (T, H), k, E, dev = x.shape, topk_ids.shape[1], w_router.shape[0], x.device
+    f32, i32, pairs = torch.float32, torch.int32, (T, k)
+    _need(x, "x", torch.bfloat16, (T, H), dev)
+    _need(w_router, "w_router", f32, (E, H), dev)
+    _need(topk_ids, "topk_ids", i32, pairs, dev)
+    _need(topk_logits, "topk_logits", f32, pairs, dev)
+    _need(grad_topk_w, "grad_topk_w", f32, pairs, dev)
+    _need(perm_src, "perm_src", i32, (T * k,), dev)
+    _need(offsets, "offsets", i32, (E + 1,), dev)
     if grad_x_add is not None:
         if not need_grad_x:
             raise ValueError("grad_x_add without need_grad_x")
-        _check(grad_x_add, "grad_x_add", torch.bfloat16, (T, H), dev)
+        _need(grad_x_add, "grad_x_add", torch.bfloat16, (T, H), dev)
     accumulate = grad_w_router is not None
     if accumulate:
-        _check(grad_w_router, "grad_w_router", torch.float32, (E, H), dev)
-    cfg = make_config(T, H, 128, num_experts=E, num_groups=1, topk_groups=1, topk=k,
-                      renormalize=renormalize)
-    nb = workspace_bytes(cfg, ENTRY_ROUTE_BACKWARD)
+        _need(grad_w_router, "grad_w_router", f32, (E, H), dev)
+    cfg, nb = _route_config(T, H, E, k, bool(renormalize))
     grad_x = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if need_grad_x else None
     if T == 0:
         return (grad_w_router if accumulate else torch.zeros_like(w_router)), grad_x
     if not accumulate:
-        grad_w_router = torch.empty(E, H, dtype=torch.float32, device=dev)
+        grad_w_router = torch.empty(E, H, dtype=f32, device=dev)
     with _on(dev):
         ws = _scratch(nb, dev, workspace)
         _call("moe_route_backward", _lib.lib().moe_route_backward(
-            ctypes.byref(cfg), _at(x), _at(w_router), _at(topk_ids), _at(topk_logits),
-            _at(grad_topk_w), _at(perm_src), _at(offsets), _at(grad_x_add), int(accumulate),
-            _at(grad_w_router), _at(grad_x), _at(ws), nb, _stream_of(dev)))
+            cfg, x.data_ptr(), w_router.data_ptr(), topk_ids.data_ptr(), topk_logits.data_ptr(),
+            grad_topk_w.data_ptr(), perm_src.data_ptr(), offsets.data_ptr(), _at(grad_x_add),
+            accumulate, grad_w_router.data_ptr(), _at(grad_x), ws.data_ptr(), nb,
+            _stream_of(dev)))
     return grad_w_router, grad_x
 
 
@@ -240,10 +261,12 @@ class AdamW:
         if step_count < 0:
             raise ValueError("step_count must not be negative")
         for i, p in enumerate(self.params):
-            _check_rows(p, f"params[{i}]", None, None, getattr(self.params[0], "device", None))
+            if not isinstance(p, torch.Tensor) or p.dtype not in _DTYPES:
+                raise TypeError(f"params[{i}] must be torch.bfloat16 or torch.float32, got "
+                                f"{getattr(p, 'dtype', type(p))}")
+            _check(p, f"params[{i}]", p.dtype, None, self.params[0].device)
         self.device = self.params[0].device
-        self.lr, self.betas, self.eps = lr, tuple(betas), eps
-        self.weight_decay, self.state_bits, self.seed = weight_decay, state_bits, seed
+        self.lr, self.state_bits = lr, state_bits
         self.step_count = step_count
         self._step_dev = None
         if capturable:
@@ -256,6 +279,8 @@ class AdamW:
             if state_bits == 8:
                 d.m_scale, d.v_scale = _at(s["exp_avg_scale"]), _at(s["exp_avg_sq_scale"])
             d.param_dtype, d.state_bits = _DTYPES[p.dtype], state_bits
+        self._opt = MoeAdamw(beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay,
+                             step_dev=_at(self._step_dev), seed=seed & 0xFFFFFFFF)
 
     def _kinds(self):
         """The state's lists and their element types."""
@@ -296,14 +321,12 @@ class AdamW:
                     raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
         return {k: tuple(v) for k, v in state.items()}
 
-    def _scalar(self, v, name):
-        """(host value, device pointer) of a number or a one-element fp32 tensor."""
-        if isinstance(v, torch.Tensor):
-            _check(v, name, torch.float32, None, self.device)
-            if v.numel() != 1:
-                raise ValueError(f"{name} must have one element, got {v.numel()}")
-            return None, v.data_ptr()
-        return float(v), None
+    def _pointer(self, t, name):
+        """Device address of a one-element fp32 tensor."""
+        _check(t, name, torch.float32, None, self.device)
+        if t.numel() != 1:
+            raise ValueError(f"{name} must have one element, got {t.numel()}")
+        return t.data_ptr()
 
     def step(self, grads, *, lr=None, grad_scale=1.0):
         """One step.  grads: one tensor (bf16 or fp32, the parameter's shape)
@@ -312,26 +335,39 @@ class AdamW:
         gradient, are numbers or one-element fp32 device tensors."""
         if len(grads) != len(self.params):
             raise ValueError(f"{len(self.params)} gradients expected, got {len(grads)}")
+        dev, opt = self.device, self._opt
         for i, (p, g, d) in enumerate(zip(self.params, grads, self._list)):
             if g is None:
                 d.n = 0
                 continue
-            _check_rows(g, f"grads[{i}]", p.shape, None, self.device)
-            d.param, d.grad, d.n = p.data_ptr(), g.data_ptr(), p.numel()
-            d.grad_dtype = _DTYPES[g.dtype]
-        rate, rate_dev = self._scalar(self.lr if lr is None else lr, "lr")
-        scale, scale_dev = self._scalar(grad_scale, "grad_scale")
+            kind = _DTYPES.get(getattr(g, "dtype", None))
+            if kind is None:
+                raise TypeError(f"grads[{i}] must be torch.bfloat16 or torch.float32, got "
+                                f"{getattr(g, 'dtype', type(g))}")
+            _need(g, f"grads[{i}]", g.dtype, p.shape, dev)
+            d.param, d.grad, d.grad_dtype, d.n = p.data_ptr(), g.data_ptr(), kind, p.numel()
+        if lr is None:
+            lr = self.lr
+        if isinstance(lr, torch.Tensor):
+            opt.lr, opt.lr_dev = 0.0, self._pointer(lr, "lr")
+        else:
+            opt.lr, opt.lr_dev = lr, None
+        if isinstance(grad_scale, torch.Tensor):
+            opt.grad_scale, opt.grad_scale_dev = 1.0, self._pointer(grad_scale, "grad_scale")
+        else:
+            opt.grad_scale, opt.grad_scale_dev = grad_scale, None
+        opt.step = self.step_count + 1
         capturing = torch.cuda.is_current_stream_capturing()
         if capturing and self._step_dev is None:
             raise RuntimeError("AdamW.step under graph capture needs capturable=True")
-        opt = MoeAdamw(0.0 if rate is None else rate, self.betas[0], self.betas[1], self.eps,
-                       self.weight_decay, 1.0 if scale is None else scale, self.step_count + 1,
-                       _at(self._step_dev), rate_dev, scale_dev, self.seed & 0xFFFFFFFF)
-        with _on(self.device):
+        with _on(dev):
             if self._step_dev is not None:
                 self._step_dev.add_(1)
-            _call("moe_adamw_step", _lib.lib().moe_adamw_step(
-                ctypes.byref(opt), self._list, len(self.params), _stream_of(self.device)))
+            status = _lib.lib().moe_adamw_step(ctypes.byref(opt), self._list, len(self.params),
+                                               _stream_of(dev))
+            if status != _lib.MOE_OK and self._step_dev is not None:
+                self._step_dev.sub_(1)  # refused: no step was made
+            _call("moe_adamw_step", status)
         if not capturing:
             self.step_count += 1
 

@@ -27,7 +27,7 @@ int validate_rows(const moe_config_t* c, int dtype) {
   if (c->num_tokens < 0 || c->hidden <= 0 || c->topk <= 0) return MOE_ERR_INVALID_ARG;
   if (!std::isfinite(c->routed_scaling)) return MOE_ERR_INVALID_ARG;
   if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_FP32) return MOE_ERR_INVALID_ARG;
-  if (c->topk > 8) return MOE_ERR_UNSUPPORTED;
+  if (c->topk > 8 || c->hidden > 1 << 28) return MOE_ERR_UNSUPPORTED;
   if (c->num_tokens >= ((int64_t)1 << 31) || pairs(c) >= ((int64_t)1 << 31))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
@@ -137,7 +137,7 @@ int moe_route_backward(const moe_config_t* cfg, const uint16_t* x, const float* 
   if ((st = device_ready())) return st;
   const RouteGradWs w = route_grad_ws(cfg->num_tokens, cfg->hidden, cfg->topk);
   char* ws = static_cast<char*>(workspace);
-  float* dz = reinterpret_cast<float*>(ws);
+  void* dz = ws;
   int32_t* plan = reinterpret_cast<int32_t*>(ws + align_up(w.dz));
   float* part = reinterpret_cast<float*>(ws + align_up(w.dz) + align_up(w.plan));
   return hip_status(launch_route_backward(
@@ -177,17 +177,18 @@ int moe_adamw_step(const moe_adamw_t* opt, const moe_adamw_tensor_t* tensors, in
   a.lr_dev = opt->lr_dev;
   a.grad_scale_dev = opt->grad_scale_dev;
   a.seed = opt->seed;
+  adamw_factors(a);
   // a launch ends where its list is full or its grid nears 2^32 threads (a
-  // tensor of 2^34 elements alone is half of that)
-  constexpr int64_t kMostSpans = (int64_t)1 << 23;
-  int64_t spans = 0;
+  // tensor of 2^34 elements alone stays below that)
+  constexpr int64_t kMostBlocks = (int64_t)1 << 23;
+  int64_t blocks = 0;
   for (int i = 0; i <= num_tensors; ++i) {
-    const int64_t mine = i < num_tensors ? adamw_spans(tensors[i].n) : 0;
+    const int64_t mine = i < num_tensors ? adamw_blocks(tensors[i].n) : 0;
     if (a.count > 0 &&
-        (i == num_tensors || a.count == kAdamTensors || spans + mine > kMostSpans)) {
-      if ((st = hip_status(launch_adamw(a, spans, static_cast<hipStream_t>(stream))))) return st;
+        (i == num_tensors || a.count == kAdamTensors || blocks + mine > kMostBlocks)) {
+      if ((st = hip_status(launch_adamw(a, blocks, static_cast<hipStream_t>(stream))))) return st;
       a.count = 0;
-      spans = 0;
+      blocks = 0;
     }
     if (mine == 0) continue;
     const moe_adamw_tensor_t& t = tensors[i];
@@ -203,8 +204,8 @@ int moe_adamw_step(const moe_adamw_t* opt, const moe_adamw_tensor_t* tensors, in
     d.kind = (t.param_dtype == MOE_DTYPE_FP32 ? 1 : 0) | (t.grad_dtype == MOE_DTYPE_FP32 ? 2 : 0) |
              (t.state_bits == 32 ? 4 : 0);
     d.place = i;
-    a.first[a.count++] = spans;
-    spans += mine;
+    a.first[a.count++] = blocks;
+    blocks += mine;
   }
   return MOE_OK;
 }

@@ -127,7 +127,7 @@ hipError_t launch_route_backward(const uint16_t* x, const float* wr, const int32
                                  const int32_t* perm_src, const int32_t* offsets,
                                  const uint16_t* add, float* grad_w, int accumulate,
                                  uint16_t* grad_x, int64_t T, int H, int topk, int renormalize,
-                                 float* dz, int32_t* plan, float* part, hipStream_t stream);
+                                 void* dz, int32_t* plan, float* part, hipStream_t stream);
 
 // AdamW (adamw.hip).
 constexpr int kAdamTensors = 40;  // tensors per launch: their list is the kernel's argument
@@ -144,9 +144,15 @@ struct AdamTensor {
                  // bit 2: 32-bit states
   int32_t place; // in the caller's list
 };
+// The factors of one step: keep = 1 - lr wd, rate = lr / (1 - b1^t),
+// root = 1 / sqrt(1 - b2^t), gs the gradients' factor.
+struct AdamFactors {
+  float b1, b2, omb1, omb2, eps, keep, rate, root, gs;
+};
 struct AdamArgs {
   AdamTensor tensor[kAdamTensors];
-  int64_t first[kAdamTensors];  // first span (workgroup) of each tensor
+  int64_t first[kAdamTensors];  // first workgroup of each tensor
+  AdamFactors factors;          // of steps without device scalars
   double lr, beta1, beta2, eps, weight_decay, grad_scale;
   int64_t step;
   const int64_t* step_dev;
@@ -156,7 +162,8 @@ struct AdamArgs {
   int32_t count;  // tensors of this launch
 };
 static_assert(sizeof(AdamArgs) <= 4096, "kernel arguments hold 4 KB");
-int64_t adamw_spans(int64_t n);
-hipError_t launch_adamw(const AdamArgs& a, int64_t spans, hipStream_t stream);
+int64_t adamw_blocks(int64_t n);
+void adamw_factors(AdamArgs& a);
+hipError_t launch_adamw(const AdamArgs& a, int64_t blocks, hipStream_t stream);
 
 }  // namespace beam

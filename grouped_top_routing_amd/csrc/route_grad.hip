@@ -14,10 +14,13 @@
 // dz is sparse (topk of 256 experts per token), so both products are sums of
 // rows: 4 topk T H operations instead of the dense 4*256 T H, no matrix cores
 // needed, and fp32 throughout.  What bounds them is how often the rows are
-// read: each x row by topk experts and each W row by all its tokens.  Both
-// kernels therefore work on slabs of 256 columns, and consecutive workgroups
-// of one XCD stay on one slab: the W slab (256 KB) and the x slab (512 B per
-// token) stay in that XCD's L2.
+// read: each x row by topk experts (420 MB from L2 at 5120 tokens of 5120
+// columns) and each W row by all its tokens (840 MB).  Workgroups therefore take
+// slabs of columns, and consecutive workgroups of one XCD stay on one slab, so
+// that an x slab (256 columns, 512 B per token) and a W slab (1 MB) stay in that
+// XCD's L2 (token by token instead, grad x of 5120 tokens takes 74 against 62
+// us of the whole call); large batches read W from LDS.  The whole call takes
+// 71 us at 5120 tokens, of which grad W 30 (14 TB/s of L2 reads).
 #include "common.h"
 #include "kernels.h"
 
@@ -26,8 +29,13 @@ namespace beam {
 namespace {
 
 constexpr int kE = 256;            // experts
-constexpr int kSlab = 256;         // columns per workgroup
-constexpr int kTokensPerWave = 4;  // of the grad x part
+constexpr int kSlab = 256;         // columns per workgroup of the grad W part
+constexpr int kDxCols = 1024;      // columns per workgroup of the grad x part
+// Batches from which grad x reads the weights from LDS instead of L2 (the whole
+// call, hidden 5120, `add` not in the caches: 72 against 90 us at 5120 tokens,
+// 235 against 310 at 16384; 38 against 42 at 2048, but 35 against 32 without
+// `add`, and 23 against 19 at 512).
+constexpr int64_t kLdsFrom = 4096;
 
 // The plan (int32): per chunk (expert, first row, rows), then for every
 // expert its first chunk (kE + 1 entries).  Every expert has at least one
@@ -38,33 +46,55 @@ struct Plan {
 };
 __host__ __device__ inline Plan plan_of(int32_t* p, int64_t chunks) { return {p, p + 3 * chunks}; }
 
+// What a slot adds: its expert (kE for none) and dz.  Every token has 8 of
+// them, whatever topk is, so that they come in one scalar load of 64 bytes.
+struct Slot {
+  int expert;
+  float dz;
+};
+
 __device__ __forceinline__ float log_sigmoid(float z) {
   return fminf(z, 0.f) - log1pf(expf(-fabsf(z)));
 }
 
-// Workgroups 0 .. gridDim.x - 2: dz of 256 tokens.  The last one: the plan.
+// Sum, maximum over the 8 lanes of a token.
+__device__ __forceinline__ float sum8(float v) {
+#pragma unroll
+  for (int off = 4; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+  return v;
+}
+__device__ __forceinline__ float max8(float v) {
+#pragma unroll
+  for (int off = 4; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off));
+  return v;
+}
+
+// Workgroups 0 .. gridDim.x - 2: dz of 32 tokens, a lane per slot (a lane per
+// token took 8.7 instead of 3.8 us at 5120 tokens: the exponentials of 8 slots
+// one after another).  The last one: the plan.
 __global__ __launch_bounds__(256) void route_dz_kernel(
     const int32_t* __restrict__ ids, const float* __restrict__ logits,
-    const float* __restrict__ grad_w, float* __restrict__ dz, const int32_t* __restrict__ offsets,
+    const float* __restrict__ grad_w, Slot* __restrict__ slots, const int32_t* __restrict__ offsets,
     int32_t* __restrict__ plan, int64_t chunks, int64_t T, int topk, int renormalize) {
   if (blockIdx.x == gridDim.x - 1) {
-    __shared__ int sum[kE];
-    const int e = threadIdx.x;
+    __shared__ int wave_sum[kE / kWave];
+    const int e = threadIdx.x, lane = e % kWave, wave = e / kWave;
     const int n = (int)(T * topk);
     const int lo = min(max(offsets[e], 0), n), hi = min(max(offsets[e + 1], lo), n);
     const int mine = max(1, (hi - lo + kRouteChunk - 1) / kRouteChunk);
-    sum[e] = mine;
-    __syncthreads();
-    for (int off = 1; off < kE; off <<= 1) {
-      const int v = e >= off ? sum[e - off] : 0;
-      __syncthreads();
-      sum[e] += v;
-      __syncthreads();
+    int sum = mine;
+#pragma unroll
+    for (int off = 1; off < kWave; off <<= 1) {
+      const int v = __shfl_up(sum, off);
+      if (lane >= off) sum += v;
     }
+    if (lane == kWave - 1) wave_sum[wave] = sum;
+    __syncthreads();
+    for (int i = 0; i < wave; ++i) sum += wave_sum[i];
     const Plan pl = plan_of(plan, chunks);
     // offsets that overlap could ask for more chunks than there are
-    const int end = (int)min((int64_t)sum[e], chunks);
-    const int begin = min(sum[e] - mine, end);
+    const int end = (int)min((int64_t)sum, chunks);
+    const int begin = min(sum - mine, end);
     pl.first[e] = begin;
     if (e == kE - 1) pl.first[kE] = end;
     for (int c = begin; c < end; ++c) {
@@ -75,86 +105,89 @@ __global__ __launch_bounds__(256) void route_dz_kernel(
     }
     return;
   }
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (t >= T) return;
-  float z[8], g[8], w[8];
-  bool on[8];
-  float top = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    on[j] = false;
-    z[j] = g[j] = w[j] = 0.f;
-    if (j < topk) {
-      const int e = ids[t * topk + j];
-      on[j] = e >= 0 && e < kE;
-      if (on[j]) {
-        z[j] = logits[t * topk + j];
-        g[j] = grad_w[t * topk + j];
-        w[j] = log_sigmoid(z[j]);
-        top = fmaxf(top, w[j]);
-      }
-    }
-  }
-  float mean = 0.f;  // sum_i g_i w_i
+  const int64_t t = (int64_t)blockIdx.x * 32 + threadIdx.x / 8;
+  const int j = threadIdx.x % 8;
+  const bool slot = t < T && j < topk;
+  const int64_t p = t * topk + j;
+  const int e = slot ? ids[p] : -1;
+  const bool on = e >= 0 && e < kE;
+  const float z = slot ? logits[p] : 0.f;
+  const float g = on ? (slot ? grad_w[p] : 0.f) : 0.f;
+  float w, mean = 0.f;  // mean = sum_i g_i w_i
   if (renormalize) {
-    // w_j = s_j / S as exp(log s_j - max): scores that all underflow (every
-    // logit -infinity) weigh nothing, and nothing flows back
-    float total = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      w[j] = on[j] && top > -INFINITY ? expf(w[j] - top) : 0.f;
-      total += w[j];
-    }
-    const float inv = total != 0.f ? 1.f / total : 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      w[j] *= inv;
-      if (on[j]) mean += g[j] * w[j];
-    }
+    // w_j = s_j / S as exp(log s_j - max): scores that all underflow keep
+    // their ratios; with every logit -infinity nothing flows back
+    const float ls = log_sigmoid(z);
+    const float top = max8(on ? ls : -INFINITY);
+    w = on && top > -INFINITY ? expf(ls - top) : 0.f;
+    const float total = sum8(w);
+    w = total != 0.f ? w / total : 0.f;
+    mean = sum8(g * w);
   } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = sigmoidf_(z[j]);
+    w = sigmoidf_(z);
   }
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < topk)
-      dz[t * topk + j] = on[j] ? w[j] * sigmoidf_(-z[j]) * (g[j] - mean) : 0.f;
+  if (t < T) slots[t * 8 + j] = {on ? e : kE, on ? w * sigmoidf_(-z) * (g - mean) : 0.f};
 }
 
 // One (chunk, slab) of grad W: 4 waves, each two rows at a time (32 lanes of
-// 8 columns each), summed in LDS.  An expert of one chunk is finished here;
-// of several, each chunk leaves a partial sum for route_dw_reduce_kernel.
+// 8 columns each), summed in LDS.  The chunk's tokens and dz are brought into
+// LDS first, so that the row loads depend on nothing and run 4 deep.  An
+// expert of one chunk is finished here; of several, each chunk leaves a
+// partial sum for route_dw_reduce_kernel.
+struct DwShared {
+  float dz[kRouteChunk];
+  int token[kRouteChunk];
+  float part[4][kSlab];
+};
 __device__ __forceinline__ void dw_item(const uint16_t* __restrict__ x,
                                         const int32_t* __restrict__ perm_src,
-                                        const float* __restrict__ dz, const Plan pl, int chunk,
+                                        const Slot* __restrict__ slots, const Plan pl, int chunk,
                                         int slab, float* __restrict__ grad, int accumulate,
                                         float* __restrict__ part, int64_t n, int H, int topk,
-                                        float (*lds)[kSlab]) {
+                                        DwShared& sh) {
   const int e = pl.chunk[3 * chunk], r0 = pl.chunk[3 * chunk + 1], rows = pl.chunk[3 * chunk + 2];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const bool whole = pl.first[e + 1] - pl.first[e] == 1;
+  static_assert(kRouteChunk == 256, "a thread per row of the chunk");
+  {
+    const int i = threadIdx.x;
+    const int64_t p = i < rows ? perm_src[r0 + i] : -1;
+    const bool ok = p >= 0 && p < n;
+    const uint32_t t = (uint32_t)p / (uint32_t)topk;
+    sh.dz[i] = ok ? slots[(int64_t)t * 8 + ((uint32_t)p - t * topk)].dz : 0.f;
+    sh.token[i] = ok ? (int)t : -1;
+  }
+  __syncthreads();
   const int col = slab * kSlab + (lane & 31) * 8;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int i = 2 * wave + (lane >> 5); i < rows; i += 8) {
-    const int64_t p = perm_src[r0 + i];
-    if (p < 0 || p >= n) continue;
-    const float d = dz[p];
-    const uint4 q = ld16(x + (int64_t)((uint32_t)p / (uint32_t)topk) * H + col);
-    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+  for (int i0 = 2 * wave + (lane >> 5); i0 < rows; i0 += 32) {
+    uint4 q[4];
+    float d[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      acc[2 * c] += d * bf16_to_f32(u[c] & 0xffffu);
-      acc[2 * c + 1] += d * __uint_as_float(u[c] & 0xffff0000u);
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + 8 * u;  // at most 255: rows past the chunk's hold no token
+      const int t = sh.token[i];
+      d[u] = sh.dz[i];
+      q[u] = t >= 0 ? ld16(x + (int64_t)t * H + col) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        acc[2 * c] += d[u] * bf16_to_f32(w[c] & 0xffffu);
+        acc[2 * c + 1] += d[u] * __uint_as_float(w[c] & 0xffff0000u);
+      }
     }
   }
 #pragma unroll
   for (int c = 0; c < 8; ++c) acc[c] += __shfl_xor(acc[c], 32);
   if (lane < 32)
 #pragma unroll
-    for (int c = 0; c < 8; ++c) lds[wave][lane * 8 + c] = acc[c];
+    for (int c = 0; c < 8; ++c) sh.part[wave][lane * 8 + c] = acc[c];
   __syncthreads();
   const int c = threadIdx.x;
-  float s = ((lds[0][c] + lds[1][c]) + lds[2][c]) + lds[3][c];
-  const bool whole = pl.first[e + 1] - pl.first[e] == 1;
+  const float s = ((sh.part[0][c] + sh.part[1][c]) + sh.part[2][c]) + sh.part[3][c];
   if (whole) {
     float* o = grad + (size_t)e * H + slab * kSlab + c;
     *o = accumulate ? *o + s : s;
@@ -163,70 +196,124 @@ __device__ __forceinline__ void dw_item(const uint16_t* __restrict__ x,
   }
 }
 
-// kTokensPerWave tokens of one slab of grad x per wave.
+// kDxCols columns of one token of grad x, 256 per wave.  `add` may be grad_x.
 __device__ __forceinline__ void dx_item(const float* __restrict__ wr,
-                                        const int32_t* __restrict__ ids,
-                                        const float* __restrict__ dz,
-                                        const uint16_t* __restrict__ add,
-                                        uint16_t* __restrict__ grad_x, int64_t group, int slab,
-                                        int64_t T, int H, int topk) {
-  const int lane = threadIdx.x & 63;
-  const int col = slab * kSlab + lane * 4;
-  for (int i = 0; i < kTokensPerWave; ++i) {
-    const int64_t t = __builtin_amdgcn_readfirstlane(
-        (int)((group * 4 + (threadIdx.x >> 6)) * kTokensPerWave + i));
-    if (t >= T) return;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (add) {
-      const uint2 a = *reinterpret_cast<const uint2*>(add + t * H + col);
-      acc = make_float4(bf16_to_f32(a.x & 0xffffu), __uint_as_float(a.x & 0xffff0000u),
-                        bf16_to_f32(a.y & 0xffffu), __uint_as_float(a.y & 0xffff0000u));
-    }
-    float4 q[8];
-    float d[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = j < topk ? ids[t * topk + j] : -1;
-      const bool on = e >= 0 && e < kE;
-      d[j] = on ? dz[t * topk + j] : 0.f;
-      q[j] = on ? *reinterpret_cast<const float4*>(wr + (size_t)e * H + col)
-                : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      acc.x += d[j] * q[j].x; acc.y += d[j] * q[j].y;
-      acc.z += d[j] * q[j].z; acc.w += d[j] * q[j].w;
-    }
-    *reinterpret_cast<uint2*>(grad_x + t * H + col) =
-        make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+                                        const Slot* __restrict__ slots, const uint16_t* add,
+                                        uint16_t* grad_x, int64_t t, int slab, int H) {
+  const int col = slab * kDxCols + 4 * threadIdx.x;
+  if (col >= H) return;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (add) {
+    const uint2 a = *reinterpret_cast<const uint2*>(add + t * H + col);
+    acc = make_float4(bf16_to_f32(a.x & 0xffffu), __uint_as_float(a.x & 0xffff0000u),
+                      bf16_to_f32(a.y & 0xffffu), __uint_as_float(a.y & 0xffff0000u));
   }
+  float4 q[8];
+  float d[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const Slot s = slots[t * 8 + j];
+    d[j] = s.dz;
+    q[j] = s.expert < kE ? *reinterpret_cast<const float4*>(wr + (size_t)s.expert * H + col)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    acc.x += d[j] * q[j].x; acc.y += d[j] * q[j].y;
+    acc.z += d[j] * q[j].z; acc.w += d[j] * q[j].w;
+  }
+  *reinterpret_cast<uint2*>(grad_x + t * H + col) =
+      make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
 }
 
 // Both products in one launch (they are independent): the first dw_items
-// workgroups take (slab, chunk), the rest (slab, 16 tokens).  Within each part
+// workgroups take (slab, chunk), the rest (slab, token).  Within each part
 // XCD b mod 8 walks a contiguous eighth of the slab-major items.
 __global__ __launch_bounds__(256) void route_grad_kernel(
-    const uint16_t* __restrict__ x, const float* __restrict__ wr, const int32_t* __restrict__ ids,
-    const int32_t* __restrict__ perm_src, const float* __restrict__ dz, int32_t* plan,
-    int64_t chunks, const uint16_t* __restrict__ add, float* __restrict__ grad_w, int accumulate,
-    float* __restrict__ part, uint16_t* __restrict__ grad_x, int64_t T, int H, int topk,
-    int64_t dw_blocks) {
-  __shared__ float lds[4][kSlab];
+    const uint16_t* __restrict__ x, const float* __restrict__ wr,
+    const int32_t* __restrict__ perm_src, const Slot* __restrict__ slots, int32_t* plan,
+    int64_t chunks, const uint16_t* add, float* __restrict__ grad_w, int accumulate,
+    float* __restrict__ part, uint16_t* grad_x, int64_t T, int H, int topk,
+    uint32_t dw_end) {
+  __shared__ DwShared sh;
   const int slabs = H / kSlab;
-  int64_t b = blockIdx.x;
-  if (b < dw_blocks) {
-    const int64_t per = dw_blocks / 8, item = (b & 7) * per + (b >> 3);
-    const int slab = (int)(item / chunks), chunk = (int)(item - slab * chunks);
+  // fewer than 2^24 workgroups: 32-bit arithmetic
+  uint32_t b = blockIdx.x;
+  if (b < dw_end) {
+    const uint32_t item = (b & 7) * (dw_end / 8) + (b >> 3);
+    const int slab = item / (uint32_t)chunks, chunk = item - slab * (uint32_t)chunks;
     const Plan pl = plan_of(plan, chunks);
     if (slab >= slabs || chunk >= pl.first[kE]) return;
-    dw_item(x, perm_src, dz, pl, chunk, slab, grad_w, accumulate, part, T * topk, H, topk, lds);
+    dw_item(x, perm_src, slots, pl, chunk, slab, grad_w, accumulate, part, T * topk, H, topk, sh);
   } else {
-    b -= dw_blocks;
-    const int64_t per = (gridDim.x - dw_blocks) / 8, item = (b & 7) * per + (b >> 3);
-    const int64_t groups = (T + 4 * kTokensPerWave - 1) / (4 * kTokensPerWave);
-    const int slab = (int)(item / groups);
-    if (slab >= slabs) return;
-    dx_item(wr, ids, dz, add, grad_x, item - slab * groups, slab, T, H, topk);
+    b -= dw_end;
+    const uint32_t item = (b & 7) * ((gridDim.x - dw_end) / 8) + (b >> 3);
+    const int slab = item / (uint32_t)T;
+    if (slab * kDxCols >= H) return;
+    dx_item(wr, slots, add, grad_x, item - slab * (uint32_t)T, slab, H);
+  }
+}
+
+// grad x of large batches: a workgroup holds 128 columns of all 256 experts'
+// weights in LDS (128 KB, read at twice the rate of L1) and walks its share of
+// the tokens, 8 per wave at a time; the next 8 tokens' slots and `add` are on
+// their way meanwhile.  `add` may be grad_x.
+constexpr int kLdsCols = 128, kLdsWaves = 16, kLdsTokens = 8;
+__global__ __launch_bounds__(kLdsWaves * 64) void route_dx_kernel(
+    const float* __restrict__ wr, const Slot* __restrict__ slots, const uint16_t* add,
+    uint16_t* grad_x, int64_t T, int H, int64_t share) {
+  __shared__ float4 w4[(kE + 1) * kLdsCols / 4];  // the last row, of an empty slot, is zero
+  const int slabs = H / kLdsCols;
+  const int slab = blockIdx.x % slabs;
+  const int64_t part = blockIdx.x / slabs;
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  const int64_t end = min(T, (part + 1) * share);
+  const int col = slab * kLdsCols + 2 * lane;
+  constexpr int kStep = kLdsWaves * kLdsTokens;
+  int64_t t0 = part * share + wave * kLdsTokens;
+  // lane 8u + j holds slot j of token t0 + u
+  const auto load = [&](int64_t t, Slot& s, uint32_t (&a)[kLdsTokens]) {
+    s = slots[min(t * 8 + lane, end * 8 - 1)];
+#pragma unroll
+    for (int u = 0; u < kLdsTokens; ++u)
+      a[u] = add ? *reinterpret_cast<const uint32_t*>(add + min(t + u, end - 1) * H + col) : 0u;
+  };
+  Slot next;
+  uint32_t next_a[kLdsTokens];
+  load(t0, next, next_a);
+#pragma unroll
+  for (int i = threadIdx.x; i < kE * kLdsCols / 4; i += kLdsWaves * 64) {
+    const int e = i / (kLdsCols / 4), c = i % (kLdsCols / 4);
+    w4[i] = *reinterpret_cast<const float4*>(wr + (size_t)e * H + slab * kLdsCols + 4 * c);
+  }
+  if (threadIdx.x < kLdsCols / 4)
+    w4[kE * kLdsCols / 4 + threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+  __syncthreads();
+  const float2* w2 = reinterpret_cast<const float2*>(w4) + lane;  // row stride kLdsCols / 2
+  for (; t0 < end; t0 += kStep) {
+    const Slot now = next;
+    uint32_t a[kLdsTokens];
+#pragma unroll
+    for (int u = 0; u < kLdsTokens; ++u) a[u] = next_a[u];
+    if (t0 + kStep < end) load(t0 + kStep, next, next_a);
+#pragma unroll
+    for (int u = 0; u < kLdsTokens; ++u) {
+      float2 q[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        q[j] = w2[__builtin_amdgcn_readlane(now.expert, 8 * u + j) * (kLdsCols / 2)];
+      float ax = bf16_to_f32(a[u] & 0xffffu), ay = __uint_as_float(a[u] & 0xffff0000u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = __uint_as_float(
+            __builtin_amdgcn_readlane(__float_as_uint(now.dz), 8 * u + j));
+        ax += d * q[j].x;
+        ay += d * q[j].y;
+      }
+      if (t0 + u < end)
+        __builtin_nontemporal_store(pack_bf16x2(ax, ay),
+                                    reinterpret_cast<uint32_t*>(grad_x + (t0 + u) * H + col));
+    }
   }
 }
 
@@ -247,22 +334,24 @@ __global__ __launch_bounds__(256) void route_dw_reduce_kernel(int32_t* plan, int
 }
 
 int64_t chunks_of(int64_t n) { return kE + n / kRouteChunk; }
-int64_t groups_of(int64_t T) { return (T + 4 * kTokensPerWave - 1) / (4 * kTokensPerWave); }
+int64_t dw_blocks(int64_t T, int H, int topk) {
+  return (chunks_of(T * topk) * (H / kSlab) + 7) / 8 * 8;
+}
+int64_t dx_blocks(int64_t T, int H) { return (T * ((H + kDxCols - 1) / kDxCols) + 7) / 8 * 8; }
 
 }  // namespace
 
 RouteGradWs route_grad_ws(int64_t T, int H, int topk) {
   const int64_t n = T * topk, chunks = chunks_of(n);
   RouteGradWs w;
-  w.dz = (size_t)n * sizeof(float);
+  w.dz = (size_t)T * 8 * sizeof(Slot);
   w.plan = (size_t)(3 * chunks + kE + 1) * sizeof(int32_t);
   w.part = n > kRouteChunk ? (size_t)chunks * H * sizeof(float) : 0;
   return w;
 }
 
 bool route_grad_fits(int64_t T, int H, int topk) {
-  const int64_t blocks = (chunks_of(T * topk) + groups_of(T)) * (H / kSlab) + 16;
-  return blocks * 256 < (int64_t)1 << 32;
+  return (dw_blocks(T, H, topk) + dx_blocks(T, H)) * 256 < (int64_t)1 << 32;
 }
 
 hipError_t launch_route_backward(const uint16_t* x, const float* wr, const int32_t* ids,
@@ -270,18 +359,29 @@ hipError_t launch_route_backward(const uint16_t* x, const float* wr, const int32
                                  const int32_t* perm_src, const int32_t* offsets,
                                  const uint16_t* add, float* grad_w, int accumulate,
                                  uint16_t* grad_x, int64_t T, int H, int topk, int renormalize,
-                                 float* dz, int32_t* plan, float* part, hipStream_t stream) {
+                                 void* dz, int32_t* plan, float* part, hipStream_t stream) {
+  Slot* slots = static_cast<Slot*>(dz);
   const int64_t n = T * topk, chunks = chunks_of(n), slabs = H / kSlab;
-  hipLaunchKernelGGL(route_dz_kernel, dim3((unsigned)((T + 255) / 256 + 1)), dim3(256), 0, stream,
-                     ids, logits, grad_topk_w, dz, offsets, plan, chunks, T, topk, renormalize);
+  hipLaunchKernelGGL(route_dz_kernel, dim3((unsigned)((T + 31) / 32 + 1)), dim3(256), 0, stream,
+                     ids, logits, grad_topk_w, slots, offsets, plan, chunks, T, topk, renormalize);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t dw = (chunks * slabs + 7) / 8 * 8;
-  const int64_t dx = grad_x ? (groups_of(T) * slabs + 7) / 8 * 8 : 0;
+  const bool lds_dx = grad_x && T >= kLdsFrom;
+  const int64_t dw = dw_blocks(T, H, topk), dx = grad_x && !lds_dx ? dx_blocks(T, H) : 0;
   hipLaunchKernelGGL(route_grad_kernel, dim3((unsigned)(dw + dx)), dim3(256), 0, stream, x, wr,
-                     ids, perm_src, dz, plan, chunks, add, grad_w, accumulate, part, grad_x, T, H,
-                     topk, dw);
+                     perm_src, slots, plan, chunks, add, grad_w, accumulate, part, grad_x, T, H,
+                     topk, (uint32_t)dw);
   if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (lds_dx) {
+    // as many workgroups as there are CUs, each with an equal share of tokens
+    const int cols = H / kLdsCols;
+    int64_t parts = cols < 256 ? 256 / cols : 1;
+    const int64_t share = (T + parts - 1) / parts;
+    parts = (T + share - 1) / share;
+    hipLaunchKernelGGL(route_dx_kernel, dim3((unsigned)(cols * parts)), dim3(kLdsWaves * 64), 0,
+                       stream, wr, slots, add, grad_x, T, H, share);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   if (n <= kRouteChunk) return hipSuccess;  // no expert has a second chunk
   hipLaunchKernelGGL(route_dw_reduce_kernel, dim3(kE, (unsigned)slabs), dim3(256), 0, stream, plan,
                      chunks, part, grad_w, H, accumulate);

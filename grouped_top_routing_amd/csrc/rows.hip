@@ -26,12 +26,33 @@ namespace {
 
 // 16 bytes at any element's alignment: gfx950 reads and writes unaligned
 // global memory in one instruction, so rows of odd length take the same path.
+typedef unsigned v4u_t __attribute__((ext_vector_type(4), aligned(2)));
 __device__ __forceinline__ uint4 ld16u(const void* p) {
-  uint4 v;
-  __builtin_memcpy(&v, p, 16);
-  return v;
+  const v4u_t v = *static_cast<const v4u_t*>(p);
+  return make_uint4(v.x, v.y, v.z, v.w);
 }
-__device__ __forceinline__ void st16u(void* p, uint4 v) { __builtin_memcpy(p, &v, 16); }
+__device__ __forceinline__ uint4 ld16u_nt(const void* p) {
+  const v4u_t v = __builtin_nontemporal_load(static_cast<const v4u_t*>(p));
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+template <bool NT>
+__device__ __forceinline__ void st16u(void* p, uint4 v) {
+  const v4u_t q = {v.x, v.y, v.z, v.w};
+  if constexpr (NT) __builtin_nontemporal_store(q, static_cast<v4u_t*>(p));
+  else *static_cast<v4u_t*>(p) = q;
+}
+
+// Cache policy.  Sorted rows are read once: non-temporal loads (dispatch then
+// its gradient, 5120 bf16 columns: 169 -> 122 us at 4096 tokens, no difference
+// at 512).  Sorted rows that are written are read next, by the experts or
+// their gradient: up to twice the 256 MB last-level cache a plain store leaves
+// enough of them there (same chain, plain against non-temporal stores: 58
+// against 69 us at 2048 tokens, 122 against 131 at 4096 with 335 MB), past it
+// only displaces what is still to be read (275 against 255 us at 8192 tokens,
+// 577 against 502 at 16384).  Token rows, an eighth of that, are written
+// non-temporally (the gradient of dispatch and a kernel that reads it, 4096
+// tokens: 88 -> 86 us, 16384: 360 -> 337).
+constexpr int64_t kCachedBytes = (int64_t)512 << 20;
 
 // The row types: storage S, elements per 16 bytes, conversions.
 struct Bf16Rows {
@@ -85,7 +106,7 @@ __device__ __forceinline__ void slot_rows(const int32_t* __restrict__ perm_dst, 
 // dispatch: thread (x, y) of a workgroup handles one piece of item
 // blockIdx.x * blockDim.y + y, an item being (token, slice of blockDim.x
 // pieces).  blockDim.x is a multiple of 64, so a wave has one token.
-template <class R, bool WEIGHTED>
+template <class R, bool WEIGHTED, bool NT>
 __global__ __launch_bounds__(256) void dispatch_kernel(
     const typename R::S* __restrict__ x, const int32_t* __restrict__ perm_dst,
     const float* __restrict__ w, typename R::S* __restrict__ out, int64_t T, int64_t n, int H,
@@ -112,7 +133,7 @@ __global__ __launch_bounds__(256) void dispatch_kernel(
         for (int c = 0; c < N; ++c) f[c] *= wt;
         o = R::round(f);
       }
-      st16u(out + rows[j] * H + v * N, o);
+      st16u<NT>(out + rows[j] * H + v * N, o);
     }
   } else {
     for (int c = 0; c < H - v * N; ++c) {
@@ -134,7 +155,7 @@ __global__ __launch_bounds__(256) void dispatch_kernel(
 // DOT: grad w[p] = c * <a[t], b[r]>.
 // Threads (.., y) of a workgroup share one token; for DOT blockDim.x threads
 // cover the whole row and its waves' sums meet in LDS.
-template <class R, bool SCATTER, bool DOT, bool WRITE>
+template <class R, bool SCATTER, bool DOT, bool WRITE, bool NT>
 __global__ __launch_bounds__(1024) void row_grad_kernel(
     const typename R::S* __restrict__ a, const typename R::S* __restrict__ b,
     const int32_t* __restrict__ perm_dst, const float* __restrict__ w,
@@ -161,10 +182,10 @@ __global__ __launch_bounds__(1024) void row_grad_kernel(
       if constexpr (DOT || !SCATTER) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          qb[j] = rows[j] >= 0 ? ld16u(b + rows[j] * H + v * N) : make_uint4(0u, 0u, 0u, 0u);
+          qb[j] = rows[j] >= 0 ? ld16u_nt(b + rows[j] * H + v * N) : make_uint4(0u, 0u, 0u, 0u);
       }
       float fa[N];
-      if constexpr (DOT || SCATTER) R::widen(ld16u(a + at), fa);
+      if constexpr (DOT || SCATTER) R::widen(ld16u_nt(a + at), fa);
       float acc[N];
 #pragma unroll
       for (int c = 0; c < N; ++c) acc[c] = 0.f;
@@ -184,13 +205,13 @@ __global__ __launch_bounds__(1024) void row_grad_kernel(
           float o[N];
 #pragma unroll
           for (int c = 0; c < N; ++c) o[c] = wt[j] * fa[c];
-          st16u(out + rows[j] * H + v * N, R::round(o));
+          st16u<NT>(out + rows[j] * H + v * N, R::round(o));
         }
       }
       if constexpr (!SCATTER) {
 #pragma unroll
         for (int c = 0; c < N; ++c) acc[c] *= scale;
-        st16u(out + at, R::round(acc));
+        st16u<true>(out + at, R::round(acc));
       }
     } else {
       for (int c = 0; c < H - v * N; ++c) {
@@ -210,13 +231,22 @@ __global__ __launch_bounds__(1024) void row_grad_kernel(
   if constexpr (DOT) {
     const int waves = blockDim.x / kWave;  // of one token
     const int wave = (threadIdx.y * blockDim.x + threadIdx.x) / kWave;
+    // the 8 sums across a wave in 10 exchanges: at each of the first three
+    // a lane hands half of its sums over and keeps the other half, so that
+    // lanes 8j .. 8j + 7 end up with the parts of sum j
+    const int lane = threadIdx.x % kWave;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
+    for (int half = 4; half >= 1; half >>= 1) {
+      const bool up = lane & (8 * half);
 #pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) dot[j] += __shfl_xor(dot[j], off);
-    if (threadIdx.x % kWave == 0)
+      for (int j = 0; j < half; ++j) {
+        const float keep = up ? dot[j + half] : dot[j], give = up ? dot[j] : dot[j + half];
+        dot[j] = keep + __shfl_xor(give, 8 * half);
+      }
+    }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) part[wave][j] = dot[j];
+    for (int off = 4; off >= 1; off >>= 1) dot[0] += __shfl_xor(dot[0], off);
+    if (lane % 8 == 0) part[wave][lane / 8] = dot[0];
     __syncthreads();
     if (t < T && (int)threadIdx.x < topk) {
       float s = 0.f;
@@ -241,19 +271,17 @@ hipError_t dispatch(const void* x, const int32_t* perm_dst, const float* w, void
     if ((nv + c - 1) / c * c <= (nv + tx - 1) / tx * tx) tx = c;
   const int slices = (nv + tx - 1) / tx, ty = 256 / tx;
   const int64_t n = T * topk;
+  const bool nt_out = n * H * (int64_t)sizeof(S) > kCachedBytes;
   int64_t most = kLaunchThreads / ((int64_t)slices * tx);
   if (most < 1) most = 1;
   for (int64_t t0 = 0; t0 < T; t0 += most) {
     const int64_t nt = T - t0 < most ? T - t0 : most;
     const dim3 grid((unsigned)((nt * slices + ty - 1) / ty)), block(tx, ty);
-    const S* xs = static_cast<const S*>(x) + t0 * H;
-    S* o = static_cast<S*>(out);
-    if (w)
-      hipLaunchKernelGGL((dispatch_kernel<R, true>), grid, block, 0, stream, xs,
-                         perm_dst + t0 * topk, w + t0 * topk, o, nt, n, H, topk, slices);
-    else
-      hipLaunchKernelGGL((dispatch_kernel<R, false>), grid, block, 0, stream, xs,
-                         perm_dst + t0 * topk, w, o, nt, n, H, topk, slices);
+    const auto kernel = w ? (nt_out ? dispatch_kernel<R, true, true> : dispatch_kernel<R, true, false>)
+                          : (nt_out ? dispatch_kernel<R, false, true> : dispatch_kernel<R, false, false>);
+    hipLaunchKernelGGL(kernel, grid, block, 0, stream, static_cast<const S*>(x) + t0 * H,
+                       perm_dst + t0 * topk, w ? w + t0 * topk : nullptr, static_cast<S*>(out), nt,
+                       n, H, topk, slices);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -271,12 +299,15 @@ hipError_t row_grad(const void* a, const void* b, const int32_t* perm_dst, const
   const int tx = kWave * ((waves + rounds - 1) / rounds);
   const int ty = tx >= 256 ? 1 : 256 / tx;
   const int64_t n = T * topk, most = kLaunchThreads / tx;
+  constexpr bool writes_sorted = SCATTER && WRITE;
+  const bool nt_out = !writes_sorted || n * H * (int64_t)sizeof(S) > kCachedBytes;
   for (int64_t t0 = 0; t0 < T; t0 += most) {
     const int64_t nt = T - t0 < most ? T - t0 : most;
     const S* as = static_cast<const S*>(a);
     S* o = static_cast<S*>(out);
-    hipLaunchKernelGGL((row_grad_kernel<R, SCATTER, DOT, WRITE>),
-                       dim3((unsigned)((nt + ty - 1) / ty)), dim3(tx, ty), 0, stream,
+    const auto kernel = nt_out ? row_grad_kernel<R, SCATTER, DOT, WRITE, true>
+                               : row_grad_kernel<R, SCATTER, DOT, WRITE, !writes_sorted>;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((nt + ty - 1) / ty)), dim3(tx, ty), 0, stream,
                        as ? as + t0 * H : nullptr, static_cast<const S*>(b),
                        perm_dst + t0 * topk, w ? w + t0 * topk : nullptr,
                        SCATTER ? o : o + t0 * H, grad_w ? grad_w + t0 * topk : nullptr, nt, n, H,

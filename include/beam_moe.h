@@ -335,7 +335,7 @@ int moe_layer_forward_lora(const moe_config_t* cfg, const uint16_t* x, const flo
  *
  * moe_dispatch, moe_dispatch_backward, moe_combine_rows and
  * moe_combine_backward move rows of `dtype` (moe_dtype) and read num_tokens, hidden, topk (and routed_scaling)
- * of cfg only: any hidden >= 1, 1 <= topk <= 8, num_tokens * topk < 2^31.
+ * of cfg only: 1 <= hidden <= 2^28, 1 <= topk <= 8, num_tokens * topk < 2^31.
  * Rows are dense; row pointers must be 16-byte aligned, though rows of odd
  * length within a tensor need not be.  perm_dst is moe_permute's (or any
  * injective map of pairs to rows); an entry outside [0, num_tokens * topk)

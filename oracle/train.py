@@ -156,9 +156,6 @@ def encode_8bit(x, random, low):
     a = np.where(finite, np.abs(y), 0.0)
     step = 2.0 ** (np.maximum(np.floor(np.log2(np.where(a > 0, a, 1.0))), -6) - 3)
     units = np.floor(a / step + random.astype(np.float64) / 65536)
-    # below 2^-6 the sum is specified in fp32
-    small = np.floor((a * 512).astype(np.float32) + random.astype(np.float32) / np.float32(65536))
-    units = np.where(a < 2.0 ** -6, small.astype(np.float64), units)
     q = units * step
     if low:
         q = np.where((a > 0) & (q == 0), 2.0 ** -9, q)

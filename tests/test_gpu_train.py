@@ -19,6 +19,8 @@ relative error of one rounding to t; with U = u(fp32) = 2^-24:
   1 + 3 additions across lanes and waves, then one per chunk: (40 + chunks) U
   times the sum of the magnitudes on top of dz's error.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -265,6 +267,7 @@ def _router_case(T, H, k, seed, dropped=0.0, hot=0, spread=1.5):
 ROUTE_CASES = [(1, 256, 1, 0.0, 0), (1, 5120, 8, 0.0, 0), (5, 512, 3, 0.3, 0),
                (31, 768, 8, 0.0, 0), (32, 256, 8, 0.0, 0), (33, 256, 8, 0.05, 0),
                (100, 1280, 5, 0.0, 8), (700, 512, 8, 0.02, 8), (3000, 256, 8, 0.0, 12),
+               (4096, 256, 8, 0.0, 0), (4099, 512, 3, 0.05, 8),
                (4, 256, 8, 1.0, 0)]
 
 
@@ -317,6 +320,24 @@ def test_route_backward_repeated_and_foreign_ids():
     within(gw, rw, bw, "grad_w_router")
     within(gx, rx, bx + u_of(BF) * 1.01 * (np.abs(rx) + bx), "grad_x")
     assert float(gx[11].abs().max()) == 0
+
+
+@pytest.mark.parametrize("T", [37, 5000])
+def test_route_backward_adds_in_place(T):
+    # the C call allows grad_x_add to be grad_x itself
+    say(f"[route_backward] in place, T={T}")
+    x, W, ids, z, g, src, off, add = _router_case(T, 768, 8, T, 0.02)
+    want_w, want_x = gtr.route_backward(x, W, ids, z, g, src, off, grad_x_add=add)
+    cfg = gtr.make_config(T, 768, 128, num_groups=1, topk_groups=1)
+    nb = gtr.workspace_bytes(cfg, gtr.ENTRY_ROUTE_BACKWARD)
+    ws = torch.empty(nb, dtype=torch.uint8, device=DEV)
+    gw, gx = torch.empty_like(W), add.clone()
+    st = gtr.lib().moe_route_backward(
+        ctypes.byref(cfg), *(t.data_ptr() for t in (x, W, ids, z, g, src, off, gx)), 0,
+        gw.data_ptr(), gx.data_ptr(), ws.data_ptr(), nb,
+        torch.cuda.current_stream(DEV).cuda_stream)
+    assert st == 0
+    assert torch.equal(gw, want_w) and torch.equal(gx, want_x)
 
 
 @pytest.mark.parametrize("renormalize", [True, False])

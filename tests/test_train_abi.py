@@ -45,6 +45,7 @@ def test_row_calls_check_the_configuration(call):
     assert call(_cfg(H=0)) == INVALID
     assert call(_cfg(topk=0)) == INVALID
     assert call(_cfg(topk=9)) == UNSUPPORTED
+    assert call(_cfg(H=(1 << 28) + 1)) == UNSUPPORTED
     assert call(_cfg(T=1 << 28)) == UNSUPPORTED
     assert call(_cfg(T=1 << 62)) == UNSUPPORTED
     assert call(_cfg(routed_scaling=float("inf"))) == INVALID
