@@ -29,9 +29,13 @@ def _at(t):
 
 
 def _need(t, name, dtype, shape, device):
-    """t is a dense tensor of this type and shape on `device`."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.is_cuda and t.device == device and t.is_contiguous()):
+    """t is a dense tensor of this type and shape on `device`, a HIP device."""
+    try:
+        good = (t.dtype is dtype and t.shape == shape and t.device == device
+                and t.is_contiguous())
+    except AttributeError:
+        good = False
+    if not good:
         _check(t, name, dtype, shape, device)
 
 
@@ -200,7 +204,8 @@ def route_backward(x, w_router, topk_ids, topk_logits, grad_topk_w, perm_src, of
         raise TypeError("w_router must be a torch.Tensor [E, H]")
     (T, H), k, E, dev = x.shape, topk_ids.shape[1], w_router.shape[0], x.device
     f32, i32, pairs = torch.float32, torch.int32, (T, k)
-    _need(x, "x", torch.bfloat16, (T, H), dev)
+    if x.dtype is not torch.bfloat16 or not x.is_cuda or not x.is_contiguous():
+        _check(x, "x", torch.bfloat16)
     _need(w_router, "w_router", f32, (E, H), dev)
     _need(topk_ids, "topk_ids", i32, pairs, dev)
     _need(topk_logits, "topk_logits", f32, pairs, dev)
@@ -215,17 +220,17 @@ def route_backward(x, w_router, topk_ids, topk_logits, grad_topk_w, perm_src, of
     if accumulate:
         _need(grad_w_router, "grad_w_router", f32, (E, H), dev)
     cfg, nb = _route_config(T, H, E, k, bool(renormalize))
-    grad_x = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if need_grad_x else None
+    grad_x = torch.empty_like(x) if need_grad_x else None
     if T == 0:
         return (grad_w_router if accumulate else torch.zeros_like(w_router)), grad_x
     if not accumulate:
-        grad_w_router = torch.empty(E, H, dtype=f32, device=dev)
+        grad_w_router = torch.empty_like(w_router)
     with _on(dev):
-        ws = _scratch(nb, dev, workspace)
+        ws = _scratch(nb, dev, workspace) if nb else None
         _call("moe_route_backward", _lib.lib().moe_route_backward(
             cfg, x.data_ptr(), w_router.data_ptr(), topk_ids.data_ptr(), topk_logits.data_ptr(),
             grad_topk_w.data_ptr(), perm_src.data_ptr(), offsets.data_ptr(), _at(grad_x_add),
-            accumulate, grad_w_router.data_ptr(), _at(grad_x), ws.data_ptr(), nb,
+            accumulate, grad_w_router.data_ptr(), _at(grad_x), _at(ws), nb,
             _stream_of(dev)))
     return grad_w_router, grad_x
 

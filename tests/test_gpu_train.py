@@ -265,7 +265,7 @@ def _router_case(T, H, k, seed, dropped=0.0, hot=0, spread=1.5):
 
 
 ROUTE_CASES = [(1, 256, 1, 0.0, 0), (1, 5120, 8, 0.0, 0), (5, 512, 3, 0.3, 0),
-               (31, 768, 8, 0.0, 0), (32, 256, 8, 0.0, 0), (33, 256, 8, 0.05, 0),
+               (31, 768, 8, 0.0, 0), (32, 256, 8, 0.0, 0), (33, 256, 8, 0.05, 0), (128, 2304, 8, 0.05, 4), (129, 2304, 8, 0.05, 4),
                (100, 1280, 5, 0.0, 8), (700, 512, 8, 0.02, 8), (3000, 256, 8, 0.0, 12),
                (4096, 256, 8, 0.0, 0), (4099, 512, 3, 0.05, 8),
                (4, 256, 8, 1.0, 0)]
@@ -585,3 +585,281 @@ def test_adamw_refuses():
     with pytest.raises(ValueError, match="state must hold"):
         _opt([p], state={"exp_avg": [p]})
     assert float(p.abs().max()) == 0
+
+
+# ---------------------------------------------------------------------------
+# together, as they are used
+def _tiny(T, seed=0):
+    w = synth.workload("tiny", T=T)
+    d = synth.make_inputs(w, seed, device=DEV)
+    return d["x"], d["w_router"], d["w_gate_up"], d["w_down"]
+
+
+@pytest.mark.parametrize("T,replay", [(40, False), (300, False), (300, True)])
+def test_router_training_steps(T, replay):
+    """Three steps of RouterTrainer: the output is the block's bit for bit, the
+    gradient that of the staged reference on the same expert outputs, and the
+    weights those of AdamW on that gradient."""
+    say(f"[trainer] T={T} replay={replay}")
+    x, W, gu, dn = _tiny(T)
+    W = W.clone()
+    ids_in = None
+    if replay:
+        ids_in = gtr.route(x, W)[0].clone()
+        ids_in[2, 3], ids_in[5] = -1, 400
+    trainer = gtr.RouterTrainer(W, gu, dn, lr=1e-3, weight_decay=0.1)
+    g = torch.Generator().manual_seed(1)
+    p, m, v = n64(W), 0.0 * n64(W), 0.0 * n64(W)
+    for step in (1, 2, 3):
+        if not replay:
+            want = gtr.layer_forward(x, W, gu, dn)
+        for micro in range(2):  # two micro-batches accumulate
+            go = (torch.randn(T, 256, generator=g) * 1e-2).to(BF).to(DEV)
+            out = trainer.forward(x, ids_in)
+            if not replay:
+                assert torch.equal(out, want)
+            xs, ids, w, z, off, src, dst, y = trainer._saved
+            before = None if trainer.grad is None else n64(trainer.grad)
+            grad = n64(trainer.backward(go))
+            idn, d = ids.cpu().numpy(), dst.cpu().numpy()
+            _, gw = train.combine_backward(n64(go), n64(y), d, n64(w), 2.5)
+            rw, _ = train.route_backward(n64(x), n64(W), idn, n64(z), gw)
+            # the weights' gradient carries 32 U of its terms' magnitudes
+            size = 2.5 * train._dots(np.abs(n64(go)), np.abs(n64(y)), d, 8) * (32 * U)
+            on = (idn >= 0) & (idn < 256)
+            dz_err = np.where(on, size + size.sum(1, keepdims=True), 0.0)  # |w (1 - s)| <= 1
+            ew = np.zeros_like(rw)
+            for j in range(8):
+                t = np.nonzero(on[:, j])[0]
+                np.add.at(ew, idn[t, j], dz_err[t, j, None] * np.abs(n64(x))[t])
+            bw, _ = _route_bounds(n64(x), n64(W), idn, n64(z), gw, True, T * 8 // 256 + 1)
+            if before is not None:
+                rw, bw = rw + before, bw + U * (np.abs(rw) + np.abs(before))
+            within(grad, rw, bw + ew, f"step {step} gradient {micro}")
+        total = n64(trainer.grad)
+        start = n64(W)
+        trainer.step(grad_scale=0.5)
+        assert trainer.grad is None
+        m0, v0 = m, v
+        _, m, v = train.adamw(start, total, m0, v0, step=step, lr=1e-3, beta1=0.9, beta2=0.999,
+                              eps=1e-8, weight_decay=0.1, grad_scale=0.5)
+        ref = train.adamw(start, total, m0, v0, step=step, lr=1e-3, beta1=0.9, beta2=0.999,
+                          eps=1e-8, weight_decay=0.1, grad_scale=0.5)[0]
+        # an update is at most lr / (1 - beta1) here; its error a few hundred U
+        # of that (m and v carry up to `step` roundings each)
+        within(W, ref, 4 * U * np.abs(start) + 1e-2 * 256 * U, f"step {step} weights")
+        m, v = n64(trainer.optimizer.state["exp_avg"][0]), n64(trainer.optimizer.state["exp_avg_sq"][0])
+    with pytest.raises(RuntimeError, match="no gradient"):
+        trainer.step()
+    with pytest.raises(RuntimeError, match="no forward"):
+        trainer.backward(go)
+
+
+def test_router_gradient_equals_differences():
+    """The chain combine -> router against central differences of the block in
+    fp64, routing and expert outputs fixed."""
+    say("[trainer] differences")
+    T = 64
+    x, W, gu, dn = _tiny(T, 3)
+    trainer = gtr.RouterTrainer(W.clone(), gu, dn)
+    trainer.forward(x)
+    _, ids, _, _, _, _, dst, y = trainer._saved
+    go = (torch.randn(T, 256, generator=torch.Generator().manual_seed(2)) * 1e-2).to(BF).to(DEV)
+    grad = n64(trainer.backward(go))
+    X, Y, G, idn = n64(x), n64(y), n64(go), ids.cpu().numpy().astype(np.int64)
+    dots = train._dots(G, Y, dst.cpu().numpy(), 8)
+
+    def loss(w64):
+        s = 1 / (1 + np.exp(-np.take_along_axis(X @ w64.T, idn, 1)))
+        return 2.5 * float(((s / s.sum(1, keepdims=True)) * dots).sum())
+
+    rng, w0 = np.random.default_rng(0), n64(W)
+    for _ in range(4):
+        d = rng.normal(size=w0.shape)
+        h = 1e-4
+        slope = (loss(w0 + h * d) - loss(w0 - h * d)) / (2 * h)
+        # the gradient's fp32 error along d, from its entries' scale; third
+        # derivatives leave h^2 of it
+        assert abs(slope - (grad * d).sum()) <= 1e-4 * np.abs(grad * d).sum(), slope
+
+
+@pytest.mark.parametrize("dt,H", [(F, 100), (BF, 256)], ids=["fp32", "bf16"])
+def test_own_experts_between_dispatch_and_combine(dt, H):
+    """A caller's trainable experts (each scales its rows by a vector): the
+    gradients of x, the weights and the experts against the reference."""
+    say(f"[own experts] {dt} H={H}")
+    T, k = 90, 4
+    ids, off, src, dst = routing(T, k, 8, 0.1)
+    d = dst.cpu().numpy()
+    x, w, a = rows(T, H, dt, 1), weights(T, k, 2), rows(256, H, F, 3)
+    n = int(off[-1])
+    e_of = torch.repeat_interleave(torch.arange(256, device=DEV), off[1:].long() - off[:-1].long())
+    xp = gtr.dispatch(x, dst, topk=k, out=torch.zeros(T * k, H, dtype=dt, device=DEV))
+    y = torch.zeros_like(xp)
+    y[:n] = (xp[:n].float() * a[e_of]).to(dt)
+    out = gtr.combine(y, dst, w, routed_scaling=2.5)
+    _sum_close(out, n64(y), d, n64(w), 2.5, dt, "out")
+    go = rows(T, H, dt, 4)
+    gy, gw = gtr.combine_backward(go, y, dst, w, out=torch.zeros_like(y))
+    grad_a = torch.zeros(256, H, device=DEV).index_add_(0, e_of, gy[:n].float() * xp[:n].float())
+    gxp = torch.zeros_like(gy)
+    gxp[:n] = (gy[:n].float() * a[e_of]).to(dt)
+    gx = gtr.dispatch_backward(gxp, dst, topk=k)
+    # the reference from the definition, per token and slot
+    X, A, Wt, G = n64(x), n64(a), n64(w), n64(go)
+    rx, rA, rw = np.zeros((T, H)), np.zeros((256, H)), np.zeros((T, k))
+    size_x, size_w, size_A = np.zeros((T, H)), np.zeros((T, k)), np.zeros((256, H))
+    for t in range(T):
+        for j in range(k):
+            e = ids[t, j]
+            if e < 0:
+                continue
+            rx[t] += 2.5 * Wt[t, j] * G[t] * A[e]
+            size_x[t] += np.abs(2.5 * Wt[t, j] * G[t] * A[e])
+            rA[e] += 2.5 * Wt[t, j] * G[t] * X[t]
+            size_A[e] += np.abs(2.5 * Wt[t, j] * G[t] * X[t])
+            rw[t, j] = 2.5 * (G[t] * X[t] * A[e]).sum()
+            size_w[t, j] = 2.5 * np.abs(G[t] * X[t] * A[e]).sum()
+    # roundings to dt on the way: gy and gxp (x), gy (A), y (w), then sums
+    u = u_of(dt)
+    within(gx, rx, (3.1 * u + 24 * U) * size_x, "grad x")
+    within(grad_a, rA, (1.1 * u + 64 * U) * size_A, "grad experts")
+    within(gw, rw, (1.1 * u + 40 * U) * size_w, "grad weights")
+
+
+def test_captured_training_step_replays():
+    """Forward, backward and a capturable AdamW step in one graph, replayed with
+    eager work and new inputs between: every replay gives the eager bits."""
+    say("[graph] a captured step, replayed five times")
+    T = 200
+    x, W0, gu, dn = _tiny(T, 5)
+    lr = torch.full((1,), 1e-3, device=DEV)
+    scale = torch.full((1,), 1.0, device=DEV)
+
+    def chain(xx, go, W, opt):
+        ids, w, z = gtr.route(xx, W, return_logits=True)
+        _, off, src, dst = gtr.permute(ids)
+        y = gtr.expert_ffn(xx, src, off, gu, dn)
+        out = gtr.combine(y, dst, w)
+        gy, gw = gtr.combine_backward(go, y, dst, w)
+        xp = gtr.dispatch(xx, dst)
+        gx = gtr.dispatch_backward(gy, dst)
+        gW, gx = gtr.route_backward(xx, W, ids, z, gw, src, off, grad_x_add=gx)
+        opt.step([gW], lr=lr, grad_scale=scale)
+        return out, gx, gW, xp
+
+    for bits in (32, 8):
+        Wc, We = W0.clone(), W0.clone()
+        oc = gtr.AdamW([Wc], state_bits=bits, seed=9, capturable=True)
+        oe = gtr.AdamW([We], state_bits=bits, seed=9)
+        xs, gos = x.clone(), torch.zeros(T, 256, dtype=BF, device=DEV)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):  # warm up, then undo
+            chain(xs, gos, Wc, oc)
+        torch.cuda.current_stream().wait_stream(side)
+        Wc.copy_(W0)
+        for name in oc.state:
+            for t in oc.state[name]:
+                if t is not None:
+                    t.view(torch.uint8).zero_()
+        oc._step_dev.zero_()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = chain(xs, gos, Wc, oc)
+        g = torch.Generator().manual_seed(4)
+        for i in range(5):
+            xs.copy_(torch.randn(T, 256, generator=g).to(BF))
+            gos.copy_((torch.randn(T, 256, generator=g) * 1e-2).to(BF))
+            lr.fill_(1e-3 / (i + 1))
+            scale.fill_(1.0 + 0.25 * i)
+            graph.replay()
+            torch.cuda.synchronize()
+            want = chain(xs, gos, We, oe)
+            torch.cuda.synchronize()
+            for a, b in zip(got, want):
+                assert torch.equal(a, b), (bits, i)
+            assert torch.equal(Wc, We), (bits, i)
+            for name in oc.state:
+                for a, b in zip(oc.state[name], oe.state[name]):
+                    assert a is None or torch.equal(a.float(), b.float()), (bits, i, name)
+        assert int(oc._step_dev) == 5
+
+
+def test_two_captured_graphs_do_not_share_scratch():
+    say("[graph] two graphs of the router's gradient on two streams at once")
+    cases = [_router_case(1500, 768, 8, s, 0.0, 8) for s in (1, 2)]
+    want = [gtr.route_backward(*c[:7], grad_x_add=c[7]) for c in cases]
+    graphs, got = [], []
+    for c in cases:
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            got.append(gtr.route_backward(*c[:7], grad_x_add=c[7]))
+        graphs.append(gr)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(3):
+        for gw, gx in got:
+            gw.zero_(), gx.zero_()
+        torch.cuda.synchronize()
+        for s, gr in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                gr.replay()
+        torch.cuda.synchronize()
+        for (gw, gx), (rw, rx) in zip(got, want):
+            assert torch.equal(gw, rw) and torch.equal(gx, rx)
+
+
+def test_side_streams_and_repeated_calls_give_the_same_bits():
+    say("[streams] calls on two side streams at once, and again")
+    x, W, ids, z, g, src, off, add = _router_case(900, 1280, 8, 3)
+    dst = torch.empty_like(src)
+    dst[src.long()] = torch.arange(900 * 8, device=DEV, dtype=torch.int32)
+    w, y = weights(900, 8, 1), rows(900 * 8, 1280, BF, 2)
+
+    def all_of():
+        return (*gtr.route_backward(x, W, ids, z, g, src, off, grad_x_add=add),
+                gtr.dispatch(x, dst, topk_w=w), *gtr.dispatch_backward(y, dst, x=x, topk_w=w),
+                *gtr.combine_backward(x, y, dst, w))
+
+    want = all_of()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(2):
+        got = []
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(all_of())
+        torch.cuda.synchronize()
+        for r in got:
+            for a, b in zip(r, want):
+                assert torch.equal(a, b)
+
+
+def test_capture_needs_a_capturable_optimizer():
+    say("[graph] AdamW without capturable=True")
+    p, g = torch.zeros(64, device=DEV), torch.ones(64, device=DEV)
+    opt = gtr.AdamW([p])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(RuntimeError, match="capturable"):
+            opt.step([g])
+    assert opt.step_count == 0
+
+
+def test_empty_batches_and_lists():
+    say("[empty] no tokens")
+    i = lambda n: torch.zeros(n, dtype=torch.int32, device=DEV)
+    z = lambda *s, dt=F: torch.zeros(*s, dtype=dt, device=DEV)
+    assert gtr.dispatch(z(0, 7), i(0)).shape == (0, 7)
+    assert gtr.dispatch_backward(z(0, 7), i(0)).shape == (0, 7)
+    gy, gw = gtr.combine_backward(z(0, 7), z(0, 7), i(0), z(0, 8))
+    assert gy.shape == (0, 7) and gw.shape == (0, 8)
+    assert gtr.combine(z(0, 7), i(0), z(0, 8)).shape == (0, 7)
+    W = rows(256, 256, F, 1)
+    args = (z(0, 256, dt=BF), W, i(0).view(0, 8), z(0, 8), z(0, 8), i(0), i(257))
+    gW, gx = gtr.route_backward(*args)
+    assert gx.shape == (0, 256) and float(gW.abs().max()) == 0
+    acc = torch.ones_like(W)
+    assert gtr.route_backward(*args, grad_w_router=acc)[0] is acc and float(acc.min()) == 1

@@ -111,9 +111,9 @@ def test_route_backward_checks_its_workspace():
     assert _route_backward(c, ws=MIS, nb=need) == INVALID
     # a grid of 2^32 threads or more
     assert _route_backward(_cfg(T=(1 << 31) // 8 - 1, H=256 * 64)) == UNSUPPORTED
-    # below one chunk of pairs no partial sums are kept
-    small = gtr.workspace_bytes(_cfg(T=16, H=5120), gtr.ENTRY_ROUTE_BACKWARD)
-    assert 0 < small < 1 << 16
+    # small batches need none
+    assert gtr.workspace_bytes(_cfg(T=128, H=5120), gtr.ENTRY_ROUTE_BACKWARD) == 0
+    assert gtr.workspace_bytes(_cfg(T=129, H=5120), gtr.ENTRY_ROUTE_BACKWARD) > 129 * 64
 
 
 # ---------------------------------------------------------------------------
