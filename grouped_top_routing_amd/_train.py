@@ -270,22 +270,33 @@ class AdamW:
                 raise TypeError(f"params[{i}] must be torch.bfloat16 or torch.float32, got "
                                 f"{getattr(p, 'dtype', type(p))}")
             _check(p, f"params[{i}]", p.dtype, None, self.params[0].device)
+        places = [p.data_ptr() for p in self.params if p.numel()]
+        if len(set(places)) < len(places):
+            raise ValueError("AdamW: a parameter is listed twice")
         self.device = self.params[0].device
         self.lr, self.state_bits = lr, state_bits
-        self.step_count = step_count
-        self._step_dev = None
+        self._steps, self._step_dev = step_count, None
         if capturable:
             self._step_dev = torch.full((1,), step_count, dtype=torch.int64, device=self.device)
         self.state = self._new_state() if state is None else self._taken(state)
         self._list = (MoeAdamwTensor * len(self.params))()
-        for i, p in enumerate(self.params):
-            d, s = self._list[i], {k: v[i] for k, v in self.state.items()}
-            d.master, d.m, d.v = _at(s["master"]), _at(s["exp_avg"]), _at(s["exp_avg_sq"])
+        self._rows = []  # per parameter: itself, its address, shape, elements and list entry
+        st = self.state
+        for i, (p, d) in enumerate(zip(self.params, self._list)):
+            d.param, d.master = p.data_ptr(), _at(st["master"][i])
+            d.m, d.v = st["exp_avg"][i].data_ptr(), st["exp_avg_sq"][i].data_ptr()
             if state_bits == 8:
-                d.m_scale, d.v_scale = _at(s["exp_avg_scale"]), _at(s["exp_avg_sq_scale"])
+                d.m_scale = st["exp_avg_scale"][i].data_ptr()
+                d.v_scale = st["exp_avg_sq_scale"][i].data_ptr()
             d.param_dtype, d.state_bits = _DTYPES[p.dtype], state_bits
+            self._rows.append((p, p.data_ptr(), p.shape, p.numel(), d))
         self._opt = MoeAdamw(beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay,
                              step_dev=_at(self._step_dev), seed=seed & 0xFFFFFFFF)
+
+    @property
+    def step_count(self):
+        """Steps made so far (with capturable read from the device)."""
+        return self._steps if self._step_dev is None else int(self._step_dev)
 
     def _kinds(self):
         """The state's lists and their element types."""
@@ -308,22 +319,23 @@ class AdamW:
         state = dict(state)
         if "master" not in state and all(p.dtype == torch.float32 for p in self.params):
             state["master"] = [None] * len(self.params)
-        want = set(self._kinds()) | {"master"}
-        if set(state) != want:
-            raise ValueError(f"state must hold {sorted(want)}, got {sorted(state)}")
+        kinds = {**self._kinds(), "master": torch.float32}
+        if set(state) != set(kinds):
+            raise ValueError(f"state must hold {sorted(kinds)}, got {sorted(state)}")
         for k, v in state.items():
             if len(v) != len(self.params):
                 raise ValueError(f"state[{k!r}] must have {len(self.params)} entries, got {len(v)}")
+            scale = k.endswith("scale")
             for i, (p, t) in enumerate(zip(self.params, v)):
-                name = f"state[{k!r}][{i}]"
-                if k == "master" and p.dtype == torch.float32:
+                if k == "master" and p.dtype is torch.float32:
                     if t is not None:
-                        raise ValueError(f"{name} must be None: its parameter is fp32")
+                        raise ValueError(f"state['master'][{i}] must be None: its parameter is "
+                                         "fp32")
                     continue
-                _check(t, name, self._kinds().get(k, torch.float32), None, self.device)
-                n = (p.numel() + 31) // 32 if k.endswith("scale") else p.numel()
+                n = (p.numel() + 31) // 32 if scale else p.numel()
+                _check(t, f"state[{k!r}][{i}]", kinds[k], None, self.device)
                 if t.numel() != n:
-                    raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+                    raise ValueError(f"state[{k!r}][{i}] must have {n} elements, got {t.numel()}")
         return {k: tuple(v) for k, v in state.items()}
 
     def _pointer(self, t, name):
@@ -333,6 +345,19 @@ class AdamW:
             raise ValueError(f"{name} must have one element, got {t.numel()}")
         return t.data_ptr()
 
+    def _refuse(self, grads):
+        """Raises the error of the first gradient or parameter that is wrong."""
+        for i, ((p, at, shape, _, _), g) in enumerate(zip(self._rows, grads)):
+            if g is None:
+                continue
+            if getattr(g, "dtype", None) not in _DTYPES:
+                raise TypeError(f"grads[{i}] must be torch.bfloat16 or torch.float32, got "
+                                f"{getattr(g, 'dtype', type(g))}")
+            _check(g, f"grads[{i}]", g.dtype, shape, self.device)
+            if p.data_ptr() != at:
+                raise RuntimeError(f"params[{i}] lies elsewhere than when this AdamW was made: "
+                                   "make a new one with its state")
+
     def step(self, grads, *, lr=None, grad_scale=1.0):
         """One step.  grads: one tensor (bf16 or fp32, the parameter's shape)
         per parameter, or None to leave that parameter and its state alone.
@@ -341,16 +366,19 @@ class AdamW:
         if len(grads) != len(self.params):
             raise ValueError(f"{len(self.params)} gradients expected, got {len(grads)}")
         dev, opt = self.device, self._opt
-        for i, (p, g, d) in enumerate(zip(self.params, grads, self._list)):
+        for (p, at, shape, n, d), g in zip(self._rows, grads):
             if g is None:
                 d.n = 0
                 continue
-            kind = _DTYPES.get(getattr(g, "dtype", None))
-            if kind is None:
-                raise TypeError(f"grads[{i}] must be torch.bfloat16 or torch.float32, got "
-                                f"{getattr(g, 'dtype', type(g))}")
-            _need(g, f"grads[{i}]", g.dtype, p.shape, dev)
-            d.param, d.grad, d.grad_dtype, d.n = p.data_ptr(), g.data_ptr(), kind, p.numel()
+            try:
+                kind = _DTYPES[g.dtype]
+                good = (g.shape == shape and g.device == dev and g.is_contiguous()
+                        and p.data_ptr() == at)
+            except (AttributeError, KeyError):
+                good = False
+            if not good:
+                self._refuse(grads)
+            d.grad, d.grad_dtype, d.n = g.data_ptr(), kind, n
         if lr is None:
             lr = self.lr
         if isinstance(lr, torch.Tensor):
@@ -361,7 +389,7 @@ class AdamW:
             opt.grad_scale, opt.grad_scale_dev = 1.0, self._pointer(grad_scale, "grad_scale")
         else:
             opt.grad_scale, opt.grad_scale_dev = grad_scale, None
-        opt.step = self.step_count + 1
+        opt.step = self._steps + 1
         capturing = torch.cuda.is_current_stream_capturing()
         if capturing and self._step_dev is None:
             raise RuntimeError("AdamW.step under graph capture needs capturable=True")
@@ -374,7 +402,7 @@ class AdamW:
                 self._step_dev.sub_(1)  # refused: no step was made
             _call("moe_adamw_step", status)
         if not capturing:
-            self.step_count += 1
+            self._steps += 1
 
 
 # ---------------------------------------------------------------------------
@@ -393,9 +421,10 @@ class RouterTrainer:
             trainer.backward(loss_gradient(out, target))
             trainer.step()
 
-    Experts are bf16 (w_gate_up, w_down in weight_layout), or Fp8Weights in
-    the place of w_gate_up with w_down None.  The hidden state's gradient is
-    not computed: it would need the experts' own."""
+    Between forward and backward x and w_router stay as they are.  Experts are
+    bf16 (w_gate_up, w_down in weight_layout), or Fp8Weights in the place of
+    w_gate_up with w_down None.  The hidden state's gradient is not computed: it
+    would need the experts' own."""
 
     def __init__(self, w_router, w_gate_up, w_down=None, *, sel_bias=None, num_groups=8,
                  topk_groups=4, topk=8, renormalize=True, routed_scaling=2.5,

@@ -112,9 +112,10 @@ __global__ __launch_bounds__(256) void dispatch_kernel(
     const float* __restrict__ w, typename R::S* __restrict__ out, int64_t T, int64_t n, int H,
     int topk, int slices) {
   constexpr int N = R::N;
-  const int64_t item = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  const int64_t t = __builtin_amdgcn_readfirstlane((int)(item / slices));
-  const int v = (int)(item - t * slices) * blockDim.x + threadIdx.x;
+  // a launch has at most 2^31 threads: 32-bit items
+  const uint32_t item = blockIdx.x * blockDim.y + threadIdx.y, it = item / (uint32_t)slices;
+  const int64_t t = __builtin_amdgcn_readfirstlane((int)it);
+  const int v = (int)(item - it * slices) * blockDim.x + threadIdx.x;
   if (t >= T || v * N >= H) return;
   int64_t rows[8];
   slot_rows(perm_dst, t, topk, n, rows);

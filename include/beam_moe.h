@@ -444,7 +444,8 @@ int moe_route_backward(const moe_config_t* cfg, const uint16_t* x, const float* 
  *
  * A gradient that is not finite reaches its own element alone (in 8 bits as
  * NaN).  All tensor pointers are 16-byte aligned except the scales; n may be
- * any number, 0 included.  State memory of zeros is a valid start.
+ * any number, 0 included.  State memory of zeros is a valid start (scale code 0
+ * stands for 0).
  */
 typedef struct moe_adamw_tensor {
   void* param;         /* [n] fp32, or bf16 with `master`                      */

@@ -573,6 +573,8 @@ def test_adamw_refuses():
         _opt([p]).step([torch.zeros(63, device=DEV)])
     with pytest.raises(TypeError):
         _opt([p]).step([torch.zeros(64, dtype=torch.float16, device=DEV)])
+    with pytest.raises(ValueError, match="listed twice"):
+        _opt([p, p])
     with pytest.raises(ValueError, match="contiguous"):
         _opt([torch.zeros(8, 8, device=DEV).t()])
     with pytest.raises(gtr.MoeError):  # a view that is not 16-byte aligned
@@ -582,6 +584,11 @@ def test_adamw_refuses():
         _opt([p]).step([torch.zeros(64, device=DEV)], lr=-1.0)
     with pytest.raises(ValueError, match="one element"):
         _opt([p]).step([torch.zeros(64, device=DEV)], lr=torch.zeros(2, device=DEV))
+    moved = torch.zeros(64, device=DEV)
+    o = _opt([moved])
+    moved.data = torch.ones(128, device=DEV)
+    with pytest.raises(RuntimeError, match="lies elsewhere"):
+        o.step([torch.zeros(64, device=DEV)])
     with pytest.raises(ValueError, match="state must hold"):
         _opt([p], state={"exp_avg": [p]})
     assert float(p.abs().max()) == 0
@@ -764,7 +771,7 @@ def test_captured_training_step_replays():
                 if t is not None:
                     t.view(torch.uint8).zero_()
         oc._step_dev.zero_()
-        torch.cuda.synchronize()
+        assert oc.step_count == 0
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             got = chain(xs, gos, Wc, oc)
@@ -784,7 +791,7 @@ def test_captured_training_step_replays():
             for name in oc.state:
                 for a, b in zip(oc.state[name], oe.state[name]):
                     assert a is None or torch.equal(a.float(), b.float()), (bits, i, name)
-        assert int(oc._step_dev) == 5
+        assert oc.step_count == oe.step_count == 5
 
 
 def test_two_captured_graphs_do_not_share_scratch():
