@@ -9,7 +9,8 @@ relative error of one rounding to t; with U = u(fp32) = 2^-24:
   of the terms' magnitudes (plus the scale's product), then u(t) |ref|;
 * a dot product over a row is at most 8 terms in a thread and column round (H up
   to 8192 bf16 or 4096 fp32 is one round), 6 additions across a wave, 15 across
-  waves and the scale: 32 U times the sum of the magnitudes;
+  waves and the scale: 32 U times the sum of the magnitudes (a row of up to 32
+  pieces: 8 terms and 5 additions);
 * dz of the router goes through log-sigmoids, exponentials and a quotient.  The
   exponent's absolute error is at most U (4 + 4 max|z|) (log1p and its
   difference, the maximum's own, their difference) and turns into a relative
@@ -85,7 +86,8 @@ def weights(T, k, seed):
 ROW_CASES = [(1, 1, 1, 0.0), (1, 5120, 8, 0.0), (3, 7, 2, 0.4), (5, 8, 3, 0.0), (17, 63, 4, 0.1),
              (33, 257, 5, 0.0), (64, 512, 8, 0.0), (31, 777, 6, 0.2), (130, 1023, 7, 0.05),
              (9, 4097, 8, 0.1), (40, 5120, 8, 0.0), (4, 8200, 8, 0.0), (700, 256, 8, 0.0),
-             (2, 33000, 3, 0.0), (6, 40, 8, 1.0)]
+             (2, 33000, 3, 0.0), (6, 40, 8, 1.0),
+             (37, 9, 8, 0.1), (1000, 64, 8, 0.05), (77, 129, 8, 0.0), (50, 130, 7, 0.1)]
 
 
 @pytest.mark.parametrize("T,H,k,dropped", ROW_CASES)
