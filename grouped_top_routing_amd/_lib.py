@@ -445,9 +445,10 @@ def _combine_rows(y_perm, perm_dst, topk_w, routed_scaling):
                       routed_scaling=routed_scaling)
     out = torch.empty(T, H, dtype=dt, device=y_perm.device)
     if T:
-        _call("moe_combine_rows", lib().moe_combine_rows(
-            ctypes.byref(cfg), DTYPE_FP32 if dt == torch.float32 else DTYPE_BF16, _ptr(y_perm),
-            _ptr(perm_dst), _ptr(topk_w), _ptr(out), _stream(y_perm.device)))
+        with torch.cuda.device(y_perm.device):
+            _call("moe_combine_rows", lib().moe_combine_rows(
+                ctypes.byref(cfg), DTYPE_FP32 if dt == torch.float32 else DTYPE_BF16,
+                _ptr(y_perm), _ptr(perm_dst), _ptr(topk_w), _ptr(out), _stream(y_perm.device)))
     return out
 
 

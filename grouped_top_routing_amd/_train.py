@@ -7,7 +7,6 @@ the current stream of the tensors' device; nothing falls back to torch.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 
@@ -54,18 +53,18 @@ def _need_rows(t, name, rows=None):
     return shape[1], t.dtype, t.device
 
 
-def _stream_of(device):
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-_NOTHING = contextlib.nullcontext()
-
-
-def _on(device):
-    """Launches go to the tensors' device, whichever is current."""
+def _launch(name, device, *args):
+    """Calls the library on the current stream of the tensors' device,
+    whichever device is current."""
+    call = getattr(_lib.lib(), name)
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
     if device.index == torch.cuda.current_device():
-        return _NOTHING
-    return torch.cuda.device(device)
+        status = call(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = call(*args, stream)
+    if status:
+        _call(name, status)
 
 
 def _scratch(nbytes, device, workspace):
@@ -118,10 +117,8 @@ def dispatch(x, perm_dst, *, topk=8, topk_w=None, out=None):
     else:
         _need(out, "out", dt, (T * topk, H), dev)
     if T:
-        with _on(dev):
-            _call("moe_dispatch", _lib.lib().moe_dispatch(
-                _rows_config(T, H, topk), _DTYPES[dt], x.data_ptr(), perm_dst.data_ptr(),
-                _at(topk_w), out.data_ptr(), _stream_of(dev)))
+        _launch("moe_dispatch", dev, _rows_config(T, H, topk), _DTYPES[dt], x.data_ptr(),
+                perm_dst.data_ptr(), _at(topk_w), out.data_ptr())
     return out
 
 
@@ -139,13 +136,11 @@ def dispatch_backward(grad_x_perm, perm_dst, *, topk=8, x=None, topk_w=None):
             raise ValueError("x is for the gradient of topk_w: pass topk_w too")
         _need(x, "x", dt, (T, H), dev)
     grad_x = torch.empty(T, H, dtype=dt, device=dev)
-    grad_w = None if x is None else torch.empty(T, topk, dtype=torch.float32, device=dev)
+    grad_w = None if x is None else torch.empty_like(topk_w)
     if T:
-        with _on(dev):
-            _call("moe_dispatch_backward", _lib.lib().moe_dispatch_backward(
-                _rows_config(T, H, topk), _DTYPES[dt], grad_x_perm.data_ptr(),
-                perm_dst.data_ptr(), _at(topk_w), _at(x), grad_x.data_ptr(), _at(grad_w),
-                _stream_of(dev)))
+        _launch("moe_dispatch_backward", dev, _rows_config(T, H, topk), _DTYPES[dt],
+                grad_x_perm.data_ptr(), perm_dst.data_ptr(), _at(topk_w), _at(x),
+                grad_x.data_ptr(), _at(grad_w))
     return grad_x if x is None else (grad_x, grad_w)
 
 
@@ -175,13 +170,11 @@ def combine_backward(grad_out, y_perm, perm_dst, topk_w, *, routed_scaling=2.5, 
             _need(out, "out", dt, (T * k, H), dev)
             grad_y = out
     if need_grad_w:
-        grad_w = torch.empty(T, k, dtype=torch.float32, device=dev)
+        grad_w = torch.empty_like(topk_w)
     if T:
-        with _on(dev):
-            _call("moe_combine_backward", _lib.lib().moe_combine_backward(
-                _rows_config(T, H, k, float(routed_scaling)), _DTYPES[dt], grad_out.data_ptr(),
-                _at(y_perm), perm_dst.data_ptr(), topk_w.data_ptr(), _at(grad_y), _at(grad_w),
-                _stream_of(dev)))
+        _launch("moe_combine_backward", dev, _rows_config(T, H, k, float(routed_scaling)),
+                _DTYPES[dt], grad_out.data_ptr(), _at(y_perm), perm_dst.data_ptr(),
+                topk_w.data_ptr(), _at(grad_y), _at(grad_w))
     return grad_y, grad_w
 
 
@@ -225,13 +218,11 @@ def route_backward(x, w_router, topk_ids, topk_logits, grad_topk_w, perm_src, of
         return (grad_w_router if accumulate else torch.zeros_like(w_router)), grad_x
     if not accumulate:
         grad_w_router = torch.empty_like(w_router)
-    with _on(dev):
-        ws = _scratch(nb, dev, workspace) if nb else None
-        _call("moe_route_backward", _lib.lib().moe_route_backward(
-            cfg, x.data_ptr(), w_router.data_ptr(), topk_ids.data_ptr(), topk_logits.data_ptr(),
-            grad_topk_w.data_ptr(), perm_src.data_ptr(), offsets.data_ptr(), _at(grad_x_add),
-            accumulate, grad_w_router.data_ptr(), _at(grad_x), _at(ws), nb,
-            _stream_of(dev)))
+    ws = _scratch(nb, dev, workspace) if nb else None
+    _launch("moe_route_backward", dev, cfg, x.data_ptr(), w_router.data_ptr(),
+            topk_ids.data_ptr(), topk_logits.data_ptr(), grad_topk_w.data_ptr(),
+            perm_src.data_ptr(), offsets.data_ptr(), _at(grad_x_add), accumulate,
+            grad_w_router.data_ptr(), _at(grad_x), _at(ws), nb)
     return grad_w_router, grad_x
 
 
@@ -265,11 +256,13 @@ class AdamW:
             raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
         if step_count < 0:
             raise ValueError("step_count must not be negative")
+        first = getattr(self.params[0], "device", None)
         for i, p in enumerate(self.params):
             if not isinstance(p, torch.Tensor) or p.dtype not in _DTYPES:
                 raise TypeError(f"params[{i}] must be torch.bfloat16 or torch.float32, got "
                                 f"{getattr(p, 'dtype', type(p))}")
-            _check(p, f"params[{i}]", p.dtype, None, self.params[0].device)
+            if not (p.is_cuda and p.device == first and p.is_contiguous()):
+                _check(p, f"params[{i}]", p.dtype, None, first)
         places = [p.data_ptr() for p in self.params if p.numel()]
         if len(set(places)) < len(places):
             raise ValueError("AdamW: a parameter is listed twice")
@@ -280,7 +273,9 @@ class AdamW:
             self._step_dev = torch.full((1,), step_count, dtype=torch.int64, device=self.device)
         self.state = self._new_state() if state is None else self._taken(state)
         self._list = (MoeAdamwTensor * len(self.params))()
-        self._rows = []  # per parameter: itself, its address, shape, elements and list entry
+        # per parameter: itself, its address, shape, elements, its list entry and
+        # the gradient (address, type) that the entry holds
+        self._rows = []
         st = self.state
         for i, (p, d) in enumerate(zip(self.params, self._list)):
             d.param, d.master = p.data_ptr(), _at(st["master"][i])
@@ -289,9 +284,10 @@ class AdamW:
                 d.m_scale = st["exp_avg_scale"][i].data_ptr()
                 d.v_scale = st["exp_avg_sq_scale"][i].data_ptr()
             d.param_dtype, d.state_bits = _DTYPES[p.dtype], state_bits
-            self._rows.append((p, p.data_ptr(), p.shape, p.numel(), d))
+            self._rows.append((p, p.data_ptr(), p.shape, p.numel(), d, [None]))
         self._opt = MoeAdamw(beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay,
                              step_dev=_at(self._step_dev), seed=seed & 0xFFFFFFFF)
+        self._opt_ref = ctypes.byref(self._opt)
 
     @property
     def step_count(self):
@@ -333,9 +329,11 @@ class AdamW:
                                          "fp32")
                     continue
                 n = (p.numel() + 31) // 32 if scale else p.numel()
+                if (isinstance(t, torch.Tensor) and t.dtype is kinds[k] and t.numel() == n
+                        and t.device == self.device and t.is_contiguous()):
+                    continue
                 _check(t, f"state[{k!r}][{i}]", kinds[k], None, self.device)
-                if t.numel() != n:
-                    raise ValueError(f"state[{k!r}][{i}] must have {n} elements, got {t.numel()}")
+                raise ValueError(f"state[{k!r}][{i}] must have {n} elements, got {t.numel()}")
         return {k: tuple(v) for k, v in state.items()}
 
     def _pointer(self, t, name):
@@ -347,7 +345,7 @@ class AdamW:
 
     def _refuse(self, grads):
         """Raises the error of the first gradient or parameter that is wrong."""
-        for i, ((p, at, shape, _, _), g) in enumerate(zip(self._rows, grads)):
+        for i, ((p, at, shape, *_), g) in enumerate(zip(self._rows, grads)):
             if g is None:
                 continue
             if getattr(g, "dtype", None) not in _DTYPES:
@@ -365,42 +363,46 @@ class AdamW:
         gradient, are numbers or one-element fp32 device tensors."""
         if len(grads) != len(self.params):
             raise ValueError(f"{len(self.params)} gradients expected, got {len(grads)}")
-        dev, opt = self.device, self._opt
-        for (p, at, shape, n, d), g in zip(self._rows, grads):
+        dev, opt, index = self.device, self._opt, self.device.index
+        for (p, at, shape, n, d, held), g in zip(self._rows, grads):
             if g is None:
-                d.n = 0
+                d.n, held[0] = 0, None
                 continue
             try:
                 kind = _DTYPES[g.dtype]
-                good = (g.shape == shape and g.device == dev and g.is_contiguous()
+                good = (g.shape == shape and g.get_device() == index and g.is_contiguous()
                         and p.data_ptr() == at)
             except (AttributeError, KeyError):
                 good = False
             if not good:
                 self._refuse(grads)
-            d.grad, d.grad_dtype, d.n = g.data_ptr(), kind, n
+            entry = (g.data_ptr(), kind)
+            if held[0] != entry:
+                held[0] = entry
+                d.grad, d.grad_dtype, d.n = *entry, n
         if lr is None:
             lr = self.lr
         if isinstance(lr, torch.Tensor):
             opt.lr, opt.lr_dev = 0.0, self._pointer(lr, "lr")
         else:
-            opt.lr, opt.lr_dev = lr, None
+            opt.lr, opt.lr_dev = float(lr), None
         if isinstance(grad_scale, torch.Tensor):
             opt.grad_scale, opt.grad_scale_dev = 1.0, self._pointer(grad_scale, "grad_scale")
         else:
-            opt.grad_scale, opt.grad_scale_dev = grad_scale, None
+            opt.grad_scale, opt.grad_scale_dev = float(grad_scale), None
         opt.step = self._steps + 1
         capturing = torch.cuda.is_current_stream_capturing()
         if capturing and self._step_dev is None:
             raise RuntimeError("AdamW.step under graph capture needs capturable=True")
-        with _on(dev):
-            if self._step_dev is not None:
-                self._step_dev.add_(1)
-            status = _lib.lib().moe_adamw_step(ctypes.byref(opt), self._list, len(self.params),
-                                               _stream_of(dev))
-            if status != _lib.MOE_OK and self._step_dev is not None:
-                self._step_dev.sub_(1)  # refused: no step was made
-            _call("moe_adamw_step", status)
+        counter = self._step_dev
+        if counter is not None:
+            counter.add_(1)
+        try:
+            _launch("moe_adamw_step", dev, self._opt_ref, self._list, len(self._rows))
+        except _lib.MoeError:
+            if counter is not None:
+                counter.sub_(1)  # refused: no step was made
+            raise
         if not capturing:
             self._steps += 1
 

@@ -12,7 +12,9 @@
  * the rows the combine reads.  A failing check records its bit below and the
  * index is clamped into range, so the kernel stays inside its buffers (its
  * results are then meaningless, and the check says why).  Correct inputs
- * produce the same results as the normal build, bit for bit.
+ * produce the same results as the normal build, bit for bit.  The training
+ * calls' kernels check their indices in both builds (a pair, row or expert out
+ * of range is dropped) and record nothing.
  */
 #ifndef BEAM_MOE_DEBUG_H
 #define BEAM_MOE_DEBUG_H

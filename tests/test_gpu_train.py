@@ -324,6 +324,34 @@ def test_route_backward_repeated_and_foreign_ids():
     assert float(gx[11].abs().max()) == 0
 
 
+@pytest.mark.parametrize("T", [60, 700])
+def test_route_backward_drops_what_lies_outside(T):
+    """Offsets outside the rows are cut to them, sorted pairs outside the batch
+    are left out (the kernels check both, so nothing outside is touched)."""
+    say(f"[route_backward] perm_src and offsets outside the batch, T={T}")
+    x, W, ids, z, g, src, off, _ = _router_case(T, 512, 8, T, 0.0, 6)
+    n = T * 8
+    want = gtr.route_backward(x, W, ids, z, g, src, off)
+    cut = off.clone()
+    cut[0], cut[256] = -7, n + 5000
+    for a, b in zip(gtr.route_backward(x, W, ids, z, g, src, cut), want):
+        assert torch.equal(a, b)
+    bad = src.clone()
+    at = [0, 5, n // 2, n - 1]
+    bad[at] = torch.tensor([-1, n, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32, device=DEV)
+    gw, gx = gtr.route_backward(x, W, ids, z, g, bad, off)
+    assert torch.equal(gx, want[1])
+    idn, dz = ids.cpu().numpy(), train.route_dz(n64(z), ids.cpu().numpy(), n64(g), True)
+    ref = train.route_backward(n64(x), n64(W), idn, n64(z), n64(g))[0]
+    for p in src.cpu().numpy()[at]:
+        ref[idn[p // 8, p % 8]] -= dz[p // 8, p % 8] * n64(x)[p // 8]
+    bw, _ = _route_bounds(n64(x), n64(W), idn, n64(z), n64(g), True, n // 256 + 1)
+    within(gw, ref, bw, "grad_w_router")
+    # offsets that run backwards give experts no rows
+    back = torch.flip(off, [0]).contiguous()
+    assert float(gtr.route_backward(x, W, ids, z, g, src, back)[0].abs().max()) == 0
+
+
 @pytest.mark.parametrize("T", [37, 5000])
 def test_route_backward_adds_in_place(T):
     # the C call allows grad_x_add to be grad_x itself
