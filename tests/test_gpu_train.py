@@ -563,7 +563,7 @@ def test_adamw_gradients_that_are_not_finite_stay_alone():
         assert torch.isfinite(m[fine]).all() and not torch.isfinite(m[~fine]).any()
 
 
-def test_adamw_zero_gradients_and_zero_eps():
+def test_adamw_zero_gradients_from_a_zero_state():
     say("[adamw] zero gradients from a zero state")
     for bits in (32, 8):
         p = rows(1, 70, F, 1).view(-1)
