@@ -245,22 +245,39 @@ def _check(t, name, dtype, shape=None, device=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _capturing(device):
+    """Whether a graph is being captured on the current stream of ``device``,
+    whichever device is current."""
+    if device.index == torch.cuda.current_device():
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(device):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class Workspace:
     """A reusable device workspace (a torch uint8 buffer grown on demand).
 
     Calls that share one Workspace must be ordered: issue them on one stream,
-    or synchronise between streams yourself.  Each use records the current
-    stream on the buffer, so a buffer replaced when the workspace grows is
-    not reused by torch's allocator before the work queued on it is done."""
+    or synchronise between streams yourself; that includes the replays of a
+    graph whose capture used it.  Each use records the current stream on the
+    buffer, so a buffer replaced when the workspace grows is not reused by
+    torch's allocator before the work queued on it is done; one that a
+    captured graph writes is kept as long as the Workspace."""
 
     def __init__(self):
         self._buf = None
+        self._captured = False  # a graph holds the address of _buf
+        self._kept = []
 
     def get(self, nbytes: int, device) -> torch.Tensor | None:
         if nbytes == 0:
             return None
         if self._buf is None or self._buf.numel() < nbytes or self._buf.device != device:
+            if self._captured:
+                self._kept.append(self._buf)
             self._buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+            self._captured = False
+        self._captured = self._captured or _capturing(device)
         self._buf.record_stream(torch.cuda.current_stream(device))
         return self._buf
 
@@ -271,7 +288,13 @@ _default_ws: dict = {}
 
 
 def _ws(workspace, device):
+    """The caller's workspace, or the stream's default one.  A captured call
+    gets scratch memory of its graph's own pool instead: graphs captured on one
+    stream may be replayed on several at once, and outlive a default workspace
+    that later grows."""
     if workspace is None:
+        if _capturing(device):
+            return Workspace()
         key = (device, torch.cuda.current_stream(device).cuda_stream)
         workspace = _default_ws.setdefault(key, Workspace())
     return workspace
