@@ -95,6 +95,8 @@ class MoeAdamwTensor(ctypes.Structure):
         ("param_dtype", ctypes.c_int32),
         ("grad_dtype", ctypes.c_int32),
         ("state_bits", ctypes.c_int32),
+        ("step", ctypes.c_int64),
+        ("step_dev", ctypes.c_void_p),
     ]
 
 

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 
 import torch
 
@@ -244,7 +245,12 @@ class AdamW:
     parameters).  Pass one in, with ``step_count``, to continue from a
     checkpoint; its tensors are used, not copied.
 
-    ``capturable`` keeps the step number on the device, so that a captured
+    A parameter without a gradient makes no step, and its bias correction goes
+    by the steps that it has made itself.  ``step_counts`` has them, one per
+    parameter, and belongs into a checkpoint: ``step_count`` takes such a list,
+    or one number for all.
+
+    ``capturable`` keeps the step numbers on the device, so that a captured
     step counts on in each replay."""
 
     def __init__(self, params, *, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2,
@@ -254,7 +260,14 @@ class AdamW:
             raise ValueError("AdamW: no parameters")
         if state_bits not in (8, 32):
             raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
-        if step_count < 0:
+        try:
+            counts = [operator.index(step_count)] * len(self.params)
+        except TypeError:
+            counts = [operator.index(c) for c in step_count]
+        if len(counts) != len(self.params):
+            raise ValueError(f"one step count per parameter ({len(self.params)}) expected, got "
+                             f"{len(counts)}")
+        if min(counts) < 0:
             raise ValueError("step_count must not be negative")
         first = getattr(self.params[0], "device", None)
         for i, p in enumerate(self.params):
@@ -268,13 +281,18 @@ class AdamW:
             raise ValueError("AdamW: a parameter is listed twice")
         self.device = self.params[0].device
         self.lr, self.state_bits = lr, state_bits
-        self._steps, self._step_dev = step_count, None
+        # steps of the list, and by how many those of a parameter are fewer; on
+        # the device the list's number, then every parameter's
+        self._steps, self._step_dev = max(counts), None
+        self._missed = {i: self._steps - c for i, c in enumerate(counts) if c < self._steps}
         if capturable:
-            self._step_dev = torch.full((1,), step_count, dtype=torch.int64, device=self.device)
+            self._step_dev = torch.tensor([self._steps, *counts], dtype=torch.int64,
+                                          device=self.device)
+            self._counters = self._step_dev.split(1)
         self.state = self._new_state() if state is None else self._taken(state)
         self._list = (MoeAdamwTensor * len(self.params))()
-        # per parameter: itself, its address, shape, elements, its list entry and
-        # the gradient (address, type) that the entry holds
+        # per parameter: itself, its address, shape, elements, its list entry,
+        # the gradient (address, type) that the entry holds, its place
         self._rows = []
         st = self.state
         for i, (p, d) in enumerate(zip(self.params, self._list)):
@@ -284,15 +302,33 @@ class AdamW:
                 d.m_scale = st["exp_avg_scale"][i].data_ptr()
                 d.v_scale = st["exp_avg_sq_scale"][i].data_ptr()
             d.param_dtype, d.state_bits = _DTYPES[p.dtype], state_bits
-            self._rows.append((p, p.data_ptr(), p.shape, p.numel(), d, [None]))
+            if capturable:
+                d.step_dev = self._step_dev.data_ptr() + 8 * (i + 1)
+            self._rows.append((p, p.data_ptr(), p.shape, p.numel(), d, [None], i))
         self._opt = MoeAdamw(beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay,
-                             step_dev=_at(self._step_dev), seed=seed & 0xFFFFFFFF)
+                             seed=seed & 0xFFFFFFFF)
         self._opt_ref = ctypes.byref(self._opt)
 
     @property
     def step_count(self):
         """Steps made so far (with capturable read from the device)."""
-        return self._steps if self._step_dev is None else int(self._step_dev)
+        return self._steps if self._step_dev is None else int(self._step_dev[0])
+
+    @property
+    def step_counts(self):
+        """The steps that each parameter has made: those with a gradient."""
+        if self._step_dev is not None:
+            return self._step_dev[1:].tolist()
+        return [self._steps - self._missed.get(i, 0) for i in range(len(self.params))]
+
+    def _count(self, absent, by):
+        """Adds `by` to the device's step numbers, but for the parameters at the
+        places in `absent`."""
+        if not absent:
+            self._step_dev.add_(by)
+        else:
+            skip = {i + 1 for i in absent}
+            torch._foreach_add_([c for i, c in enumerate(self._counters) if i not in skip], by)
 
     def _kinds(self):
         """The state's lists and their element types."""
@@ -358,15 +394,17 @@ class AdamW:
 
     def step(self, grads, *, lr=None, grad_scale=1.0):
         """One step.  grads: one tensor (bf16 or fp32, the parameter's shape)
-        per parameter, or None to leave that parameter and its state alone.
+        per parameter, or None to leave that parameter, its state and its step
+        number alone.
         lr (default: the constructor's) and grad_scale, a factor on every
         gradient, are numbers or one-element fp32 device tensors."""
         if len(grads) != len(self.params):
             raise ValueError(f"{len(self.params)} gradients expected, got {len(grads)}")
-        dev, opt, index = self.device, self._opt, self.device.index
-        for (p, at, shape, n, d, held), g in zip(self._rows, grads):
+        dev, opt, index, absent = self.device, self._opt, self.device.index, []
+        for (p, at, shape, n, d, held, place), g in zip(self._rows, grads):
             if g is None:
                 d.n, held[0] = 0, None
+                absent.append(place)
                 continue
             try:
                 kind = _DTYPES[g.dtype]
@@ -394,17 +432,23 @@ class AdamW:
         capturing = torch.cuda.is_current_stream_capturing()
         if capturing and self._step_dev is None:
             raise RuntimeError("AdamW.step under graph capture needs capturable=True")
-        counter = self._step_dev
-        if counter is not None:
-            counter.add_(1)
+        counted = self._step_dev is not None
+        if counted:
+            self._count(absent, 1)
+        else:
+            for i, fewer in self._missed.items():
+                self._list[i].step = opt.step - fewer
         try:
             _launch("moe_adamw_step", dev, self._opt_ref, self._list, len(self._rows))
         except _lib.MoeError:
-            if counter is not None:
-                counter.sub_(1)  # refused: no step was made
+            if counted:
+                self._count(absent, -1)  # refused: no step was made
             raise
         if not capturing:
             self._steps += 1
+            if not counted:
+                for i in absent:
+                    self._missed[i] = self._missed.get(i, 0) + 1
 
 
 # ---------------------------------------------------------------------------

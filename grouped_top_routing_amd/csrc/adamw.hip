@@ -4,7 +4,9 @@
 //   m = b1 m + (1 - b1) g',  v = b2 v + (1 - b2) g'^2
 //   p = p - lr wd p - lr / (1 - b1^t) * m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 // in fp32.  p is the parameter (fp32), or the fp32 master of a bf16 one, which
-// is then rounded to nearest into the parameter.
+// is then rounded to nearest into the parameter.  t is the tensor's own: one
+// that gets a gradient now and then has made fewer steps than its list, and its
+// moments are corrected for those.
 //
 // States in 8 bits: blocks of 32 consecutive elements, an E4M3 code per element
 // and one E8M0 scale (a power of two, so scaling is exact) per block.  Kept are
@@ -256,10 +258,12 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a) {
   }
   const AdamTensor& t = a.tensor[lo];
   AdamFactors k = a.factors;
-  int64_t step = a.step;
-  if (a.step_dev || a.lr_dev || a.grad_scale_dev) {
+  k.rate = t.rate;
+  k.root = t.root;
+  const bool counted = t.kind & 8;
+  const int64_t step = counted ? *t.step_dev : t.step;
+  if (counted || a.lr_dev || a.grad_scale_dev) {
     __shared__ AdamFactors shared;
-    if (a.step_dev) step = *a.step_dev;
     if (threadIdx.x == 0)
       shared = factors_of(a, step, a.lr_dev ? (double)*a.lr_dev : a.lr,
                           (float)a.grad_scale * (a.grad_scale_dev ? *a.grad_scale_dev : 1.f));
@@ -271,7 +275,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a) {
   const int64_t i = ((int64_t)blockIdx.x - a.first[lo]) * kSpan + threadIdx.x * kPer;
   const int64_t left = t.n - i;
   const int n = left >= kPer ? kPer : left > 0 ? (int)left : 0;
-  switch (t.kind) {
+  switch (t.kind & 7) {
     case 0: update8<false, false, false>(t, k, key, i, n); break;
     case 1: update8<true, false, false>(t, k, key, i, n); break;
     case 2: update8<false, true, false>(t, k, key, i, n); break;
@@ -288,8 +292,16 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a) {
 int64_t adamw_blocks(int64_t n) { return (n + kSpan - 1) / kSpan; }
 
 void adamw_factors(AdamArgs& a) {
-  // without device scalars all factors are known here
-  if (!a.step_dev) a.factors = factors_of(a, a.step, a.lr, (float)a.grad_scale);
+  // of the tensors whose step is known here; most lists have one step
+  int64_t last = 0;
+  for (int i = 0; i < a.count; ++i) {
+    AdamTensor& t = a.tensor[i];
+    if (t.kind & 8) continue;
+    if (t.step != last) a.factors = factors_of(a, t.step, a.lr, (float)a.grad_scale);
+    last = t.step;
+    t.rate = a.factors.rate;
+    t.root = a.factors.root;
+  }
 }
 
 hipError_t launch_adamw(const AdamArgs& a, int64_t blocks, hipStream_t stream) {

@@ -41,6 +41,7 @@ bool tensor_ok(const moe_adamw_tensor_t& t) {
   if (t.param_dtype != MOE_DTYPE_BF16 && t.param_dtype != MOE_DTYPE_FP32) return false;
   if (t.grad_dtype != MOE_DTYPE_BF16 && t.grad_dtype != MOE_DTYPE_FP32) return false;
   if (t.state_bits != 32 && t.state_bits != 8) return false;
+  if (t.step < 0 || (reinterpret_cast<uintptr_t>(t.step_dev) & 7u)) return false;
   if (t.n == 0) return true;
   if (!t.param || !t.grad || !t.m || !t.v) return false;
   if ((t.param_dtype == MOE_DTYPE_BF16) != (t.master != nullptr)) return false;
@@ -172,12 +173,9 @@ int moe_adamw_step(const moe_adamw_t* opt, const moe_adamw_tensor_t* tensors, in
   a.eps = opt->eps;
   a.weight_decay = opt->weight_decay;
   a.grad_scale = opt->grad_scale;
-  a.step = opt->step;
-  a.step_dev = opt->step_dev;
   a.lr_dev = opt->lr_dev;
   a.grad_scale_dev = opt->grad_scale_dev;
   a.seed = opt->seed;
-  adamw_factors(a);
   // a launch ends where its list is full or its grid nears 2^32 threads (a
   // tensor of 2^34 elements alone stays below that)
   constexpr int64_t kMostBlocks = (int64_t)1 << 23;
@@ -186,6 +184,7 @@ int moe_adamw_step(const moe_adamw_t* opt, const moe_adamw_tensor_t* tensors, in
     const int64_t mine = i < num_tensors ? adamw_blocks(tensors[i].n) : 0;
     if (a.count > 0 &&
         (i == num_tensors || a.count == kAdamTensors || blocks + mine > kMostBlocks)) {
+      adamw_factors(a);
       if ((st = hip_status(launch_adamw(a, blocks, static_cast<hipStream_t>(stream))))) return st;
       a.count = 0;
       blocks = 0;
@@ -203,6 +202,12 @@ int moe_adamw_step(const moe_adamw_t* opt, const moe_adamw_tensor_t* tensors, in
     d.n = t.n;
     d.kind = (t.param_dtype == MOE_DTYPE_FP32 ? 1 : 0) | (t.grad_dtype == MOE_DTYPE_FP32 ? 2 : 0) |
              (t.state_bits == 32 ? 4 : 0);
+    if (const int64_t* counter = t.step_dev ? t.step_dev : t.step > 0 ? nullptr : opt->step_dev) {
+      d.step_dev = counter;
+      d.kind |= 8;
+    } else {
+      d.step = t.step > 0 ? t.step : opt->step;
+    }
     d.place = i;
     a.first[a.count++] = blocks;
     blocks += mine;

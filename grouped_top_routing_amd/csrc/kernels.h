@@ -140,8 +140,13 @@ struct AdamTensor {
   uint8_t* m_scale;
   uint8_t* v_scale;
   int64_t n;
+  union {
+    int64_t step;             // its t
+    const int64_t* step_dev;  // or where the kernel reads it (kind bit 3)
+  };
+  float rate, root;  // of t (AdamFactors), in steps without device scalars
   int32_t kind;  // bit 0: fp32 parameter (else bf16 with a master); bit 1: fp32 gradient;
-                 // bit 2: 32-bit states
+                 // bit 2: 32-bit states; bit 3: t on the device
   int32_t place; // in the caller's list
 };
 // The factors of one step: keep = 1 - lr wd, rate = lr / (1 - b1^t),
@@ -152,10 +157,8 @@ struct AdamFactors {
 struct AdamArgs {
   AdamTensor tensor[kAdamTensors];
   int64_t first[kAdamTensors];  // first workgroup of each tensor
-  AdamFactors factors;          // of steps without device scalars
+  AdamFactors factors;          // of steps without device scalars; rate and root per tensor
   double lr, beta1, beta2, eps, weight_decay, grad_scale;
-  int64_t step;
-  const int64_t* step_dev;
   const float* lr_dev;
   const float* grad_scale_dev;
   uint32_t seed;
@@ -163,7 +166,7 @@ struct AdamArgs {
 };
 static_assert(sizeof(AdamArgs) <= 4096, "kernel arguments hold 4 KB");
 int64_t adamw_blocks(int64_t n);
-void adamw_factors(AdamArgs& a);
+void adamw_factors(AdamArgs& a);  // of a launch's tensors
 hipError_t launch_adamw(const AdamArgs& a, int64_t blocks, hipStream_t stream);
 
 }  // namespace beam

@@ -427,7 +427,8 @@ int moe_route_backward(const moe_config_t* cfg, const uint16_t* x, const float* 
 
 /*
  * One AdamW step (decoupled weight decay) over a list of tensors.  With
- * g = grad_scale * grad and t the step:
+ * g = grad_scale * grad and t the step of the tensor (its own where it has one,
+ * the list's otherwise; the moments are corrected for the steps they hold):
  *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
  *   p = p - lr weight_decay p - lr / (1 - beta1^t) m / (sqrt(v / (1 - beta2^t)) + eps)
  * in fp32, p being the parameter, or the fp32 master of a bf16 one (which is
@@ -459,12 +460,17 @@ typedef struct moe_adamw_tensor {
   int32_t param_dtype; /* moe_dtype                                            */
   int32_t grad_dtype;  /* moe_dtype                                            */
   int32_t state_bits;  /* 32 or 8                                              */
+  /* The tensor's own t, where it has made fewer steps than the list (one whose
+   * gradient came late, or comes now and then): step_dev, read when the step
+   * runs, or else step; NULL and 0 stand for the list's. */
+  int64_t step;
+  const int64_t* step_dev;
 } moe_adamw_tensor_t;
 
 typedef struct moe_adamw {
   double lr, beta1, beta2, eps, weight_decay; /* betas in [0, 1), the others >= 0 */
   double grad_scale;           /* factor on every gradient (clipping, loss scaling) */
-  int64_t step;                /* t >= 1 of this step                          */
+  int64_t step;                /* t >= 1 of this step, for tensors without their own */
   /* Device scalars for steps replayed from a captured graph, each NULL or read
    * when the step runs: the step number in place of `step` (>= 1), the rate in
    * place of `lr`, and a further factor on the gradients. */

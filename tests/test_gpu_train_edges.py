@@ -110,3 +110,157 @@ def test_a_captured_workspace_outlives_its_growth():
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert all(torch.equal(a, b) for a, b in zip(gtr.route(big, W, workspace=ws), want_big))
     assert all(torch.equal(a, b) for a, b in zip(got_big, want_big))
+
+
+# ---------------------------------------------------------------------------
+# AdamW counts the steps of each tensor
+LATE_SIZES = (1000, 70, 33, 2049)
+
+
+def _late_grads(step, dt):
+    """Gradients of step 1, 2, ...: always; from the fifth; odd ones; never."""
+    on = (True, step >= 5, step % 2 == 1, False)
+    return [rows(1, n, dt, 10 * step + i).view(-1) * 0.1 if yes else None
+            for i, (n, yes) in enumerate(zip(LATE_SIZES, on))]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("capturable", [False, True])
+@pytest.mark.parametrize("dt", [F, BF], ids=NAMES.get)
+def test_adamw_counts_the_steps_of_each_tensor(bits, capturable, dt):
+    """A tensor without a gradient makes no step: its bias correction (and the
+    rounding of its 8-bit states) goes by the steps it has made."""
+    say(f"[adamw] late and rare gradients, {bits} bits, capturable={capturable}, {dt}")
+    params = [rows(1, n, dt, i).view(-1) for i, n in enumerate(LATE_SIZES)]
+    never = params[3].clone()
+    opt = _opt(params, state_bits=bits, seed=11, capturable=capturable)
+    made = [0] * 4
+
+    def state(i):
+        st = opt.state
+        p = n64(st["master"][i] if dt == BF else params[i])
+        if bits == 32:
+            return p, n64(st["exp_avg"][i]), n64(st["exp_avg_sq"][i])
+        m, r = (train.decode_8bit(st[k][i].view(torch.uint8).cpu().numpy(),
+                                  st[k + "_scale"][i].view(torch.uint8).cpu().numpy())
+                for k in ("exp_avg", "exp_avg_sq"))
+        return p, m, r * r
+
+    for step in range(1, 9):
+        grads = _late_grads(step, dt)
+        before = [state(i) for i in range(4)]
+        opt.step(grads)
+        for i, g in enumerate(grads):
+            if g is None:
+                assert all(np.array_equal(a, b) for a, b in zip(state(i), before[i]))
+                continue
+            made[i] += 1
+            p0, m0, v0 = before[i]
+            ref = train.adamw(p0, n64(g), m0, v0, step=made[i], **HP)
+            bounds = _adam_bounds(p0, n64(g), m0, v0, made[i], 1.0)
+            got = state(i)
+            within(got[0], ref[0], bounds[0], f"step {step} tensor {i}")
+            if bits == 32:
+                within(got[1], ref[1], bounds[1], "m")
+                within(got[2], ref[2], bounds[2], "v")
+                continue
+            f32 = np.float32
+            root = np.sqrt(v0)  # exact: codes and scales are short
+            m, _, root = train.adamw_state_f32(n64(g), m0, f32(root) * f32(root),
+                                               beta1=HP["beta1"], beta2=HP["beta2"])
+            random = train.rounding_bits(11, made[i], i, len(p0))
+            for k, x, b, low in (("exp_avg", m, random & np.uint64(0xFFFF), False),
+                                 ("exp_avg_sq", root, random >> np.uint64(16), True)):
+                code, scale = train.encode_8bit(x, b, low)
+                raw = opt.state[k][i].view(torch.uint8).cpu().numpy()
+                assert np.array_equal(train.decode_8bit(raw, scale),
+                                      train.decode_8bit(code, scale)), (step, i, k)
+    assert torch.equal(params[3], never)
+    assert opt.step_count == 8
+    assert list(opt.step_counts) == made == [8, 4, 4, 0]
+
+
+def test_adamw_first_update_of_a_late_tensor_is_the_rate():
+    # from zero states the first update is lr sign(g), whatever the others did
+    say("[adamw] a first gradient after 500 steps of the others")
+    p, q = torch.zeros(64, device=DEV), torch.zeros(64, device=DEV)
+    g = torch.ones(64, device=DEV)
+    opt = gtr.AdamW([p, q], lr=1e-3, weight_decay=0.0)
+    for _ in range(500):
+        opt.step([g, None])
+    opt.step([None, g])
+    # m / (1 - b1) and sqrt(v / (1 - b2)) are 1 within a few roundings; eps is 1e-8
+    within(q, np.full(64, -1e-3), 1e-3 * (16 * U + 1e-8) * np.ones(64), "first update")
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("capturable", [False, True])
+def test_adamw_step_counts_continue_from_a_checkpoint(bits, capturable):
+    say(f"[adamw] step_count as a list, {bits} bits, capturable={capturable}")
+    a_params = [rows(1, n, BF, i).view(-1) for i, n in enumerate(LATE_SIZES)]
+    a = _opt(a_params, state_bits=bits, seed=2, capturable=capturable)
+    for step in range(1, 6):
+        a.step(_late_grads(step, BF))
+    counts = a.step_counts
+    assert list(counts) == [5, 1, 3, 0]
+    state = {k: [None if t is None else t.clone() for t in v] for k, v in a.state.items()}
+    b_params = [t.clone() for t in a_params]
+    b = _opt(b_params, state_bits=bits, seed=2, state=state, step_count=counts,
+             capturable=not capturable)
+    assert list(b.step_counts) == [5, 1, 3, 0] and b.step_count == 5
+    for step in range(6, 9):
+        a.step(_late_grads(step, BF))
+        b.step(_late_grads(step, BF))
+    for x, y in zip(a_params, b_params):
+        assert torch.equal(x, y)
+    for k in state:
+        for x, y in zip(a.state[k], state[k]):
+            assert torch.equal(x.float(), y.float())
+    assert list(a.step_counts) == list(b.step_counts) == [8, 4, 4, 0]
+
+
+def test_adamw_captured_step_without_some_gradients_counts_on():
+    say("[adamw] a captured step of some of the tensors, replayed among eager ones")
+    def made():
+        return [rows(1, n, F, i).view(-1) for i, n in enumerate(LATE_SIZES)]
+    for bits in (32, 8):
+        pc, pe = made(), made()
+        oc = _opt(pc, state_bits=bits, seed=4, capturable=True)
+        oe = _opt(pe, state_bits=bits, seed=4)
+        every = [rows(1, n, F, 50 + i).view(-1) for i, n in enumerate(LATE_SIZES)]
+        some = [g if i % 2 else None for i, g in enumerate(every)]
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            oc.step(some)
+        assert list(oc.step_counts) == [0] * 4
+        for i in range(4):
+            graph.replay()
+            oe.step(some)
+            torch.cuda.synchronize()
+            for a, b in zip(pc, pe):
+                assert torch.equal(a, b), (bits, i)
+            oc.step(every)
+            oe.step(every)
+            for a, b in zip(pc, pe):
+                assert torch.equal(a, b), (bits, i)
+        assert list(oc.step_counts) == list(oe.step_counts) == [4, 8, 4, 8]
+        assert oc.step_count == oe.step_count == 8
+
+
+def test_adamw_refuses_wrong_step_counts_and_keeps_its_own():
+    p, q = torch.zeros(64, device=DEV), torch.zeros(64, device=DEV)
+    for bad, what in (([1], "one step count per parameter"), ([1, 2, 3], "one step count per"),
+                      ([1, -1], "negative")):
+        with pytest.raises(ValueError, match=what):
+            gtr.AdamW([p, q], step_count=bad)
+    g = torch.ones(64, device=DEV)
+    for capturable in (False, True):
+        opt = gtr.AdamW([p, q], capturable=capturable)
+        opt.step([g, None])
+        for bad in (dict(lr=-1.0), dict(grad_scale=float("nan"))):
+            with pytest.raises(gtr.MoeError):
+                opt.step([g, None], **bad)
+            with pytest.raises(gtr.MoeError):
+                opt.step([g, g], **bad)
+        assert list(opt.step_counts) == [1, 0] and opt.step_count == 1
