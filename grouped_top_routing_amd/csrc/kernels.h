@@ -162,7 +162,8 @@ struct AdamArgs {
   const float* lr_dev;
   const float* grad_scale_dev;
   uint32_t seed;
-  int32_t count;  // tensors of this launch
+  int32_t count;   // tensors of this launch
+  int32_t device;  // whether any device scalar is read (steps, lr, grad_scale)
 };
 static_assert(sizeof(AdamArgs) <= 4096, "kernel arguments hold 4 KB");
 int64_t adamw_blocks(int64_t n);
