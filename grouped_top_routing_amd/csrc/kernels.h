@@ -149,10 +149,10 @@ struct AdamTensor {
                  // bit 2: 32-bit states; bit 3: t on the device
   int32_t place; // in the caller's list
 };
-// The factors of one step: keep = 1 - lr wd, rate = lr / (1 - b1^t),
-// root = 1 / sqrt(1 - b2^t), gs the gradients' factor.
+// The factors of one step: keep - decay = 1 - lr wd (one of the two carries it),
+// rate = lr / (1 - b1^t), root = 1 / sqrt(1 - b2^t), gs the gradients' factor.
 struct AdamFactors {
-  float b1, b2, omb1, omb2, eps, keep, rate, root, gs;
+  float b1, b2, omb1, omb2, eps, keep, decay, rate, root, gs;
 };
 struct AdamArgs {
   AdamTensor tensor[kAdamTensors];

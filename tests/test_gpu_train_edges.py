@@ -264,3 +264,63 @@ def test_adamw_refuses_wrong_step_counts_and_keeps_its_own():
             with pytest.raises(gtr.MoeError):
                 opt.step([g, g], **bad)
         assert list(opt.step_counts) == [1, 0] and opt.step_count == 1
+
+
+# ---------------------------------------------------------------------------
+# AdamW: decay far below a rounding of the parameter
+@pytest.mark.parametrize("lr,wd", [(2e-5, 0.01), (2e-6, 0.01), (1e-4, 0.1), (3e-3, 0.1), (1e-5, 0.0)])
+@pytest.mark.parametrize("dt", [F, BF], ids=NAMES.get)
+@pytest.mark.parametrize("device_rate", [False, True])
+def test_adamw_decay_keeps_its_mean(lr, wd, dt, device_rate):
+    """p - lr wd p - ... with lr wd down to 2e-8 (a rounding of p is 6e-8): an
+    element cannot show it, the mean over many, whose updates differ, does.
+
+    An element's error is at most e = U |p'| (its one rounding, of either sign)
+    + 16 U |update| (of a sign independent of p's), except for decay's own
+    factor, product and sum, 3 U lr wd |p|; where lr wd is 2^-12 and more, the
+    product with 1 - lr wd adds a rounding of either sign and that factor's own
+    error (U / 2) |p|.  By Hoeffding the signed sum of the errors of either
+    sign passes 6 sqrt(sum e^2) with a probability of 3e-8."""
+    say(f"[adamw] decay lr={lr} wd={wd} {dt} device_rate={device_rate}")
+    n = 1 << 20
+    g = torch.Generator(device=DEV).manual_seed(7)
+    p32 = (torch.rand(n, generator=g, device=DEV) + 0.5) * torch.where(
+        torch.rand(n, generator=g, device=DEV) < 0.5, -1.0, 1.0)
+    grad = torch.randn(n, generator=g, device=DEV)
+    m, root = torch.randn(n, generator=g, device=DEV), torch.rand(n, generator=g, device=DEV) + 0.5
+    p = p32.clone() if dt == F else p32.to(BF)
+    state = {"exp_avg": [m.clone()], "exp_avg_sq": [root * root],
+             "master": [None if dt == F else p32.clone()]}
+    opt = gtr.AdamW([p], lr=lr, weight_decay=wd, state=state, step_count=99)
+    start = p32.double()
+    v0 = (root * root).double()
+    rate = torch.full((1,), lr, device=DEV) if device_rate else lr
+    lr = float(rate) if device_rate else lr
+    opt.step([grad], lr=rate)
+    got = (p if dt == F else opt.state["master"][0]).double()
+    b1, b2, eps = 0.9, 0.999, 1e-8
+    m1 = b1 * m.double() + (1 - b1) * grad.double()
+    v1 = b2 * v0 + (1 - b2) * grad.double() ** 2
+    upd = lr * (m1 / (1 - b1 ** 100)) / ((v1 / (1 - b2 ** 100)).sqrt() + eps)
+    want = start - lr * wd * start - upd
+    err = got - want
+    large = lr * wd >= 2.0 ** -12
+    e = (2 if large else 1) * U * got.abs() + 16 * U * upd.abs()
+    factor = lr * wd * 3 * U + (U / 2 if large else 0.0)
+    assert bool((err.abs() <= 1.01 * (e + factor * start.abs())).all())
+    signed = abs(float((err * start.sign()).sum()))
+    allowed = 6 * float((e * e).sum().sqrt()) + factor * float(start.abs().sum())
+    whole = lr * wd * float(start.abs().sum())
+    say(f"  signed error {signed:.3e}, allowed {allowed:.3e}, decay {whole:.3e}")
+    assert signed <= allowed
+
+
+def test_adamw_infinite_parameters_stay_so():
+    say("[adamw] infinite parameters under decay")
+    for wd in (0.0, 1e-3, 0.5):
+        for bits in (32, 8):
+            p = torch.tensor([float("inf"), -float("inf"), 1.0, float("nan")], device=DEV)
+            gtr.AdamW([p], lr=1e-2, weight_decay=wd, state_bits=bits).step(
+                [torch.tensor([1.0, 1.0, 1.0, 1.0], device=DEV)])
+            assert torch.isposinf(p[0]) and torch.isneginf(p[1]) and torch.isnan(p[3])
+            assert torch.isfinite(p[2])
