@@ -338,7 +338,7 @@ class AdamW:
                 "exp_avg_scale": torch.float8_e8m0fnu, "exp_avg_sq_scale": torch.float8_e8m0fnu}
 
     def _new_state(self):
-        state = {"master": tuple(p.float() if p.dtype == torch.bfloat16 else None
+        state = {"master": tuple(p.detach().float() if p.dtype == torch.bfloat16 else None
                                  for p in self.params)}
         for k, dt in self._kinds().items():
             state[k] = tuple(

@@ -324,3 +324,20 @@ def test_adamw_infinite_parameters_stay_so():
                 [torch.tensor([1.0, 1.0, 1.0, 1.0], device=DEV)])
             assert torch.isposinf(p[0]) and torch.isneginf(p[1]) and torch.isnan(p[3])
             assert torch.isfinite(p[2])
+
+
+# ---------------------------------------------------------------------------
+# AdamW beside autograd
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_state_of_parameters_that_require_grad(bits):
+    say(f"[adamw] nn.Parameter, {bits} bits")
+    params = [torch.nn.Parameter(rows(1, 100, dt, 1).view(-1)) for dt in (BF, F)]
+    opt = _opt(params, state_bits=bits)
+    for k, v in opt.state.items():
+        assert all(t is None or (not t.requires_grad and t.grad_fn is None) for t in v), k
+    saved = copy.deepcopy(opt.state)
+    assert torch.equal(saved["master"][0], params[0].detach().float())
+    grads = [rows(1, 100, p.dtype, 2).view(-1) for p in params]
+    opt.step(grads)
+    assert torch.equal(params[0].detach(), opt.state["master"][0].to(BF))
+    assert not torch.equal(saved["master"][0], opt.state["master"][0])
