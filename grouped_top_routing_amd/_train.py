@@ -305,6 +305,8 @@ class AdamW:
             if capturable:
                 d.step_dev = self._step_dev.data_ptr() + 8 * (i + 1)
             self._rows.append((p, p.data_ptr(), p.shape, p.numel(), d, [None], i))
+        # places of the parameters that autograd may have saved for a backward pass
+        self._saved = [i for i, p in enumerate(self.params) if p.requires_grad]
         self._opt = MoeAdamw(beta1=betas[0], beta2=betas[1], eps=eps, weight_decay=weight_decay,
                              seed=seed & 0xFFFFFFFF)
         self._opt_ref = ctypes.byref(self._opt)
@@ -449,6 +451,10 @@ class AdamW:
             if not counted:
                 for i in absent:
                     self._missed[i] = self._missed.get(i, 0) + 1
+        if self._saved:  # changed in place: a backward pass that needs the old values fails
+            still = set(absent)
+            torch.autograd.graph.increment_version(
+                [self.params[i] for i in self._saved if i not in still])
 
 
 # ---------------------------------------------------------------------------

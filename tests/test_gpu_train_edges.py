@@ -341,3 +341,17 @@ def test_adamw_state_of_parameters_that_require_grad(bits):
     opt.step(grads)
     assert torch.equal(params[0].detach(), opt.state["master"][0].to(BF))
     assert not torch.equal(saved["master"][0], opt.state["master"][0])
+
+
+def test_adamw_tells_autograd_that_parameters_changed():
+    say("[adamw] a backward pass through parameters that a step has changed since")
+    for dt in (F, BF):
+        p = torch.nn.Parameter(rows(1, 64, dt, 3).view(-1))
+        q = torch.nn.Parameter(rows(1, 64, dt, 4).view(-1))
+        opt = _opt([p, q])
+        loss_p, loss_q = (p * p).sum(), (q * q).sum()
+        opt.step([torch.ones(64, dtype=dt, device=DEV), None])
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss_p.backward()
+        loss_q.backward()  # q had no gradient and stayed
+        assert torch.equal(q.grad, 2 * q.detach())
