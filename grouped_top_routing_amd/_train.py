@@ -290,6 +290,7 @@ class AdamW:
                                           device=self.device)
             self._counters = self._step_dev.split(1)
         self.state = self._new_state() if state is None else self._taken(state)
+        self._refuse_overlaps()
         self._list = (MoeAdamwTensor * len(self.params))()
         # per parameter: itself, its address, shape, elements, its list entry,
         # the gradient (address, type) that the entry holds, its place
@@ -373,6 +374,17 @@ class AdamW:
                 _check(t, f"state[{k!r}][{i}]", kinds[k], None, self.device)
                 raise ValueError(f"state[{k!r}][{i}] must have {n} elements, got {t.numel()}")
         return {k: tuple(v) for k, v in state.items()}
+
+    def _refuse_overlaps(self):
+        """Parameters and states are each written by one workgroup alone: no two
+        may share memory."""
+        spans = [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), name, i)
+                 for name, ts in (("params", self.params), *self.state.items())
+                 for i, t in enumerate(ts) if t is not None and t.numel()]
+        spans.sort()
+        for (_, end, name, i), (start, _, other, j) in zip(spans, spans[1:]):
+            if start < end:
+                raise ValueError(f"AdamW: {name}[{i}] and {other}[{j}] overlap in memory")
 
     def _pointer(self, t, name):
         """Device address of a one-element fp32 tensor."""

@@ -355,3 +355,28 @@ def test_adamw_tells_autograd_that_parameters_changed():
             loss_p.backward()
         loss_q.backward()  # q had no gradient and stayed
         assert torch.equal(q.grad, 2 * q.detach())
+
+
+def test_adamw_refuses_memory_that_overlaps():
+    say("[adamw] parameters and states that share memory")
+    b = torch.zeros(256, device=DEV)
+    for params in ([b[:64], b[32:96]], [b, b[128:192]], [b[128:192], b[64:200]],
+                   [b[:64], b.view(BF)[64:72]]):
+        with pytest.raises(ValueError, match="overlap"):
+            gtr.AdamW(params)
+    gtr.AdamW([b[:64], b[64:128], b[128:128], b[128:]])  # side by side
+    p, m, v = torch.zeros(64, device=DEV), torch.zeros(64, device=DEV), torch.zeros(64, device=DEV)
+    for state in ({"exp_avg": [m], "exp_avg_sq": [m]}, {"exp_avg": [p], "exp_avg_sq": [v]}):
+        with pytest.raises(ValueError, match="overlap"):
+            gtr.AdamW([p], state=state)
+    gtr.AdamW([p], state={"exp_avg": [m], "exp_avg_sq": [v]})
+    low = torch.zeros(64, dtype=BF, device=DEV)
+    codes = torch.zeros(128, dtype=torch.uint8, device=DEV)
+    f8, e8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+    state = {"master": [p], "exp_avg": [codes[:64].view(f8)], "exp_avg_sq": [codes[64:].view(f8)],
+             "exp_avg_scale": [torch.zeros(2, dtype=torch.uint8, device=DEV).view(e8)],
+             "exp_avg_sq_scale": [torch.zeros(2, dtype=torch.uint8, device=DEV).view(e8)]}
+    gtr.AdamW([low], state=state, state_bits=8)
+    state["exp_avg_sq_scale"] = [codes[126:].view(e8)]
+    with pytest.raises(ValueError, match="overlap"):
+        gtr.AdamW([low], state=state, state_bits=8)
