@@ -3,6 +3,7 @@
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
+#include <initializer_list>
 
 #include "../../include/beam_moe.h"
 #include "capi_common.h"
@@ -33,6 +34,37 @@ int validate_rows(const moe_config_t* c, int dtype) {
   return MOE_OK;
 }
 
+// Whether no output overlaps an input or another output (null: not given).
+// The kernels read and write them in no order.
+struct Span {
+  const void* at;
+  int64_t bytes;
+  bool meets(const Span& o) const {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(at), b = reinterpret_cast<uintptr_t>(o.at);
+    return at && o.at && (a < b ? b - a < (uint64_t)bytes : a - b < (uint64_t)o.bytes);
+  }
+};
+bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (o->meets(i)) return false;
+    for (const Span* p = outs.begin(); p != o; ++p)
+      if (o->meets(*p)) return false;
+  }
+  return true;
+}
+
+// Bytes of the row calls' arguments.
+struct RowBytes {
+  int64_t token_rows, sorted_rows, pairs;
+  RowBytes(const moe_config_t* c, int dtype) {
+    const int64_t row = (int64_t)c->hidden * (dtype == MOE_DTYPE_FP32 ? 4 : 2);
+    token_rows = c->num_tokens * row;
+    sorted_rows = beam::pairs(c) * row;
+    pairs = beam::pairs(c) * 4;
+  }
+};
+
 bool rate_ok(double v) { return std::isfinite(v) && v >= 0.0; }
 bool beta_ok(double v) { return v >= 0.0 && v < 1.0; }
 
@@ -62,6 +94,10 @@ int moe_dispatch(const moe_config_t* cfg, int dtype, const void* x, const int32_
   if (!aligned16(x) || !aligned16(x_perm) || !aligned4(perm_dst) || !aligned4(topk_w))
     return MOE_ERR_INVALID_ARG;
   if (cfg->num_tokens == 0) return MOE_OK;
+  const RowBytes b(cfg, dtype);
+  if (!apart({{x_perm, b.sorted_rows}},
+             {{x, b.token_rows}, {perm_dst, b.pairs}, {topk_w, b.pairs}}))
+    return MOE_ERR_INVALID_ARG;
   if ((st = device_ready())) return st;
   return hip_status(launch_dispatch(dtype == MOE_DTYPE_FP32, x, perm_dst, topk_w, x_perm,
                                     cfg->num_tokens, cfg->hidden, cfg->topk,
@@ -79,6 +115,11 @@ int moe_dispatch_backward(const moe_config_t* cfg, int dtype, const void* grad_x
       !aligned4(topk_w) || !aligned4(grad_topk_w))
     return MOE_ERR_INVALID_ARG;
   if (cfg->num_tokens == 0) return MOE_OK;
+  const RowBytes b(cfg, dtype);
+  if (!apart({{grad_x, b.token_rows}, {grad_topk_w, b.pairs}},
+             {{grad_x_perm, b.sorted_rows}, {perm_dst, b.pairs}, {topk_w, b.pairs},
+              {x, b.token_rows}}))
+    return MOE_ERR_INVALID_ARG;
   if ((st = device_ready())) return st;
   return hip_status(launch_dispatch_backward(dtype == MOE_DTYPE_FP32, grad_x_perm, perm_dst,
                                              topk_w, x, grad_x, grad_topk_w, cfg->num_tokens,
@@ -94,6 +135,10 @@ int moe_combine_rows(const moe_config_t* cfg, int dtype, const void* y_perm,
   if (!aligned16(y_perm) || !aligned16(out) || !aligned4(perm_dst) || !aligned4(topk_w))
     return MOE_ERR_INVALID_ARG;
   if (cfg->num_tokens == 0) return MOE_OK;
+  const RowBytes b(cfg, dtype);
+  if (!apart({{out, b.token_rows}},
+             {{y_perm, b.sorted_rows}, {perm_dst, b.pairs}, {topk_w, b.pairs}}))
+    return MOE_ERR_INVALID_ARG;
   if ((st = device_ready())) return st;
   return hip_status(launch_combine_rows(dtype == MOE_DTYPE_FP32, y_perm, perm_dst, topk_w, out,
                                         cfg->num_tokens, cfg->hidden, cfg->topk,
@@ -111,6 +156,11 @@ int moe_combine_backward(const moe_config_t* cfg, int dtype, const void* grad_ou
       !aligned4(perm_dst) || !aligned4(topk_w) || !aligned4(grad_topk_w))
     return MOE_ERR_INVALID_ARG;
   if (cfg->num_tokens == 0) return MOE_OK;
+  const RowBytes b(cfg, dtype);
+  if (!apart({{grad_y_perm, b.sorted_rows}, {grad_topk_w, b.pairs}},
+             {{grad_out, b.token_rows}, {y_perm, b.sorted_rows}, {perm_dst, b.pairs},
+              {topk_w, b.pairs}}))
+    return MOE_ERR_INVALID_ARG;
   if ((st = device_ready())) return st;
   return hip_status(launch_combine_backward(dtype == MOE_DTYPE_FP32, grad_out, y_perm, perm_dst,
                                             topk_w, grad_y_perm, grad_topk_w, cfg->num_tokens,
@@ -135,6 +185,14 @@ int moe_route_backward(const moe_config_t* cfg, const uint16_t* x, const float* 
   if (!route_grad_fits(cfg->num_tokens, cfg->hidden, cfg->topk)) return MOE_ERR_UNSUPPORTED;
   if ((st = check_ws(workspace, workspace_bytes, route_backward_ws(cfg)))) return st;
   if (cfg->num_tokens == 0) return MOE_OK;
+  const RowBytes b(cfg, MOE_DTYPE_BF16);
+  const int64_t weights = (int64_t)cfg->num_experts * cfg->hidden * 4;
+  if (!apart({{grad_w_router, weights}, {grad_x, b.token_rows},
+              {workspace, (int64_t)route_backward_ws(cfg)}},
+             {{x, b.token_rows}, {w_router, weights}, {topk_ids, b.pairs}, {topk_logits, b.pairs},
+              {grad_topk_w, b.pairs}, {perm_src, b.pairs}, {offsets, (cfg->num_experts + 1) * 4},
+              {grad_x_add == grad_x ? nullptr : grad_x_add, b.token_rows}}))
+    return MOE_ERR_INVALID_ARG;
   if ((st = device_ready())) return st;
   const RouteGradWs w = route_grad_ws(cfg->num_tokens, cfg->hidden, cfg->topk);
   char* ws = static_cast<char*>(workspace);

@@ -340,7 +340,8 @@ int moe_layer_forward_lora(const moe_config_t* cfg, const uint16_t* x, const flo
  * length within a tensor need not be.  perm_dst is moe_permute's (or any
  * injective map of pairs to rows); an entry outside [0, num_tokens * topk)
  * drops its pair.  Sorted rows that no pair names are neither read nor written.
- * Inputs and outputs must not overlap.
+ * Outputs that overlap an input or each other are refused
+ * (MOE_ERR_INVALID_ARG).
  */
 enum moe_dtype { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP32 = 1 };
 
@@ -414,8 +415,9 @@ int moe_combine_backward(const moe_config_t* cfg, int dtype, const void* grad_ou
  *   grad_x_add               [T, H] bf16 or NULL: the hidden state's gradient from
  *                            elsewhere (the experts); may be grad_x itself
  *   grad_x                   NULL: not wanted (then grad_x_add is NULL too)
- * Sums are fp32 in a fixed order.  With no tokens nothing is written,
- * grad_w_router included.  Workspace MOE_ENTRY_ROUTE_BACKWARD; batches whose
+ * Sums are fp32 in a fixed order.  Other than grad_x_add == grad_x, outputs (and
+ * the workspace) that overlap an input or each other are refused.  With no
+ * tokens nothing is written, grad_w_router included.  Workspace MOE_ENTRY_ROUTE_BACKWARD; batches whose
  * grids exceed 2^32 threads (num_tokens * hidden around 2^37) return
  * MOE_ERR_UNSUPPORTED.
  */

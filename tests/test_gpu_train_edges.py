@@ -380,3 +380,27 @@ def test_adamw_refuses_memory_that_overlaps():
     state["exp_avg_sq_scale"] = [codes[126:].view(e8)]
     with pytest.raises(ValueError, match="overlap"):
         gtr.AdamW([low], state=state, state_bits=8)
+
+
+# ---------------------------------------------------------------------------
+# rows and the router's gradient
+def test_row_calls_refuse_outputs_that_overlap_inputs():
+    say("[rows] out= that shares memory with an input")
+    T, H, k = 64, 128, 2
+    buf = torch.zeros(2 * T * k * H, device=DEV)
+    x, apart = buf[:T * H].view(T, H), buf[T * H:T * H + T * k * H].view(T * k, H)
+    dst = torch.arange(T * k, dtype=torch.int32, device=DEV)
+    w = torch.ones(T, k, device=DEV)
+    for start in (0, T * H - 4):
+        with pytest.raises(gtr.MoeError):
+            gtr.dispatch(x, dst, topk=k, out=buf[start:start + T * k * H].view(T * k, H))
+    gtr.dispatch(x, dst, topk=k, out=apart)  # side by side
+    with pytest.raises(gtr.MoeError):
+        gtr.combine_backward(x, apart, dst, w, out=apart)
+    with pytest.raises(gtr.MoeError):
+        gtr.combine_backward(x, None, dst, w, need_grad_w=False,
+                             out=buf[:T * k * H].view(T * k, H))
+    xb, W, ids, z, g, src, off, _ = _router_case(40, 256, 8, 1)
+    with pytest.raises(gtr.MoeError):
+        gtr.route_backward(xb, W, ids, z, g, src, off, grad_w_router=W)
+    assert float(buf.abs().max()) == 0

@@ -1,5 +1,11 @@
 """CPU-side checks of the training calls' less usual arguments: each is settled
 on the host, before anything reaches a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+import grouped_top_routing_amd as gtr
 from grouped_top_routing_amd import _lib as L
 from test_train_abi import _opt, _step, _tensor
 
@@ -14,3 +20,53 @@ def test_adamw_checks_the_steps_of_its_tensors():
         assert _step(_opt(), _tensor(n=0, **kw)) == L.MOE_OK, kw
     # the list has a step of its own in any case
     assert _step(_opt(step=0), _tensor(n=0, step=3)) == L.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are made up")
+def test_outputs_that_overlap_are_refused():
+    """Every output against every input and every other output: one byte of
+    either end in common is refused, side by side passes this check (and then
+    finds no device here)."""
+    T, H, k, far = 64, 512, 4, 1 << 30
+    row, pair = {0: 2 * H, 1: 4 * H}, 4 * T * k
+    cfg = gtr.make_config(T, H, 128, num_groups=1, topk_groups=1, topk=k)
+    lib, c = gtr.lib(), ctypes.byref(cfg)
+    for dt in (0, 1):
+        tokens, srt = T * row[dt], T * k * row[dt]
+        calls = [
+            (lambda *a: lib.moe_dispatch(c, dt, *a, None), [tokens, pair, pair, srt], [3]),
+            (lambda *a: lib.moe_dispatch_backward(c, dt, *a, None),
+             [srt, pair, pair, tokens, tokens, pair], [4, 5]),
+            (lambda *a: lib.moe_combine_rows(c, dt, *a, None), [srt, pair, pair, tokens], [3]),
+            (lambda *a: lib.moe_combine_backward(c, dt, *a, None),
+             [tokens, srt, pair, pair, srt, pair], [4, 5]),
+        ]
+        for call, sizes, outs in calls:
+            _overlaps(call, sizes, outs, far, set())
+    ws = gtr.workspace_bytes(gtr.make_config(300, H, 128, num_groups=1, topk_groups=1, topk=k),
+                             gtr.ENTRY_ROUTE_BACKWARD)
+    T = cfg.num_tokens = 300
+    pair = 4 * T * k
+    call = lambda x, w, ids, z, g, src, off, add, gw, gx, work: lib.moe_route_backward(
+        c, x, w, ids, z, g, src, off, add, 0, gw, gx, work, ws, None)
+    sizes = [T * 2 * H, 1024 * H, pair, pair, pair, pair, 257 * 4, T * 2 * H, 1024 * H, T * 2 * H, ws]
+    _overlaps(call, sizes, [8, 9, 10], far, {(9, 7)})
+
+
+def _overlaps(call, sizes, outs, far, same_is_fine):
+    at = [far * (i + 1) for i in range(len(sizes))]
+    assert call(*at) == L.MOE_ERR_HIP
+    for o in outs:
+        for i in range(len(sizes)):
+            if i == o:
+                continue
+            moved = list(at)
+            # 16 bytes are the least by which aligned tensors can overlap
+            for start in (at[i], at[i] + sizes[i] // 16 * 16 - 16, at[i] - (sizes[o] - 16) // 16 * 16):
+                moved[o] = start
+                want = (L.MOE_ERR_HIP if (o, i) in same_is_fine and start == at[i]
+                        else L.MOE_ERR_INVALID_ARG)
+                assert call(*moved) == want, (o, i, start - at[i])
+            for start in (at[i] + -(-sizes[i] // 16) * 16, at[i] - -(-sizes[o] // 16) * 16):
+                moved[o] = start
+                assert call(*moved) == L.MOE_ERR_HIP, (o, i, start - at[i])
