@@ -182,7 +182,8 @@ int moe_route_backward(const moe_config_t* cfg, const uint16_t* x, const float* 
       !aligned16(grad_x_add) || !aligned4(topk_ids) || !aligned4(topk_logits) ||
       !aligned4(grad_topk_w) || !aligned4(perm_src) || !aligned4(offsets))
     return MOE_ERR_INVALID_ARG;
-  if (!route_grad_fits(cfg->num_tokens, cfg->hidden, cfg->topk)) return MOE_ERR_UNSUPPORTED;
+  if (!route_grad_fits(cfg->num_tokens, cfg->hidden, cfg->topk, grad_x != nullptr))
+    return MOE_ERR_UNSUPPORTED;
   if ((st = check_ws(workspace, workspace_bytes, route_backward_ws(cfg)))) return st;
   if (cfg->num_tokens == 0) return MOE_OK;
   const RowBytes b(cfg, MOE_DTYPE_BF16);

@@ -120,8 +120,8 @@ struct RouteGradWs {
   size_t dz, plan, part;  // bytes
 };
 RouteGradWs route_grad_ws(int64_t T, int H, int topk);
-// whether the launch's grid holds the batch
-bool route_grad_fits(int64_t T, int H, int topk);
+// whether the launches' grids hold the batch (grad_x: that is wanted too)
+bool route_grad_fits(int64_t T, int H, int topk, bool grad_x);
 hipError_t launch_route_backward(const uint16_t* x, const float* wr, const int32_t* ids,
                                  const float* logits, const float* grad_topk_w,
                                  const int32_t* perm_src, const int32_t* offsets,

@@ -428,7 +428,11 @@ int64_t chunks_of(int64_t n) { return kE + n / kRouteChunk; }
 int64_t dw_blocks(int64_t T, int H, int topk) {
   return (chunks_of(T * topk) * (H / kSlab) + 7) / 8 * 8;
 }
-int64_t dx_blocks(int64_t T, int H) { return (T * ((H + kDxCols - 1) / kDxCols) + 7) / 8 * 8; }
+int64_t dx_blocks(int64_t T, int64_t H) {
+  return (T * ((H + kDxCols - 1) / kDxCols) + 7) / 8 * 8;
+}
+// whether grad x, where wanted, is route_grad_kernel's (else route_dx_kernel's)
+bool dx_beside_dw(int64_t T) { return T < kLdsFrom; }
 
 }  // namespace
 
@@ -442,8 +446,12 @@ RouteGradWs route_grad_ws(int64_t T, int H, int topk) {
   return w;
 }
 
-bool route_grad_fits(int64_t T, int H, int topk) {
-  return (dw_blocks(T, H, topk) + dx_blocks(T, H)) * 256 < (int64_t)1 << 32;
+bool route_grad_fits(int64_t T, int H, int topk, bool grad_x) {
+  // a grid holds fewer than 2^32 threads.  The other launches' are smaller than
+  // this one's, but for the one of 8 threads per token.
+  const int64_t blocks =
+      dw_blocks(T, H, topk) + (grad_x && dx_beside_dw(T) ? dx_blocks(T, H) : 0);
+  return blocks < (int64_t)1 << 24 && (T / 32 + 2) * 256 < (int64_t)1 << 32;
 }
 
 hipError_t launch_route_backward(const uint16_t* x, const float* wr, const int32_t* ids,
@@ -466,7 +474,7 @@ hipError_t launch_route_backward(const uint16_t* x, const float* wr, const int32
                      ids, logits, grad_topk_w, slots, offsets, plan, chunks, T, topk, renormalize);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const bool lds_dx = grad_x && T >= kLdsFrom;
+  const bool lds_dx = grad_x && !dx_beside_dw(T);
   const int64_t dw = dw_blocks(T, H, topk), dx = grad_x && !lds_dx ? dx_blocks(T, H) : 0;
   hipLaunchKernelGGL(route_grad_kernel, dim3((unsigned)(dw + dx)), dim3(256), 0, stream, x, wr,
                      perm_src, slots, plan, chunks, add, grad_w, accumulate, part, grad_x, T, H,

@@ -417,9 +417,11 @@ int moe_combine_backward(const moe_config_t* cfg, int dtype, const void* grad_ou
  *   grad_x                   NULL: not wanted (then grad_x_add is NULL too)
  * Sums are fp32 in a fixed order.  Other than grad_x_add == grad_x, outputs (and
  * the workspace) that overlap an input or each other are refused.  With no
- * tokens nothing is written, grad_w_router included.  Workspace MOE_ENTRY_ROUTE_BACKWARD; batches whose
- * grids exceed 2^32 threads (num_tokens * hidden around 2^37) return
- * MOE_ERR_UNSUPPORTED.
+ * tokens nothing is written, grad_w_router included.  Workspace
+ * MOE_ENTRY_ROUTE_BACKWARD.  Batches whose grids reach 2^32 threads return
+ * MOE_ERR_UNSUPPORTED: num_tokens * topk * hidden around 2^40 (2^37 for 8
+ * slots), num_tokens from 2^29, hidden from 2^24, and up to 4095 tokens with
+ * grad_x num_tokens * hidden around 2^34.
  */
 int moe_route_backward(const moe_config_t* cfg, const uint16_t* x, const float* w_router,
                        const int32_t* topk_ids, const float* topk_logits,

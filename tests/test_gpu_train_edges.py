@@ -404,3 +404,38 @@ def test_row_calls_refuse_outputs_that_overlap_inputs():
     with pytest.raises(gtr.MoeError):
         gtr.route_backward(xb, W, ids, z, g, src, off, grad_w_router=W)
     assert float(buf.abs().max()) == 0
+
+
+def test_route_backward_past_2_to_34():
+    """2^24 + 5 tokens of 256 columns (a limit that counted workgroups which
+    only batches below 4096 tokens launch refused it); row offsets pass 2^32
+    elements.  With one slot and no renormalisation every gradient is one
+    product: grad x rows are checked singly, grad W against sums in fp64."""
+    T, H = (1 << 24) + 5, 256
+    say(f"[route_backward] {T} tokens of {H} columns")
+    g = torch.Generator(device=DEV).manual_seed(0)
+    x = torch.randn(T, H, generator=g, device=DEV, dtype=BF)
+    W = 0.02 * torch.randn(256, H, generator=g, device=DEV)
+    ids = torch.randint(0, 256, (T, 1), generator=g, device=DEV, dtype=torch.int32)
+    z = torch.randn(T, 1, generator=g, device=DEV)
+    gr = 1e-2 * torch.randn(T, 1, generator=g, device=DEV)
+    _, off, src, _ = gtr.permute(ids)
+    gw, gx = gtr.route_backward(x, W, ids, z, gr, src, off, renormalize=False)
+    s = torch.sigmoid(z.double())[:, 0]
+    dz = s * (1 - s) * gr.double()[:, 0]
+    dz_err = (32 + 8 * float(z.abs().max())) * U * dz.abs()
+    at = torch.tensor([0, 1, 65_537, T // 2, (1 << 24) - 1, 1 << 24, T - 1], device=DEV)
+    ref = dz[at, None] * W[ids[at, 0].long()].double()
+    size = (dz_err[at] + 2 * U * dz[at].abs())[:, None] * W[ids[at, 0].long()].double().abs()
+    within(gx[at], ref.cpu().numpy(),
+           (1.01 * (size + u_of(BF) * (ref.abs() + size))).cpu().numpy(), "grad_x")
+    want = torch.zeros(256, H, dtype=torch.float64, device=DEV)
+    dz_part, sums = torch.zeros_like(want), torch.zeros_like(want)
+    for t in range(0, T, 1 << 20):
+        e, part = ids[t:t + (1 << 20), 0].long(), x[t:t + (1 << 20)].double()
+        want.index_add_(0, e, dz[t:t + (1 << 20), None] * part)
+        sums.index_add_(0, e, dz[t:t + (1 << 20), None].abs() * part.abs())
+        dz_part.index_add_(0, e, dz_err[t:t + (1 << 20), None] * part.abs())
+    chunks = int((off[1:] - off[:-1]).max()) // 256 + 1
+    within(gw, want.cpu().numpy(),
+           (1.01 * (dz_part + (40 + chunks) * U * sums)).cpu().numpy(), "grad_w_router")

@@ -7,7 +7,7 @@ import torch
 
 import grouped_top_routing_amd as gtr
 from grouped_top_routing_amd import _lib as L
-from test_train_abi import _opt, _step, _tensor
+from test_train_abi import A, _opt, _step, _tensor
 
 
 def test_adamw_checks_the_steps_of_its_tensors():
@@ -70,3 +70,39 @@ def _overlaps(call, sizes, outs, far, same_is_fine):
             for start in (at[i] + -(-sizes[i] // 16) * 16, at[i] - -(-sizes[o] // 16) * 16):
                 moved[o] = start
                 assert call(*moved) == L.MOE_ERR_HIP, (o, i, start - at[i])
+
+
+def test_route_backward_batches_at_the_grids_limit():
+    """The largest batches: of (rows of 256 per expert + experts) * columns / 256
+    workgroups, and of tokens * columns / 1024 more where those are launched
+    (below 4096 tokens, with grad_x), fewer than 2^24 are taken."""
+    def status(T, H, k, gx=A):
+        cfg = gtr.make_config(T, H, 128, num_groups=1, topk_groups=1, topk=k)
+        # taken: the missing workspace is what is left to refuse
+        return gtr.lib().moe_route_backward(ctypes.byref(cfg), A, A, A, A, A, A, A, None, 0, A, gx,
+                                            None, 0, None)
+
+    def edge(H, k):
+        """The most tokens: (256 + T k / 256) H / 256, a multiple of 8, is below 2^24."""
+        rows = ((1 << 24) - 8) // (H // 256) - 256
+        return ((rows + 1) * 256 - 1) // k
+
+    for H, k in ((5120, 8), (5120, 3), (7168, 1), (512, 8)):
+        T = edge(H, k)
+        for gx in (A, None):
+            assert status(T, H, k, gx) == L.MOE_ERR_WORKSPACE, (H, k)
+            assert status(T + 256, H, k, gx) == L.MOE_ERR_UNSUPPORTED, (H, k)
+    # 8 threads per token: fewer than 2^29 tokens
+    assert status((1 << 29) - 65, 256, 1) == L.MOE_ERR_WORKSPACE
+    assert status(1 << 29, 256, 1) == L.MOE_ERR_UNSUPPORTED
+    # few tokens of very many columns
+    for T, k in ((129, 1), (4095, 1), (4096, 1)):
+        assert status(T, 1 << 24, k, None) == L.MOE_ERR_UNSUPPORTED
+    wide = 1 << 22
+    assert status(4096, wide, 8) == L.MOE_ERR_WORKSPACE
+    assert status(4095, wide, 8) == L.MOE_ERR_UNSUPPORTED
+    assert status(4095, wide, 8, None) == L.MOE_ERR_WORKSPACE
+    assert status(2000, wide, 8) == L.MOE_ERR_WORKSPACE
+    # small batches need no workspace: only the refusal is seen here
+    assert status(128, 1 << 24, 8) == L.MOE_ERR_UNSUPPORTED
+    assert status(128, (1 << 31) - 256, 8) == L.MOE_ERR_UNSUPPORTED
