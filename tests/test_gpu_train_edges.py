@@ -439,3 +439,20 @@ def test_route_backward_past_2_to_34():
     chunks = int((off[1:] - off[:-1]).max()) // 256 + 1
     within(gw, want.cpu().numpy(),
            (1.01 * (dz_part + (40 + chunks) * U * sums)).cpu().numpy(), "grad_w_router")
+
+
+@pytest.mark.parametrize("T", [60, 700])
+def test_route_backward_a_dropped_pair_adds_nothing(T):
+    # a sorted pair outside the batch has no token, so no token's infinities
+    # reach the gradient through it
+    say(f"[route_backward] a pair outside the batch beside an infinite row, T={T}")
+    x, W, ids, z, g, src, off, _ = _router_case(T, 512, 8, T, 0.0, 6)
+    others = torch.ones(256, dtype=torch.bool, device=DEV)
+    others[ids[0].long()] = False  # the experts that token 0 did not choose
+    at = int(others[ids.view(-1)[src.long()].long()].nonzero()[0])
+    src[at] = -1
+    want, _ = gtr.route_backward(x, W, ids, z, g, src, off)
+    x[0] = float("inf")
+    got, _ = gtr.route_backward(x, W, ids, z, g, src, off)
+    assert torch.equal(got[others], want[others])
+    assert bool(torch.isfinite(want).all()) and not bool(torch.isfinite(got[~others]).any())
