@@ -456,3 +456,117 @@ def test_route_backward_a_dropped_pair_adds_nothing(T):
     got, _ = gtr.route_backward(x, W, ids, z, g, src, off)
     assert torch.equal(got[others], want[others])
     assert bool(torch.isfinite(want).all()) and not bool(torch.isfinite(got[~others]).any())
+
+
+def _route_reference(x, W, ids, z, g, renormalize, chunks, add=None):
+    """(grad W, its bound, grad x, its bound) in fp64 on the device."""
+    x, W, idn = x.double(), W.double(), ids.cpu().numpy()
+    on = (idn >= 0) & (idn < 256)
+    zz, gg = np.where(on, n64(z), 0.0), np.where(on, n64(g), 0.0)
+    dz = train.route_dz(zz, idn, gg, renormalize)
+    s = 1 / (1 + np.exp(-zz))
+    if renormalize:
+        w = np.where(on, s, 0.0)
+        w = w / np.maximum(w.sum(1, keepdims=True), 1e-300)
+        size = w * (1 - s) * (np.abs(gg) + (np.abs(gg) * w).sum(1, keepdims=True))
+    else:
+        size = s * (1 - s) * np.abs(gg)
+    err = (32 + 8 * np.abs(zz).max()) * U * size
+    dev = lambda a: torch.from_numpy(a).to(DEV)
+    dz, err = dev(dz), dev(np.where(on, err, 0.0))
+    gw, bw = torch.zeros_like(W), torch.zeros_like(W)
+    gx, bx = torch.zeros_like(x), torch.zeros_like(x)
+    if add is not None:
+        gx, bx = add.double(), 2 * U * add.double().abs()
+    for j in range(ids.shape[1]):
+        t = dev(np.nonzero(on[:, j])[0])
+        e = ids[t, j].long()
+        d, de = dz[t, j, None], err[t, j, None]
+        gw.index_add_(0, e, d * x[t])
+        bw.index_add_(0, e, (de + (40 + chunks) * U * d.abs()) * x[t].abs())
+        gx[t] += d * W[e]
+        bx[t] += (de + 20 * U * d.abs()) * W[e].abs()
+    bx = bx + u_of(BF) * 1.01 * (gx.abs() + bx)
+    return gw, 1.01 * bw, gx, 1.01 * bx
+
+
+def _inside(got, ref, bound, what):
+    """within() on the device."""
+    worst = float(((got.double() - ref).abs() / bound.clamp(min=1e-300)).max())
+    say(f"  {what}: largest error {worst:.3f} of its bound")
+    assert worst <= 1, what
+
+
+#: shares of 684, 429, 250 and 3200 tokens per workgroup of the kernel that
+#: holds the weights in LDS, which takes 128 at a time: whole and partial last
+#: turns, the ends of waves' tokens among them
+@pytest.mark.parametrize("T,H,k,dropped", [(4099, 5120, 8, 0.02), (6001, 2304, 8, 0.0),
+                                           (16000, 512, 3, 0.05), (6400, 16640, 2, 0.0)])
+def test_route_backward_over_many_turns(T, H, k, dropped):
+    say(f"[route_backward] T={T} H={H} k={k} dropped={dropped}")
+    x, W, ids, z, g, src, off, add = _router_case(T, H, k, T, dropped, 8)
+    chunks = int((off[1:] - off[:-1]).max()) // 256 + 1
+    for extra in (None, add):
+        gw, gx = gtr.route_backward(x, W, ids, z, g, src, off, grad_x_add=extra)
+        rw, bw, rx, bx = _route_reference(x, W, ids, z, g, True, chunks, extra)
+        _inside(gw, rw, bw, "grad_w_router")
+        _inside(gx, rx, bx, "grad_x" if extra is None else "grad_x with add")
+    # in place: the C call takes grad_x_add == grad_x
+    cfg = gtr.make_config(T, H, 128, num_groups=1, topk_groups=1, topk=k)
+    nb = gtr.workspace_bytes(cfg, gtr.ENTRY_ROUTE_BACKWARD)
+    ws = torch.empty(nb, dtype=torch.uint8, device=DEV)
+    gw2, both = torch.empty_like(W), add.clone()
+    st = gtr.lib().moe_route_backward(
+        ctypes.byref(cfg), *(t.data_ptr() for t in (x, W, ids, z, g, src, off, both)), 0,
+        gw2.data_ptr(), both.data_ptr(), ws.data_ptr(), nb,
+        torch.cuda.current_stream(DEV).cuda_stream)
+    assert st == 0
+    assert torch.equal(gw2, gw) and torch.equal(both, gx)
+
+
+@pytest.mark.parametrize("T,H,k,dt,dropped", [(7000, 5120, 8, BF, 0.02), (4500, 4099, 8, F, 0.0),
+                                              (300_000, 136, 7, BF, 0.05)])
+def test_rows_past_the_cached_size(T, H, k, dt, dropped):
+    """Sorted rows of more than 512 MiB, which are stored past the caches: wide,
+    odd and narrow rows, every call that writes them."""
+    say(f"[rows] {T} x {k} x {H} {dt}: more than 512 MiB")
+    assert T * k * H * dt.itemsize > 512 << 20
+    g = torch.Generator(device=DEV).manual_seed(T)
+    ids = torch.randint(0, 256, (T, k), generator=g, device=DEV, dtype=torch.int32)
+    ids = torch.where(torch.rand(T, k, generator=g, device=DEV) < dropped, -1, ids)
+    _, off, _, dst = gtr.permute(ids)
+    x = torch.randn(T, H, generator=g, device=DEV).to(dt)
+    y = torch.randn(T * k, H, generator=g, device=DEV).to(dt)
+    w = weights(T, k, 1)
+    n = int(off[-1])
+    d, on = dst.view(T, k).long(), dst.view(T, k) >= 0
+    assert bool((on == (ids >= 0)).all()) and (dropped == 0) == (n == T * k)
+    mark = torch.full((), 7.0, dtype=dt, device=DEV)
+
+    def fresh():
+        return mark.expand(T * k, H).contiguous()
+
+    copied = gtr.dispatch(x, dst, topk=k, out=fresh())
+    scaled = gtr.dispatch(x, dst, topk=k, topk_w=w, out=fresh())
+    gy, gw = gtr.combine_backward(x, y, dst, w, out=fresh())
+    gy_alone, none = gtr.combine_backward(x, None, dst, w, need_grad_w=False, out=fresh())
+    assert none is None and torch.equal(gy_alone, gy)
+    del gy_alone
+    for got in (copied, scaled, gy):
+        assert bool((got[n:] == 7).all())  # rows that no pair names
+    u = u_of(dt)
+    for j in range(k):
+        t = on[:, j].nonzero()[:, 0]
+        for a in range(0, len(t), 50_000):
+            s = t[a:a + 50_000]
+            r, xs, ws = d[s, j], x[s].double(), w[s, j, None].double()
+            assert torch.equal(copied[r], x[s])
+            for got, c, rounds in ((scaled, 1.0, 1), (gy, 2.5, 2)):
+                ref = c * ws * xs
+                assert bool(((got[r].double() - ref).abs()
+                             <= (rounds * U + u) * 1.01 * ref.abs()).all())
+            terms = xs * y[r].double()
+            rounds = -(-H // 4096)
+            assert bool(((gw[s, j].double() - 2.5 * terms.sum(1)).abs()
+                         <= (24 + 8 * rounds) * U * 2.5 * terms.abs().sum(1)).all())
+    assert float(gw[~on].abs().sum()) == 0
