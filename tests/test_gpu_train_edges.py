@@ -570,3 +570,61 @@ def test_rows_past_the_cached_size(T, H, k, dt, dropped):
             assert bool(((gw[s, j].double() - 2.5 * terms.sum(1)).abs()
                          <= (24 + 8 * rounds) * U * 2.5 * terms.abs().sum(1)).all())
     assert float(gw[~on].abs().sum()) == 0
+
+
+# ---------------------------------------------------------------------------
+# RouterTrainer in the forms it can be built in
+@pytest.mark.parametrize("kind", ["fp8", "packed", "sel_bias", "plain_weights", "groups",
+                                  "scaling", "8bit"])
+def test_router_trainer_forms(kind):
+    """The output is the block's, the gradient that of the reference on the
+    same expert outputs, the weights those of AdamW by itself on it."""
+    say(f"[trainer] {kind}")
+    T = 150
+    d = synth.make_inputs(synth.workload("tiny", T=T), 0, device=DEV)
+    x, W, gu, dn = d["x"], d["w_router"].clone(), d["w_gate_up"], d["w_down"]
+    kw, layer, opt_kw, renormalize, scaling = {}, {}, {}, True, 2.5
+    experts = (gu, dn)
+    if kind == "fp8":
+        experts = (gtr.quantize_fp8(gu, dn),)
+    elif kind == "packed":
+        experts = gtr.pack_weights(gu, dn)
+        kw = layer = dict(weight_layout=gtr.LAYOUT_PACKED)
+    elif kind == "sel_bias":
+        kw = layer = dict(sel_bias=torch.linspace(-0.3, 0.3, 256, device=DEV))
+    elif kind == "plain_weights":
+        renormalize = False
+        kw = layer = dict(renormalize=False)
+    elif kind == "groups":
+        kw = layer = dict(num_groups=1, topk_groups=1, topk=5)
+    elif kind == "scaling":
+        scaling = -0.75
+        kw = layer = dict(routed_scaling=scaling)
+    else:
+        kw = opt_kw = dict(state_bits=8, seed=6)
+    forward = gtr.layer_forward_fp8 if kind == "fp8" else gtr.layer_forward
+    trainer = gtr.RouterTrainer(W, *experts, lr=1e-3, weight_decay=0.1, **kw)
+    twin = W.clone()
+    alone = gtr.AdamW([twin], lr=1e-3, weight_decay=0.1, **opt_kw)
+    g = torch.Generator().manual_seed(1)
+    for step in range(3):
+        want = forward(x, W, *experts, **layer)
+        out = trainer.forward(x)
+        assert torch.equal(out, want)
+        xs, ids, w, z, off, src, dst, y = trainer._saved
+        go = (torch.randn(T, 256, generator=g) * 1e-2).to(BF).to(DEV)
+        grad = n64(trainer.backward(go))
+        idn, dn_ = ids.cpu().numpy(), dst.cpu().numpy()
+        k = idn.shape[1]
+        _, gw = train.combine_backward(n64(go), n64(y), dn_, n64(w), scaling)
+        rw, _ = train.route_backward(n64(x), n64(W), idn, n64(z), gw, renormalize)
+        size = abs(scaling) * train._dots(np.abs(n64(go)), np.abs(n64(y)), dn_, k) * (32 * U)
+        dz_err = size + size.sum(1, keepdims=True)  # |w (1 - s)| and |s (1 - s)| are at most 1
+        ew = np.zeros_like(rw)
+        for j in range(k):
+            np.add.at(ew, idn[:, j], dz_err[:, j, None] * np.abs(n64(x)))
+        bw, _ = _route_bounds(n64(x), n64(W), idn, n64(z), gw, renormalize, T * k // 256 + 1)
+        within(grad, rw, bw + ew, f"step {step} gradient")
+        alone.step([trainer.grad])
+        trainer.step()
+        assert torch.equal(W, twin)
