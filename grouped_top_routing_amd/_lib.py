@@ -8,6 +8,7 @@ is no fallback: if the library is missing or a call fails, it raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -302,11 +303,28 @@ def _ws(workspace, device):
     return workspace
 
 
+def _on_their_device(call):
+    """`call` with the device of its tensors as the current one: a launch goes
+    there only by the stream it is given, and a device's default stream has the
+    same handle on every device."""
+    @functools.wraps(call)
+    def on_device(*args, **kw):
+        for t in (*args, *kw.values()):
+            if getattr(t, "is_cuda", False):
+                if t.device.index != torch.cuda.current_device():
+                    with torch.cuda.device(t.device):
+                        return call(*args, **kw)
+                break
+        return call(*args, **kw)
+    return on_device
+
+
 def _call(name, code):
     if code != MOE_OK:
         raise MoeError(code, name)
 
 
+@_on_their_device
 def route(x, w_router, *, sel_bias=None, num_groups=8, topk_groups=4, topk=8, renormalize=True,
           return_logits=False, workspace=None):
     """Router: returns (topk_ids int32 [T, k], topk_w fp32 [T, k]), and with
@@ -335,6 +353,7 @@ def route(x, w_router, *, sel_bias=None, num_groups=8, topk_groups=4, topk=8, re
     return ids, w
 
 
+@_on_their_device
 def route_replay(x, w_router, topk_ids, *, renormalize=True, return_logits=False, workspace=None):
     """Combine weights for caller-supplied expert ids: fp32 [T, k]; with
     return_logits (weights, router logits), both fp32 [T, k]."""
@@ -361,6 +380,7 @@ def route_replay(x, w_router, topk_ids, *, renormalize=True, return_logits=False
     return w
 
 
+@_on_their_device
 def permute(topk_ids, *, num_experts=256, workspace=None):
     """Returns (counts [E], offsets [E+1], perm_src [T*k], perm_dst [T*k]), all int32."""
     T, k = topk_ids.shape
@@ -379,6 +399,7 @@ def permute(topk_ids, *, num_experts=256, workspace=None):
     return counts, offsets, psrc, pdst
 
 
+@_on_their_device
 def expert_ffn(x, perm_src, offsets, w_gate_up, w_down, *, topk=8, weight_layout=LAYOUT_ROW_MAJOR,
                workspace=None):
     """Expert SwiGLU MLPs over the permuted rows: y_perm bf16 [T*k, H]."""
@@ -401,6 +422,7 @@ def expert_ffn(x, perm_src, offsets, w_gate_up, w_down, *, topk=8, weight_layout
     return y
 
 
+@_on_their_device
 def expert_gate_up(x, perm_src, offsets, w_gate_up, *, topk=8, weight_layout=LAYOUT_ROW_MAJOR,
                    workspace=None):
     """First expert GEMM with the fused SwiGLU: h bf16 [T*k, I]."""
@@ -422,6 +444,7 @@ def expert_gate_up(x, perm_src, offsets, w_gate_up, *, topk=8, weight_layout=LAY
     return h
 
 
+@_on_their_device
 def expert_down(h, offsets, w_down, *, topk=8, weight_layout=LAYOUT_ROW_MAJOR, workspace=None):
     """Second expert GEMM: y_perm bf16 [T*k, H]."""
     R, I = h.shape
@@ -441,6 +464,7 @@ def expert_down(h, offsets, w_down, *, topk=8, weight_layout=LAYOUT_ROW_MAJOR, w
     return y
 
 
+@_on_their_device
 def combine(y_perm, perm_dst, topk_w, *, routed_scaling=2.5):
     """Weighted un-permute: out [T, H], bf16 or fp32 as y_perm."""
     T, k = topk_w.shape
@@ -470,13 +494,13 @@ def _combine_rows(y_perm, perm_dst, topk_w, routed_scaling):
                       routed_scaling=routed_scaling)
     out = torch.empty(T, H, dtype=dt, device=y_perm.device)
     if T:
-        with torch.cuda.device(y_perm.device):
-            _call("moe_combine_rows", lib().moe_combine_rows(
-                ctypes.byref(cfg), DTYPE_FP32 if dt == torch.float32 else DTYPE_BF16,
-                _ptr(y_perm), _ptr(perm_dst), _ptr(topk_w), _ptr(out), _stream(y_perm.device)))
+        _call("moe_combine_rows", lib().moe_combine_rows(
+            ctypes.byref(cfg), DTYPE_FP32 if dt == torch.float32 else DTYPE_BF16,
+            _ptr(y_perm), _ptr(perm_dst), _ptr(topk_w), _ptr(out), _stream(y_perm.device)))
     return out
 
 
+@_on_their_device
 def layer_forward(x, w_router, w_gate_up, w_down, *, sel_bias=None, num_groups=8, topk_groups=4,
                   topk=8, renormalize=True, routed_scaling=2.5, weight_layout=LAYOUT_ROW_MAJOR,
                   return_routing=False, out=None, workspace=None):
@@ -510,6 +534,7 @@ def layer_forward(x, w_router, w_gate_up, w_down, *, sel_bias=None, num_groups=8
     return (out, ids, w) if return_routing else out
 
 
+@_on_their_device
 def layer_forward_noalloc(x, w_router, w_gate_up, w_down, *, sel_bias=None, num_groups=8,
                           topk_groups=4, topk=8, renormalize=True, routed_scaling=2.5,
                           weight_layout=LAYOUT_ROW_MAJOR, out=None, ids=None, w=None):
@@ -544,6 +569,7 @@ def layer_forward_noalloc(x, w_router, w_gate_up, w_down, *, sel_bias=None, num_
     return out if ids is None and w is None else (out, ids, w)
 
 
+@_on_their_device
 def pack_weights(w_gate_up=None, w_down=None):
     """Fragment-packed copies of the expert weights (MOE_LAYOUT_PACKED), same
     shapes and dtype as the inputs.  Either argument may be None."""
@@ -597,6 +623,7 @@ class Fp8Weights:
                    for t in (self.q_gate_up, self.s_gate_up, self.q_down, self.s_down))
 
 
+@_on_their_device
 def quantize_fp8(w_gate_up, w_down) -> Fp8Weights:
     """Per-channel FP8 quantisation of row-major bf16 expert weights."""
     E, I2, H = w_gate_up.shape
@@ -615,6 +642,7 @@ def quantize_fp8(w_gate_up, w_down) -> Fp8Weights:
     return f
 
 
+@_on_their_device
 def expert_ffn_fp8(x, perm_src, offsets, w: Fp8Weights, *, topk=8, workspace=None):
     """expert_ffn with FP8 weights: y_perm bf16 [T*k, H]."""
     T, H = x.shape
@@ -635,6 +663,7 @@ def expert_ffn_fp8(x, perm_src, offsets, w: Fp8Weights, *, topk=8, workspace=Non
     return y
 
 
+@_on_their_device
 def expert_gate_up_fp8(x, perm_src, offsets, w: Fp8Weights, *, topk=8, workspace=None):
     """expert_gate_up with FP8 weights: h bf16 [T*k, I]."""
     T, H = x.shape
@@ -654,6 +683,7 @@ def expert_gate_up_fp8(x, perm_src, offsets, w: Fp8Weights, *, topk=8, workspace
     return h
 
 
+@_on_their_device
 def expert_down_fp8(h, offsets, w: Fp8Weights, *, topk=8, workspace=None):
     """expert_down with FP8 weights: y_perm bf16 [T*k, H]."""
     R, I = h.shape
@@ -673,6 +703,7 @@ def expert_down_fp8(h, offsets, w: Fp8Weights, *, topk=8, workspace=None):
     return y
 
 
+@_on_their_device
 def layer_forward_fp8(x, w_router, w: Fp8Weights, *, sel_bias=None, num_groups=8, topk_groups=4,
                       topk=8, renormalize=True, routed_scaling=2.5, return_routing=False,
                       out=None, workspace=None):
@@ -731,6 +762,7 @@ class LoraWeights:
                        self.a_down.data_ptr(), self.b_down.data_ptr(), self.rank, self.scale)
 
 
+@_on_their_device
 def expert_ffn_lora(x, perm_src, offsets, w_gate_up, w_down, lora: LoraWeights, *, topk=8,
                     weight_layout=LAYOUT_ROW_MAJOR, workspace=None):
     """expert_ffn with expert LoRA: y_perm bf16 [T*k, H]."""
@@ -755,6 +787,7 @@ def expert_ffn_lora(x, perm_src, offsets, w_gate_up, w_down, lora: LoraWeights, 
     return y
 
 
+@_on_their_device
 def layer_forward_lora(x, w_router, w_gate_up, w_down, lora: LoraWeights, *, sel_bias=None,
                        num_groups=8, topk_groups=4, topk=8, renormalize=True, routed_scaling=2.5,
                        weight_layout=LAYOUT_ROW_MAJOR, return_routing=False, out=None,
