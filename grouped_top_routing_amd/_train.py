@@ -443,7 +443,7 @@ class AdamW:
         else:
             opt.grad_scale, opt.grad_scale_dev = float(grad_scale), None
         opt.step = self._steps + 1
-        capturing = torch.cuda.is_current_stream_capturing()
+        capturing = _lib._capturing(dev)
         if capturing and self._step_dev is None:
             raise RuntimeError("AdamW.step under graph capture needs capturable=True")
         counted = self._step_dev is not None

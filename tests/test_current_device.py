@@ -49,3 +49,28 @@ def test_calls_run_with_their_tensors_device_current(current, index):
 def test_every_call_does(name):
     fn = getattr(gtr, name)
     assert inspect.unwrap(fn) is not fn and inspect.unwrap(fn).__name__ == name
+
+
+def test_capture_is_looked_for_on_the_tensors_device(current, monkeypatch):
+    capturing = {0: True, 1: False}
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[current[0]])
+    assert L._capturing(torch.device("cuda", 0)) is True
+    assert L._capturing(torch.device("cuda", 1)) is False
+    assert current == [0]
+
+
+def test_adamw_asks_for_its_own_device(monkeypatch):
+    """A graph captured on another device is no business of this optimizer's."""
+    asked = []
+
+    def capturing(device):
+        asked.append(device)
+        return True
+
+    monkeypatch.setattr(L, "_capturing", capturing)
+    opt = gtr.AdamW.__new__(gtr.AdamW)
+    opt.params, opt._rows, opt.lr = (), (), 1e-3
+    opt.device, opt._opt, opt._step_dev, opt._steps = torch.device("cuda", 1), L.MoeAdamw(), None, 0
+    with pytest.raises(RuntimeError, match="capturable"):
+        opt.step([])
+    assert asked == [torch.device("cuda", 1)]
