@@ -261,13 +261,13 @@ __device__ __forceinline__ void update8(const AdamTensor& t, const AdamFactors& 
   }
 }
 
-// v, the same in every lane, as a scalar.  (The step read into vector registers
-// would leave its hash there too, also in steps that take it from the list: 227
-// against 213 us for the 8-bit states of 73.4 M elements.)
-__device__ __forceinline__ int64_t uniform(int64_t v) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)v);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
-  return (int64_t)((uint64_t)hi << 32 | lo);
+// *p by a scalar load (p is the same in every lane, and nothing in the kernel
+// writes there).  Through vector registers the step takes its hash there too,
+// also in steps that have it from the list: 227 against 213 us for the 8-bit
+// states of 73.4 M elements.
+__device__ __forceinline__ int64_t scalar_load(const int64_t* p) {
+  typedef const __attribute__((address_space(4))) int64_t* scalar_ptr;
+  return *(scalar_ptr)(uintptr_t)p;
 }
 
 __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a) {
@@ -283,10 +283,10 @@ __global__ __launch_bounds__(256) void adamw_kernel(const AdamArgs a) {
   AdamFactors k = a.factors;
   k.rate = t.rate;
   k.root = t.root;
-  int64_t step = t.step;
-  if (a.device) {
+  const bool counted = t.kind & 8;
+  const int64_t step = counted ? scalar_load(t.step_dev) : t.step;
+  if (counted || a.lr_dev || a.grad_scale_dev) {
     __shared__ AdamFactors shared;
-    if (t.kind & 8) step = uniform(*t.step_dev);
     if (threadIdx.x == 0)
       shared = factors_of(a, step, a.lr_dev ? (double)*a.lr_dev : a.lr,
                           (float)a.grad_scale * (a.grad_scale_dev ? *a.grad_scale_dev : 1.f));
@@ -317,13 +317,9 @@ int64_t adamw_blocks(int64_t n) { return (n + kSpan - 1) / kSpan; }
 void adamw_factors(AdamArgs& a) {
   // of the tensors whose step is known here; most lists have one step
   int64_t last = 0;
-  a.device = a.lr_dev || a.grad_scale_dev;
   for (int i = 0; i < a.count; ++i) {
     AdamTensor& t = a.tensor[i];
-    if (t.kind & 8) {
-      a.device = 1;
-      continue;
-    }
+    if (t.kind & 8) continue;
     if (t.step != last) a.factors = factors_of(a, t.step, a.lr, (float)a.grad_scale);
     last = t.step;
     t.rate = a.factors.rate;

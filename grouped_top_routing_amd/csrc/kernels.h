@@ -132,6 +132,15 @@ hipError_t launch_route_backward(const uint16_t* x, const float* wr, const int32
 // AdamW (adamw.hip).
 constexpr int kAdamTensors = 40;  // tensors per launch: their list is the kernel's argument
 struct AdamTensor {
+  union {
+    int64_t step;             // its t
+    const int64_t* step_dev;  // or where the kernel reads it (kind bit 3)
+  };
+  int64_t n;
+  float rate, root;  // of t (AdamFactors), in steps without device scalars
+  int32_t kind;  // bit 0: fp32 parameter (else bf16 with a master); bit 1: fp32 gradient;
+                 // bit 2: 32-bit states; bit 3: t on the device
+  int32_t place; // in the caller's list
   void* param;
   float* master;
   const void* grad;
@@ -139,15 +148,6 @@ struct AdamTensor {
   void* v;
   uint8_t* m_scale;
   uint8_t* v_scale;
-  int64_t n;
-  union {
-    int64_t step;             // its t
-    const int64_t* step_dev;  // or where the kernel reads it (kind bit 3)
-  };
-  float rate, root;  // of t (AdamFactors), in steps without device scalars
-  int32_t kind;  // bit 0: fp32 parameter (else bf16 with a master); bit 1: fp32 gradient;
-                 // bit 2: 32-bit states; bit 3: t on the device
-  int32_t place; // in the caller's list
 };
 // The factors of one step: keep - decay = 1 - lr wd (one of the two carries it),
 // rate = lr / (1 - b1^t), root = 1 / sqrt(1 - b2^t), gs the gradients' factor.
@@ -162,8 +162,7 @@ struct AdamArgs {
   const float* lr_dev;
   const float* grad_scale_dev;
   uint32_t seed;
-  int32_t count;   // tensors of this launch
-  int32_t device;  // whether any device scalar is read (steps, lr, grad_scale)
+  int32_t count;  // tensors of this launch
 };
 static_assert(sizeof(AdamArgs) <= 4096, "kernel arguments hold 4 KB");
 int64_t adamw_blocks(int64_t n);
