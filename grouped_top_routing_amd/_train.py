@@ -3,7 +3,9 @@ their gradients, the router's gradient, AdamW, and the router's training loop
 made of them.
 
 As in the rest of the binding, every step runs in the library's HIP kernels on
-the current stream of the tensors' device; nothing falls back to torch.
+the current stream of the tensors' device; nothing falls back to torch.  Results
+have no autograd graph, also where inputs require grad: a call and its gradient
+go into the forward and backward of a torch.autograd.Function.
 """
 from __future__ import annotations
 
@@ -107,7 +109,7 @@ def dispatch(x, perm_dst, *, topk=8, topk_w=None, out=None):
 
     Rows that no pair names (as many as perm_dst has entries of -1, the last
     ones of moe_permute's order) are left as ``out`` holds them; without
-    ``out`` they are not initialised."""
+    ``out`` they are not initialised.  ``out`` overlaps no input."""
     T = _tokens_of(perm_dst, topk)
     H, dt, dev = _need_rows(x, "x", T)
     _need(perm_dst, "perm_dst", torch.int32, (T * topk,), dev)
@@ -150,7 +152,7 @@ def combine_backward(grad_out, y_perm, perm_dst, topk_w, *, routed_scaling=2.5, 
     """Gradient of combine: (grad_y_perm [T*k, H], grad_topk_w fp32 [T, k]);
     None in the place of one that is not needed.  y_perm may be None without
     need_grad_w.  Rows of grad_y_perm that no pair names are left as ``out``
-    holds them (without ``out``: not initialised)."""
+    holds them (without ``out``: not initialised); ``out`` overlaps no input."""
     if not (need_grad_y or need_grad_w):
         raise ValueError("combine_backward: no gradient asked for")
     if not isinstance(topk_w, torch.Tensor) or topk_w.dim() != 2:
@@ -234,8 +236,8 @@ class AdamW:
     call (a launch per 40 tensors).
 
     params: fp32 tensors, or bf16 ones, which get an fp32 master copy that the
-    update works on; contiguous, 16-byte aligned, on one device, updated in
-    place.  state_bits: 32, or 8 for states in E4M3 codes with a power-of-two
+    update works on; contiguous, 16-byte aligned (gradients too), on one device,
+    apart in memory, updated in place.  state_bits: 32, or 8 for states in E4M3 codes with a power-of-two
     scale per 32 elements (2.06 bytes per element instead of 8), rounded
     stochastically from ``seed``.
 
@@ -485,7 +487,7 @@ class RouterTrainer:
             trainer.backward(loss_gradient(out, target))
             trainer.step()
 
-    Between forward and backward x and w_router stay as they are.  Experts are
+    Between forward and backward x, w_router and topk_ids stay as they are.  Experts are
     bf16 (w_gate_up, w_down in weight_layout), or Fp8Weights in the place of
     w_gate_up with w_down None.  The hidden state's gradient is not computed: it
     would need the experts' own."""

@@ -24,11 +24,13 @@
 // to keep or to copy), kAdamTensors tensors to a launch; a workgroup takes one
 // span of 2048 elements (four spans: 415 -> 432 us, and the factors of a step
 // are worked out on the host unless they are on the device).  Measured on 73.4
-// M elements (one layer's rank-16 adapters): 378 us with 32-bit states (5.4
-// TB/s), 208 with 8-bit ones (5.7 TB/s; 307 before the conversions were the
-// hardware's).  Stores are non-temporal (415 -> 378 and 224 -> 208 us, and 10.6
-// -> 9.5 on 1.3 M elements that stay in the caches); loads are not (393, 213
-// and 10.3 with them).
+// M elements (one layer's rank-16 adapters): 377 us with 32-bit states (5.5
+// TB/s), 213 with 8-bit ones (5.5 TB/s; conversions that are not the hardware's
+// take 307).  With the step, the rate or the gradients' factor on the device
+// every workgroup works the factors out before it can use its loads: 381 and 233
+// us.  Stores are non-temporal (plain ones took 415 instead of 378 and 224
+// instead of 208 us, and 10.6 instead of 9.5 on 1.3 M elements that stay in the
+// caches); loads are not (393, 213 and 10.3 with them).
 #include <cfloat>
 
 #include "common.h"

@@ -19,8 +19,10 @@
 // slabs of columns, and consecutive workgroups of one XCD stay on one slab, so
 // that an x slab (256 columns, 512 B per token) and a W slab (1 MB) stay in that
 // XCD's L2 (token by token instead, grad x of 5120 tokens takes 74 against 62
-// us of the whole call); large batches read W from LDS.  The whole call takes
-// 71 us at 5120 tokens, of which grad W 30 (14 TB/s of L2 reads).
+// us of the whole call); large batches read W from LDS.  With 5120 tokens of
+// 5120 columns and `add` the call takes 62 us, 75 with the tokens on few experts:
+// grad W 37 (its 420 MB of row reads at 11 TB/s), grad x 32, dz and the plan 4,
+// the partial sums 5.
 #include "common.h"
 #include "kernels.h"
 
@@ -31,10 +33,13 @@ namespace {
 constexpr int kE = 256;            // experts
 constexpr int kSlab = 256;         // columns per workgroup of the grad W part
 constexpr int kDxCols = 1024;      // columns per workgroup of the grad x part
-// Batches from which grad x reads the weights from LDS instead of L2 (the whole
-// call, hidden 5120, `add` not in the caches: 72 against 90 us at 5120 tokens,
-// 235 against 310 at 16384; 38 against 42 at 2048, but 35 against 32 without
-// `add`, and 23 against 19 at 512).
+// Batches from which grad x reads the weights from LDS instead of L2.  The whole
+// call, LDS against L2, with `add` and without: 5120 columns, 2048 tokens 35.1
+// against 33.8 us and 33.4 against 32.1, 4096 tokens 53.1 against 54.0 and 50.7
+// against 50.9, 5120 tokens 62 against 76 and 59 against 61, 16384 tokens 235
+// against 309 and 220 against 238; 1280 columns, 2048 tokens 19.8 against 17.2
+// and 19.1 against 16.1, 4096 tokens 24.6 against 24.5 and 23.4 against 22.9,
+// 5120 tokens 26.8 against 28.7 and 25.6 against 27.0.
 constexpr int64_t kLdsFrom = 4096;
 
 // The plan (int32): per chunk (expert, first row, rows), then for every
