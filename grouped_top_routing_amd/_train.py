@@ -456,9 +456,14 @@ class AdamW:
                 self._list[i].step = opt.step - fewer
         try:
             _launch("moe_adamw_step", dev, self._opt_ref, self._list, len(self._rows))
-        except _lib.MoeError:
+        except _lib.MoeError as e:
             if counted:
                 self._count(absent, -1)  # refused: no step was made
+            for name, ts in (("params", self.params), ("grads", grads)):
+                for i, t in enumerate(ts):
+                    if t is not None and t.data_ptr() % 16:
+                        raise _lib.MoeError(e.code, f"moe_adamw_step: {name}[{i}] is not 16-byte "
+                                                    "aligned") from None
             raise
         if not capturing:
             self._steps += 1

@@ -465,8 +465,8 @@ typedef struct moe_adamw_tensor {
   int32_t grad_dtype;  /* moe_dtype                                            */
   int32_t state_bits;  /* 32 or 8                                              */
   /* The tensor's own t, where it has made fewer steps than the list (one whose
-   * gradient came late, or comes now and then): step_dev, read when the step
-   * runs, or else step; NULL and 0 stand for the list's. */
+   * gradient came late, or comes now and then): step_dev (>= 1, read when the
+   * step runs), or else step; NULL and 0 stand for the list's. */
   int64_t step;
   const int64_t* step_dev;
 } moe_adamw_tensor_t;

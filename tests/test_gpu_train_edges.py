@@ -628,3 +628,18 @@ def test_router_trainer_forms(kind):
         alone.step([trainer.grad])
         trainer.step()
         assert torch.equal(W, twin)
+
+
+def test_adamw_names_what_is_not_aligned():
+    say("[adamw] a gradient that starts inside 16 bytes")
+    p = [torch.zeros(64, device=DEV), torch.zeros(32, device=DEV)]
+    flat = torch.ones(97, device=DEV)
+    for capturable in (False, True):
+        opt = gtr.AdamW(p, capturable=capturable)
+        with pytest.raises(gtr.MoeError, match=r"grads\[1\] is not 16-byte aligned"):
+            opt.step([flat[:64], flat[65:]])
+        assert opt.step_count == 0 and float(p[0].abs().max()) == 0
+        with pytest.raises(gtr.MoeError, match="MOE_ERR_INVALID_ARG"):
+            opt.step([flat[:64], None], lr=-1.0)
+    with pytest.raises(gtr.MoeError, match=r"params\[0\] is not 16-byte aligned"):
+        gtr.AdamW([flat[1:65]]).step([p[0]])
