@@ -237,19 +237,20 @@ class AdamW:
 
     params: fp32 tensors, or bf16 ones, which get an fp32 master copy that the
     update works on; contiguous, 16-byte aligned (gradients too), on one device,
-    apart in memory, updated in place.  state_bits: 32, or 8 for states in E4M3 codes with a power-of-two
-    scale per 32 elements (2.06 bytes per element instead of 8), rounded
-    stochastically from ``seed``.
+    apart in memory, updated in place.  state_bits: 32, or 8 for states in E4M3
+    codes with a power-of-two scale per 32 elements (2.06 bytes per element
+    instead of 8), rounded stochastically from ``seed``.
 
     ``state`` is a dict of lists, one entry per parameter: ``exp_avg``,
     ``exp_avg_sq`` (with 8 bits the codes of its square root), with 8 bits
     ``exp_avg_scale`` and ``exp_avg_sq_scale``, and ``master`` (None for fp32
-    parameters).  Pass one in, with ``step_count``, to continue from a
-    checkpoint; its tensors are used, not copied.
+    parameters).  Pass one in, with ``step_count`` (the old one's
+    ``step_counts``), to continue from a checkpoint; its tensors are used, not
+    copied.
 
     A parameter without a gradient makes no step, and its bias correction goes
     by the steps that it has made itself.  ``step_counts`` has them, one per
-    parameter, and belongs into a checkpoint: ``step_count`` takes such a list,
+    parameter, and belongs in a checkpoint: ``step_count`` takes such a list,
     or one number for all.
 
     ``capturable`` keeps the step numbers on the device, so that a captured

@@ -643,3 +643,37 @@ def test_adamw_names_what_is_not_aligned():
             opt.step([flat[:64], None], lr=-1.0)
     with pytest.raises(gtr.MoeError, match=r"params\[0\] is not 16-byte aligned"):
         gtr.AdamW([flat[1:65]]).step([p[0]])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_c_call_takes_steps_of_list_and_tensors(bits):
+    """In one call: a tensor with a step of its own, one with its own on the
+    device, and one that goes by the list's, on the device or not."""
+    say(f"[adamw] the C call's four places of a step, {bits} bits")
+    sizes, own = (1000, 70, 2049), (3, 7, 12)
+    counters = torch.tensor([7, 12], dtype=torch.int64, device=DEV)
+    got = None
+    for on_device in (False, True):
+        params = [rows(1, n, F, i).view(-1) for i, n in enumerate(sizes)]
+        grads = [rows(1, n, F, 10 + i).view(-1) for i, n in enumerate(sizes)]
+        want = [p.clone() for p in params]
+        ref = _opt(want, state_bits=bits, seed=3, step_count=[s - 1 for s in own])
+        ref.step(grads)
+        opt = _opt(params, state_bits=bits, seed=3)  # its states, and its list to fill in
+        for d, g, n in zip(opt._list, grads, sizes):
+            d.grad, d.grad_dtype, d.n = g.data_ptr(), gtr.DTYPE_FP32, n
+        opt._list[0].step = 3
+        opt._list[1].step, opt._list[1].step_dev = 99, counters.data_ptr()  # the device's goes first
+        a = opt._opt
+        a.lr, a.grad_scale, a.step = HP["lr"], 1.0, 1 if on_device else 12
+        a.step_dev = counters.data_ptr() + 8 if on_device else None
+        st = gtr.lib().moe_adamw_step(ctypes.byref(a), opt._list, 3,
+                                      torch.cuda.current_stream(DEV).cuda_stream)
+        assert st == 0
+        for i in range(3):
+            assert torch.equal(params[i], want[i]), (on_device, i)
+            for k in ref.state:
+                if ref.state[k][i] is not None:
+                    assert torch.equal(opt.state[k][i].float(), ref.state[k][i].float()), (i, k)
+        assert got is None or all(torch.equal(x, y) for x, y in zip(got, params))
+        got = params
