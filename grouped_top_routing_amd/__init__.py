@@ -19,7 +19,10 @@ from ._lib import (  # noqa: F401
     pack_weights, permute, quantize_fp8, route, route_replay, status_string, workspace_bytes,
     LIB_CHECKED_PATH, CHECK_BITS, check_flags, use_library,
     DTYPE_BF16, DTYPE_FP32, ENTRY_ROUTE_BACKWARD,
+    LAYOUT_FP4_PACKED, Fp4Weights, expert_down_fp4, expert_ffn_fp4, expert_gate_up_fp4,
+    layer_forward_fp4, pack_fp4, quantize_fp4,
 )
 from ._train import (  # noqa: F401
     AdamW, RouterTrainer, combine_backward, dispatch, dispatch_backward, route_backward,
 )
+from ._select import balance_loss, route_select, select, select_backward  # noqa: F401

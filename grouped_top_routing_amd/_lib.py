@@ -42,6 +42,7 @@ ENTRY_ROUTE_BACKWARD = 8
 LAYOUT_ROW_MAJOR = 0
 LAYOUT_PACKED = 1
 LAYOUT_FP8_PACKED = 2
+LAYOUT_FP4_PACKED = 4
 
 DTYPE_BF16 = 0
 DTYPE_FP32 = 1
@@ -54,7 +55,10 @@ EXPORTS = ("moe_workspace_bytes", "moe_route", "moe_route_replay", "moe_permute"
            "moe_expert_ffn_lora", "moe_layer_forward_lora", "moe_layer_forward_noalloc",
            "moe_debug_check_flags", "moe_status_string", "moe_route_logits", "moe_dispatch",
            "moe_dispatch_backward", "moe_combine_rows", "moe_combine_backward",
-           "moe_route_backward", "moe_adamw_step")
+           "moe_route_backward", "moe_adamw_step", "moe_select", "moe_route_select",
+           "moe_balance_workspace_bytes", "moe_balance_loss", "moe_select_backward",
+           "moe_quantize_fp4", "moe_pack_fp4", "moe_expert_ffn_fp4", "moe_expert_gate_up_fp4",
+           "moe_expert_down_fp4", "moe_layer_forward_fp4")
 
 
 class MoeConfig(ctypes.Structure):
@@ -117,6 +121,20 @@ class MoeAdamw(ctypes.Structure):
     ]
 
 
+class MoeSelectConfig(ctypes.Structure):
+    _fields_ = [
+        ("num_tokens", ctypes.c_int64),
+        ("num_experts", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32),
+        ("group_best", ctypes.c_int32),
+        ("topk", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("logits_dtype", ctypes.c_int32),
+    ]
+
+
 class MoeError(RuntimeError):
     def __init__(self, code: int, what: str):
         self.code = code
@@ -159,6 +177,12 @@ def load(path: str) -> ctypes.CDLL:
     L.moe_expert_gate_up_fp8.argtypes = [CP, P, P, P, P, P, P, P, Z, P]
     L.moe_expert_down_fp8.argtypes = [CP, P, P, P, P, P, P, Z, P]
     L.moe_layer_forward_fp8.argtypes = [CP, P, P, P, P, P, P, P, P, P, P, P, Z, P]
+    L.moe_quantize_fp4.argtypes = [CP, P, P, P, P, P, P, P]
+    L.moe_pack_fp4.argtypes = [CP, P, P, P, P, P, P, P, P, P]
+    L.moe_expert_ffn_fp4.argtypes = [CP, P, P, P, P, P, P, P, P, P, Z, P]
+    L.moe_expert_gate_up_fp4.argtypes = [CP, P, P, P, P, P, P, P, Z, P]
+    L.moe_expert_down_fp4.argtypes = [CP, P, P, P, P, P, P, Z, P]
+    L.moe_layer_forward_fp4.argtypes = [CP, P, P, P, P, P, P, P, P, P, P, P, Z, P]
     LP = ctypes.POINTER(MoeLora)
     L.moe_expert_ffn_lora.argtypes = [CP, P, P, P, P, P, LP, P, P, Z, P]
     L.moe_layer_forward_lora.argtypes = [CP, P, P, P, P, P, LP, P, P, P, P, Z, P]
@@ -169,6 +193,12 @@ def load(path: str) -> ctypes.CDLL:
     L.moe_combine_backward.argtypes = [CP, I, P, P, P, P, P, P, P]
     L.moe_route_backward.argtypes = [CP, P, P, P, P, P, P, P, P, I, P, P, P, Z, P]
     L.moe_adamw_step.argtypes = [ctypes.POINTER(MoeAdamw), ctypes.POINTER(MoeAdamwTensor), I, P]
+    SP = ctypes.POINTER(MoeSelectConfig)
+    L.moe_select.argtypes = [SP, P, P, P, P, P]
+    L.moe_route_select.argtypes = [CP, SP, P, P, P, P, P, P, P, Z, P]
+    L.moe_balance_workspace_bytes.argtypes = [SP, ctypes.POINTER(Z)]
+    L.moe_balance_loss.argtypes = [SP, P, P, ctypes.c_float, P, P, P, Z, P]
+    L.moe_select_backward.argtypes = [SP, P, P, P, P, P, P, P]
     L.moe_debug_check_flags.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
     L.moe_status_string.argtypes = [I]
     L.moe_status_string.restype = ctypes.c_char_p
@@ -732,6 +762,188 @@ def layer_forward_fp8(x, w_router, w: Fp8Weights, *, sel_bias=None, num_groups=8
         ctypes.byref(cfg), _ptr(x), _ptr(w_router), _ptr(sel_bias), _ptr(w.q_gate_up),
         _ptr(w.s_gate_up), _ptr(w.q_down), _ptr(w.s_down), _ptr(out), _ptr(ids), _ptr(tw),
         _ptr(ws), nb, _stream(x.device)))
+    return (out, ids, tw) if return_routing else out
+
+
+# ---------------------------------------------------------------------------
+# 4-bit (E2M1) expert weights with one E8M0 scale per 32 weights
+class Fp4Weights:
+    """Expert weights in 4 bits, in the fp4 fragment layout: codes uint8
+    (q_gate_up [E, 2I, H/2], q_down [E, H, I/2]) and E8M0 scales uint8
+    (s_gate_up [E, 2I, H/32], s_down [E, H, I/32])."""
+
+    def __init__(self, q_gate_up, s_gate_up, q_down, s_down):
+        self.q_gate_up, self.s_gate_up = q_gate_up, s_gate_up
+        self.q_down, self.s_down = q_down, s_down
+
+    @property
+    def shape(self):
+        """(E, H, I)."""
+        E, I2, H2 = self.q_gate_up.shape
+        return E, H2 * 2, I2 // 2
+
+    def check(self, device):
+        _check_fp4(self.shape, device, self.q_gate_up, self.s_gate_up, self.q_down, self.s_down)
+
+    def nbytes(self) -> int:
+        return sum(t.numel() for t in (self.q_gate_up, self.s_gate_up, self.q_down, self.s_down))
+
+
+def _check_fp4(shape, device, codes_gate_up, scales_gate_up, codes_down, scales_down):
+    E, H, I = shape
+    _check(codes_gate_up, "codes_gate_up", torch.uint8, (E, 2 * I, H // 2), device)
+    _check(scales_gate_up, "scales_gate_up", torch.uint8, (E, 2 * I, H // 32), device)
+    _check(codes_down, "codes_down", torch.uint8, (E, H, I // 2), device)
+    _check(scales_down, "scales_down", torch.uint8, (E, H, I // 32), device)
+
+
+def _fp4_like(E, H, I, device):
+    return Fp4Weights(torch.empty(E, 2 * I, H // 2, dtype=torch.uint8, device=device),
+                      torch.empty(E, 2 * I, H // 32, dtype=torch.uint8, device=device),
+                      torch.empty(E, H, I // 2, dtype=torch.uint8, device=device),
+                      torch.empty(E, H, I // 32, dtype=torch.uint8, device=device))
+
+
+@_on_their_device
+def quantize_fp4(w_gate_up, w_down) -> Fp4Weights:
+    """4-bit quantisation of row-major bf16 expert weights, one power-of-two
+    scale per 32 weights of a row."""
+    E, I2, H = w_gate_up.shape
+    I = I2 // 2
+    _check(w_gate_up, "w_gate_up", torch.bfloat16, (E, 2 * I, H))
+    _check(w_down, "w_down", torch.bfloat16, (E, H, I), w_gate_up.device)
+    cfg = make_config(0, H, I, num_experts=E, num_groups=1, topk_groups=1, topk=1)
+    f = _fp4_like(E, H, I, w_gate_up.device)
+    _call("moe_quantize_fp4", lib().moe_quantize_fp4(
+        ctypes.byref(cfg), _ptr(w_gate_up), _ptr(w_down), _ptr(f.q_gate_up), _ptr(f.s_gate_up),
+        _ptr(f.q_down), _ptr(f.s_down), _stream(w_gate_up.device)))
+    return f
+
+
+@_on_their_device
+def pack_fp4(codes_gate_up, scales_gate_up, codes_down, scales_down) -> Fp4Weights:
+    """Fp4Weights of a row-major checkpoint: uint8 codes [E, 2I, H/2] and [E, H,
+    I/2], two per byte with the lower k in the low half, and uint8 E8M0 scales
+    [E, 2I, H/32] and [E, H, I/32]."""
+    E, I2, H2 = codes_gate_up.shape
+    H, I = H2 * 2, I2 // 2
+    dev = codes_gate_up.device
+    _check(codes_gate_up, "codes_gate_up", torch.uint8)
+    _check_fp4((E, H, I), dev, codes_gate_up, scales_gate_up, codes_down, scales_down)
+    cfg = make_config(0, H, I, num_experts=E, num_groups=1, topk_groups=1, topk=1)
+    f = _fp4_like(E, H, I, dev)
+    _call("moe_pack_fp4", lib().moe_pack_fp4(
+        ctypes.byref(cfg), _ptr(codes_gate_up), _ptr(scales_gate_up), _ptr(codes_down),
+        _ptr(scales_down), _ptr(f.q_gate_up), _ptr(f.s_gate_up), _ptr(f.q_down), _ptr(f.s_down),
+        _stream(dev)))
+    return f
+
+
+def _fp4_config(T, w, topk):
+    E, H, I = w.shape
+    return make_config(T, H, I, num_experts=E, num_groups=1, topk_groups=1, topk=topk,
+                       weight_layout=LAYOUT_FP4_PACKED)
+
+
+@_on_their_device
+def expert_ffn_fp4(x, perm_src, offsets, w: Fp4Weights, *, topk=8, out=None, workspace=None):
+    """expert_ffn with 4-bit weights: y_perm bf16 [T*k, H].  Rows past
+    offsets[E] (dropped pairs) are left as ``out`` holds them; without ``out``
+    they are not initialised."""
+    T, H = x.shape
+    E, H_w, I = w.shape
+    _check(x, "x", torch.bfloat16, (T, H_w))
+    w.check(x.device)
+    _check(perm_src, "perm_src", torch.int32, (T * topk,), x.device)
+    _check(offsets, "offsets", torch.int32, (E + 1,), x.device)
+    cfg = _fp4_config(T, w, topk)
+    if out is None:
+        out = torch.empty(T * topk, H, dtype=torch.bfloat16, device=x.device)
+    else:
+        _check(out, "out", torch.bfloat16, (T * topk, H), x.device)
+    if T == 0:
+        return out
+    nb = workspace_bytes(cfg, ENTRY_EXPERT_FFN)
+    ws = _ws(workspace, x.device).get(nb, x.device)
+    _call("moe_expert_ffn_fp4", lib().moe_expert_ffn_fp4(
+        ctypes.byref(cfg), _ptr(x), _ptr(perm_src), _ptr(offsets), _ptr(w.q_gate_up),
+        _ptr(w.s_gate_up), _ptr(w.q_down), _ptr(w.s_down), _ptr(out), _ptr(ws), nb,
+        _stream(x.device)))
+    return out
+
+
+@_on_their_device
+def expert_gate_up_fp4(x, perm_src, offsets, w: Fp4Weights, *, topk=8, workspace=None):
+    """expert_gate_up with 4-bit weights: h bf16 [T*k, I]."""
+    T, H = x.shape
+    E, H_w, I = w.shape
+    _check(x, "x", torch.bfloat16, (T, H_w))
+    w.check(x.device)
+    _check(perm_src, "perm_src", torch.int32, (T * topk,), x.device)
+    _check(offsets, "offsets", torch.int32, (E + 1,), x.device)
+    cfg = _fp4_config(T, w, topk)
+    h = torch.empty(T * topk, I, dtype=torch.bfloat16, device=x.device)
+    if T == 0:
+        return h
+    nb = workspace_bytes(cfg, ENTRY_EXPERT_STAGE)
+    ws = _ws(workspace, x.device).get(nb, x.device)
+    _call("moe_expert_gate_up_fp4", lib().moe_expert_gate_up_fp4(
+        ctypes.byref(cfg), _ptr(x), _ptr(perm_src), _ptr(offsets), _ptr(w.q_gate_up),
+        _ptr(w.s_gate_up), _ptr(h), _ptr(ws), nb, _stream(x.device)))
+    return h
+
+
+@_on_their_device
+def expert_down_fp4(h, offsets, w: Fp4Weights, *, topk=8, workspace=None):
+    """expert_down with 4-bit weights: y_perm bf16 [T*k, H]."""
+    R, I = h.shape
+    E, H, I_w = w.shape
+    T = R // topk
+    _check(h, "h", torch.bfloat16, (T * topk, I_w))
+    w.check(h.device)
+    _check(offsets, "offsets", torch.int32, (E + 1,), h.device)
+    cfg = _fp4_config(T, w, topk)
+    y = torch.empty(T * topk, H, dtype=torch.bfloat16, device=h.device)
+    if T == 0:
+        return y
+    nb = workspace_bytes(cfg, ENTRY_EXPERT_STAGE)
+    ws = _ws(workspace, h.device).get(nb, h.device)
+    _call("moe_expert_down_fp4", lib().moe_expert_down_fp4(
+        ctypes.byref(cfg), _ptr(h), _ptr(offsets), _ptr(w.q_down), _ptr(w.s_down), _ptr(y),
+        _ptr(ws), nb, _stream(h.device)))
+    return y
+
+
+@_on_their_device
+def layer_forward_fp4(x, w_router, w: Fp4Weights, *, sel_bias=None, num_groups=8, topk_groups=4,
+                      topk=8, renormalize=True, routed_scaling=2.5, return_routing=False,
+                      out=None, workspace=None):
+    """layer_forward with 4-bit expert weights."""
+    T, H = x.shape
+    E, H_w, I = w.shape
+    _check(x, "x", torch.bfloat16, (T, H_w))
+    _check(w_router, "w_router", torch.float32, (E, H), x.device)
+    w.check(x.device)
+    if sel_bias is not None:
+        _check(sel_bias, "sel_bias", torch.float32, (E,), x.device)
+    cfg = make_config(T, H, I, num_experts=E, num_groups=num_groups, topk_groups=topk_groups,
+                      topk=topk, renormalize=renormalize, routed_scaling=routed_scaling,
+                      weight_layout=LAYOUT_FP4_PACKED)
+    if out is None:
+        out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
+    else:
+        _check(out, "out", torch.bfloat16, (T, H), x.device)
+    ids = tw = None
+    if return_routing:
+        ids = torch.empty(T, topk, dtype=torch.int32, device=x.device)
+        tw = torch.empty(T, topk, dtype=torch.float32, device=x.device)
+    if T:
+        nb = workspace_bytes(cfg, ENTRY_LAYER)
+        ws = _ws(workspace, x.device).get(nb, x.device)
+        _call("moe_layer_forward_fp4", lib().moe_layer_forward_fp4(
+            ctypes.byref(cfg), _ptr(x), _ptr(w_router), _ptr(sel_bias), _ptr(w.q_gate_up),
+            _ptr(w.s_gate_up), _ptr(w.q_down), _ptr(w.s_down), _ptr(out), _ptr(ids), _ptr(tw),
+            _ptr(ws), nb, _stream(x.device)))
     return (out, ids, tw) if return_routing else out
 
 

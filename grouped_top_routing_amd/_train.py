@@ -16,8 +16,9 @@ import operator
 import torch
 
 from . import _lib
-from ._lib import (DTYPE_BF16, DTYPE_FP32, ENTRY_ROUTE_BACKWARD, LAYOUT_ROW_MAJOR, Fp8Weights,
-                   MoeAdamw, MoeAdamwTensor, _call, _check, make_config, workspace_bytes)
+from ._lib import (DTYPE_BF16, DTYPE_FP32, ENTRY_ROUTE_BACKWARD, LAYOUT_ROW_MAJOR, Fp4Weights,
+                   Fp8Weights, MoeAdamw, MoeAdamwTensor, _call, _check, make_config,
+                   workspace_bytes)
 
 _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
 
@@ -494,8 +495,8 @@ class RouterTrainer:
             trainer.step()
 
     Between forward and backward x, w_router and topk_ids stay as they are.  Experts are
-    bf16 (w_gate_up, w_down in weight_layout), or Fp8Weights in the place of
-    w_gate_up with w_down None.  The hidden state's gradient is not computed: it
+    bf16 (w_gate_up, w_down in weight_layout), or Fp8Weights or Fp4Weights in the
+    place of w_gate_up with w_down None.  The hidden state's gradient is not computed: it
     would need the experts' own."""
 
     def __init__(self, w_router, w_gate_up, w_down=None, *, sel_bias=None, num_groups=8,
@@ -525,6 +526,8 @@ class RouterTrainer:
         _, offsets, src, dst = _lib.permute(ids, num_experts=self.w_router.shape[0])
         if isinstance(self.w_gate_up, Fp8Weights):
             y = _lib.expert_ffn_fp8(x, src, offsets, self.w_gate_up, topk=ids.shape[1])
+        elif isinstance(self.w_gate_up, Fp4Weights):
+            y = _lib.expert_ffn_fp4(x, src, offsets, self.w_gate_up, topk=ids.shape[1])
         else:
             y = _lib.expert_ffn(x, src, offsets, self.w_gate_up, self.w_down, topk=ids.shape[1],
                                 weight_layout=self.weight_layout)

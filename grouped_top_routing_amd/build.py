@@ -30,7 +30,8 @@ def clang_rt_dir() -> str:
         raise RuntimeError("clang's AddressSanitizer runtime was not found under /opt/rocm")
     return os.path.dirname(hits[-1])
 SOURCES = ["capi.hip", "route.hip", "permute.hip", "ffn.hip", "ffn_fp8.hip", "lora.hip", "combine.hip",
-           "rows.hip", "route_grad.hip", "adamw.hip", "capi_train.hip"]
+           "rows.hip", "route_grad.hip", "adamw.hip", "capi_train.hip", "select.hip", "capi_select.hip",
+           "ffn_fp4.hip"]
 ARCH = "gfx950"
 
 

@@ -19,13 +19,16 @@ using namespace beam;
 int mb_for(const moe_config_t* c) { return ffn_choose_mb(pairs(c), c->num_experts); }
 int mb_for_fp8(const moe_config_t* c) { return ffn_fp8_choose_mb(pairs(c), c->num_experts); }
 
-// Upper bound on the m-tiles of either weight format's plan (one workspace
-// size serves the bf16 and the fp8 entry points).
+int mb_for_fp4(const moe_config_t* c) { return ffn_fp4_choose_mb(pairs(c), c->num_experts); }
+
+// Upper bound on the m-tiles of the plan (one workspace size serves the bf16
+// and the fp8 entry points; the 4-bit layout has its own).
 int64_t max_tiles_for(const moe_config_t* c) {
   const int64_t n = pairs(c);
   int64_t bmax = ffn_rows_per_tile(mb_for(c));
   const int64_t b8 = ffn_rows_per_tile(mb_for_fp8(c));
   if (b8 < bmax) bmax = b8;
+  if (c->weight_layout == MOE_LAYOUT_FP4_PACKED) bmax = ffn_rows_per_tile(mb_for_fp4(c));
   return n / bmax + (n < c->num_experts ? n : c->num_experts) + 1;
 }
 
@@ -236,6 +239,43 @@ bool fp8_weights_ok(const uint8_t* q, const float* sc) {
   return q && sc && aligned16(q) && aligned4(sc);
 }
 
+// ---- 4-bit expert weights ----
+struct Fp4Matrix {
+  const uint8_t* q;
+  const uint8_t* s;
+  bool ok() const { return q && s && aligned16(q) && aligned16(s); }
+};
+
+int do_gate_up_fp4(const moe_config_t* c, const uint16_t* x, const int32_t* psrc,
+                   const int32_t* plan, const Fp4Matrix& w, uint16_t* h, hipStream_t s) {
+  return hip_status(launch_grouped_gemm_fp4(mb_for_fp4(c), true, x, psrc, c->topk, w.q, w.s, h,
+                                            plan, (int)max_tiles_for(c), c->hidden,
+                                            c->intermediate, c->intermediate, s,
+                                            bounds_of(c, true)));
+}
+
+int do_down_fp4(const moe_config_t* c, const uint16_t* h, const int32_t* plan, const Fp4Matrix& w,
+                uint16_t* y, hipStream_t s) {
+  return hip_status(launch_grouped_gemm_fp4(mb_for_fp4(c), false, h, nullptr, c->topk, w.q, w.s, y,
+                                            plan, (int)max_tiles_for(c), c->intermediate,
+                                            c->hidden, 0, s, bounds_of(c, false)));
+}
+
+int do_ffn_fp4(const moe_config_t* c, const uint16_t* x, const int32_t* psrc,
+               const int32_t* offsets, const Fp4Matrix& gu, const Fp4Matrix& down, uint16_t* y,
+               void* scratch, hipStream_t s) {
+  int32_t* plan = static_cast<int32_t*>(scratch);
+  uint16_t* h = reinterpret_cast<uint16_t*>(static_cast<char*>(scratch) + plan_bytes(c));
+  int st = do_plan(c, offsets, plan, mb_for_fp4(c), s);
+  if (st) return st;
+  if ((st = do_gate_up_fp4(c, x, psrc, plan, gu, h, s))) return st;
+  return do_down_fp4(c, h, plan, down, y, s);
+}
+
+// Bytes of a code and a scale array of n weights.
+int64_t codes4(int64_t n) { return n / 2; }
+int64_t scales4(int64_t n) { return n / 32; }
+
 // The whole block around an expert-MLP step `ffn(x, psrc, offsets, y, scratch)`.
 template <class Ffn>
 int layer_common(const moe_config_t* cfg, const uint16_t* x, const float* w_router,
@@ -308,6 +348,12 @@ int noalloc_scratch(void** out) {
 }
 
 }  // namespace
+
+namespace beam {
+
+size_t route_workspace(const moe_config_t* c) { return route_ws(c); }
+
+}  // namespace beam
 
 extern "C" {
 
@@ -528,7 +574,7 @@ int moe_debug_check_flags(uint32_t* flags) {
 #if BEAM_MOE_CHECKED
   if (device_ready()) return MOE_ERR_HIP;
   if (hipDeviceSynchronize() != hipSuccess) return MOE_ERR_HIP;
-  *flags = check_flags_permute() | check_flags_ffn() | check_flags_combine();
+  *flags = check_flags_permute() | check_flags_ffn() | check_flags_ffn_fp4() | check_flags_combine();
   return MOE_OK;
 #else
   return MOE_ERR_UNSUPPORTED;
@@ -665,6 +711,141 @@ int moe_layer_forward_fp8(const moe_config_t* cfg, const uint16_t* x, const floa
                       workspace_bytes, s,
                       [&](const int32_t* psrc, const int32_t* offsets, uint16_t* y, void* scratch) {
                         return do_ffn_fp8(cfg, x, psrc, offsets, w, y, scratch, s);
+                      });
+}
+
+int moe_quantize_fp4(const moe_config_t* cfg, const uint16_t* w_gate_up, const uint16_t* w_down,
+                     uint8_t* q_gate_up, uint8_t* s_gate_up, uint8_t* q_down, uint8_t* s_down,
+                     void* stream) {
+  moe_config_t c = cfg ? *cfg : moe_config_t{};
+  c.num_tokens = 0;
+  c.weight_layout = MOE_LAYOUT_ROW_MAJOR;  // not read here
+  int st = validate(cfg ? &c : nullptr);
+  if (st) return st;
+  const bool gu = w_gate_up || q_gate_up || s_gate_up;
+  const bool dn = w_down || q_down || s_down;
+  const Fp4Matrix mg{q_gate_up, s_gate_up}, md{q_down, s_down};
+  if ((gu && (!w_gate_up || !aligned16(w_gate_up) || !mg.ok())) ||
+      (dn && (!w_down || !aligned16(w_down) || !md.ok())))
+    return MOE_ERR_INVALID_ARG;
+  const int64_t E = c.num_experts, H = c.hidden, I = c.intermediate;
+  const int64_t ngu = E * 2 * I * H, ndn = E * H * I;
+  if (!apart({{q_gate_up, codes4(ngu)}, {s_gate_up, scales4(ngu)}, {q_down, codes4(ndn)},
+              {s_down, scales4(ndn)}},
+             {{w_gate_up, 2 * ngu}, {w_down, 2 * ndn}}))
+    return MOE_ERR_INVALID_ARG;
+  if (!gu && !dn) return MOE_OK;
+  if ((st = device_ready())) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (gu && (st = hip_status(launch_quantize_fp4(w_gate_up, q_gate_up, s_gate_up, (int)E,
+                                                 (int)(2 * I), (int)H, s))))
+    return st;
+  if (dn && (st = hip_status(launch_quantize_fp4(w_down, q_down, s_down, (int)E, (int)H, (int)I, s))))
+    return st;
+  return MOE_OK;
+}
+
+int moe_pack_fp4(const moe_config_t* cfg, const uint8_t* c_gate_up, const uint8_t* r_gate_up,
+                 const uint8_t* c_down, const uint8_t* r_down, uint8_t* q_gate_up,
+                 uint8_t* s_gate_up, uint8_t* q_down, uint8_t* s_down, void* stream) {
+  moe_config_t c = cfg ? *cfg : moe_config_t{};
+  c.num_tokens = 0;
+  c.weight_layout = MOE_LAYOUT_ROW_MAJOR;  // not read here
+  int st = validate(cfg ? &c : nullptr);
+  if (st) return st;
+  const bool gu = c_gate_up || r_gate_up || q_gate_up || s_gate_up;
+  const bool dn = c_down || r_down || q_down || s_down;
+  const Fp4Matrix ig{c_gate_up, r_gate_up}, id{c_down, r_down};
+  const Fp4Matrix og{q_gate_up, s_gate_up}, od{q_down, s_down};
+  if ((gu && (!ig.ok() || !og.ok())) || (dn && (!id.ok() || !od.ok()))) return MOE_ERR_INVALID_ARG;
+  const int64_t E = c.num_experts, H = c.hidden, I = c.intermediate;
+  const int64_t ngu = E * 2 * I * H, ndn = E * H * I;
+  if (!apart({{q_gate_up, codes4(ngu)}, {s_gate_up, scales4(ngu)}, {q_down, codes4(ndn)},
+              {s_down, scales4(ndn)}},
+             {{c_gate_up, codes4(ngu)}, {r_gate_up, scales4(ngu)}, {c_down, codes4(ndn)},
+              {r_down, scales4(ndn)}}))
+    return MOE_ERR_INVALID_ARG;
+  if (!gu && !dn) return MOE_OK;
+  if ((st = device_ready())) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (gu && (st = hip_status(launch_pack_fp4(c_gate_up, r_gate_up, q_gate_up, s_gate_up, (int)E,
+                                             (int)(2 * I), (int)H, s))))
+    return st;
+  if (dn && (st = hip_status(launch_pack_fp4(c_down, r_down, q_down, s_down, (int)E, (int)H,
+                                             (int)I, s))))
+    return st;
+  return MOE_OK;
+}
+
+int moe_expert_ffn_fp4(const moe_config_t* cfg, const uint16_t* x, const int32_t* perm_src,
+                       const int32_t* offsets, const uint8_t* q_gate_up, const uint8_t* s_gate_up,
+                       const uint8_t* q_down, const uint8_t* s_down, uint16_t* y_perm,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  int st = validate(cfg, kFp4Layouts);
+  if (st) return st;
+  const Fp4Matrix gu{q_gate_up, s_gate_up}, down{q_down, s_down};
+  if (!x || !perm_src || !offsets || !y_perm || !gu.ok() || !down.ok()) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(y_perm) || !aligned4(perm_src) || !aligned4(offsets))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_ws(workspace, workspace_bytes, ffn_ws(cfg)))) return st;
+  if (cfg->num_tokens == 0) return MOE_OK;
+  if ((st = device_ready())) return st;
+  return do_ffn_fp4(cfg, x, perm_src, offsets, gu, down, y_perm, workspace,
+                    static_cast<hipStream_t>(stream));
+}
+
+int moe_expert_gate_up_fp4(const moe_config_t* cfg, const uint16_t* x, const int32_t* perm_src,
+                           const int32_t* offsets, const uint8_t* q_gate_up,
+                           const uint8_t* s_gate_up, uint16_t* h, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  int st = validate(cfg, kFp4Layouts);
+  if (st) return st;
+  const Fp4Matrix gu{q_gate_up, s_gate_up};
+  if (!x || !perm_src || !offsets || !h || !gu.ok()) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(h) || !aligned4(perm_src) || !aligned4(offsets))
+    return MOE_ERR_INVALID_ARG;
+  if ((st = check_ws(workspace, workspace_bytes, plan_bytes(cfg)))) return st;
+  if (cfg->num_tokens == 0) return MOE_OK;
+  if ((st = device_ready())) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  int32_t* plan = static_cast<int32_t*>(workspace);
+  if ((st = do_plan(cfg, offsets, plan, mb_for_fp4(cfg), s))) return st;
+  return do_gate_up_fp4(cfg, x, perm_src, plan, gu, h, s);
+}
+
+int moe_expert_down_fp4(const moe_config_t* cfg, const uint16_t* h, const int32_t* offsets,
+                        const uint8_t* q_down, const uint8_t* s_down, uint16_t* y_perm,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  int st = validate(cfg, kFp4Layouts);
+  if (st) return st;
+  const Fp4Matrix down{q_down, s_down};
+  if (!h || !offsets || !y_perm || !down.ok()) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(h) || !aligned16(y_perm) || !aligned4(offsets)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_ws(workspace, workspace_bytes, plan_bytes(cfg)))) return st;
+  if (cfg->num_tokens == 0) return MOE_OK;
+  if ((st = device_ready())) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  int32_t* plan = static_cast<int32_t*>(workspace);
+  if ((st = do_plan(cfg, offsets, plan, mb_for_fp4(cfg), s))) return st;
+  return do_down_fp4(cfg, h, plan, down, y_perm, s);
+}
+
+int moe_layer_forward_fp4(const moe_config_t* cfg, const uint16_t* x, const float* w_router,
+                          const float* sel_bias, const uint8_t* q_gate_up,
+                          const uint8_t* s_gate_up, const uint8_t* q_down, const uint8_t* s_down,
+                          uint16_t* out, int32_t* topk_ids_out, float* topk_w_out,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  int st = validate(cfg, kFp4Layouts);
+  if (st) return st;
+  const Fp4Matrix gu{q_gate_up, s_gate_up}, down{q_down, s_down};
+  if (!layer_args_ok(cfg, x, w_router, sel_bias, out, topk_ids_out, topk_w_out) || !gu.ok() ||
+      !down.ok())
+    return MOE_ERR_INVALID_ARG;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return layer_common(cfg, x, w_router, sel_bias, out, topk_ids_out, topk_w_out, workspace,
+                      workspace_bytes, s,
+                      [&](const int32_t* psrc, const int32_t* offsets, uint16_t* y, void* scratch) {
+                        return do_ffn_fp4(cfg, x, psrc, offsets, gu, down, y, scratch, s);
                       });
 }
 

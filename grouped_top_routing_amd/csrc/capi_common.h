@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
+#include <initializer_list>
 
 #include "../../include/beam_moe.h"
 
@@ -22,7 +23,8 @@ inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3
 // Weight layouts an entry point accepts (bit i = layout i).
 constexpr int kBf16Layouts = (1 << MOE_LAYOUT_ROW_MAJOR) | (1 << MOE_LAYOUT_PACKED);
 constexpr int kFp8Layouts = 1 << MOE_LAYOUT_FP8_PACKED;
-constexpr int kAnyLayout = kBf16Layouts | kFp8Layouts;
+constexpr int kFp4Layouts = 1 << MOE_LAYOUT_FP4_PACKED;
+constexpr int kAnyLayout = kBf16Layouts | kFp8Layouts | kFp4Layouts;
 
 inline int validate(const moe_config_t* c, int layouts = kBf16Layouts) {
   if (!c) return MOE_ERR_INVALID_ARG;
@@ -32,7 +34,8 @@ inline int validate(const moe_config_t* c, int layouts = kBf16Layouts) {
   if (c->renormalize != 0 && c->renormalize != 1) return MOE_ERR_INVALID_ARG;
   if (!std::isfinite(c->routed_scaling)) return MOE_ERR_INVALID_ARG;
   if (c->num_experts % c->num_groups != 0) return MOE_ERR_INVALID_ARG;
-  if (c->weight_layout < 0 || c->weight_layout > 2 || !((layouts >> c->weight_layout) & 1))
+  if (c->weight_layout < 0 || c->weight_layout > MOE_LAYOUT_FP4_PACKED ||
+      !((layouts >> c->weight_layout) & 1))
     return MOE_ERR_INVALID_ARG;
   if (c->topk_groups > c->num_groups) return MOE_ERR_INVALID_ARG;
   if ((int64_t)c->topk > (int64_t)c->topk_groups * (c->num_experts / c->num_groups))
@@ -56,6 +59,29 @@ inline int check_ws(void* ws, size_t have, size_t need) {
 }
 
 inline int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
+
+// Whether no output overlaps an input or another output (null: not given).
+// The kernels read and write them in no order.
+struct Span {
+  const void* at;
+  int64_t bytes;
+  bool meets(const Span& o) const {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(at), b = reinterpret_cast<uintptr_t>(o.at);
+    return at && o.at && (a < b ? b - a < (uint64_t)bytes : a - b < (uint64_t)o.bytes);
+  }
+};
+inline bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (o->meets(i)) return false;
+    for (const Span* p = outs.begin(); p != o; ++p)
+      if (o->meets(*p)) return false;
+  }
+  return true;
+}
+
+// Workspace of moe_route and its kin (capi.hip).
+size_t route_workspace(const moe_config_t* c);
 
 // Workspace of moe_route_backward (capi_train.hip).
 size_t route_backward_ws(const moe_config_t* c);

@@ -3,7 +3,6 @@
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
-#include <initializer_list>
 
 #include "../../include/beam_moe.h"
 #include "capi_common.h"
@@ -32,26 +31,6 @@ int validate_rows(const moe_config_t* c, int dtype) {
   if (c->num_tokens >= ((int64_t)1 << 31) || pairs(c) >= ((int64_t)1 << 31))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
-}
-
-// Whether no output overlaps an input or another output (null: not given).
-// The kernels read and write them in no order.
-struct Span {
-  const void* at;
-  int64_t bytes;
-  bool meets(const Span& o) const {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(at), b = reinterpret_cast<uintptr_t>(o.at);
-    return at && o.at && (a < b ? b - a < (uint64_t)bytes : a - b < (uint64_t)o.bytes);
-  }
-};
-bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
-  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
-    for (const Span& i : ins)
-      if (o->meets(i)) return false;
-    for (const Span* p = outs.begin(); p != o; ++p)
-      if (o->meets(*p)) return false;
-  }
-  return true;
 }
 
 // Bytes of the row calls' arguments.

@@ -195,6 +195,17 @@ __device__ __forceinline__ uint32_t fp8x2_to_bf16x2(uint32_t w) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
 }
 
+// Eight E2M1 codes (the lowest in the low bits) times `scale`, a power of two,
+// widened to bf16: exact, since a code has two mantissa bits.
+__device__ __forceinline__ bf16x8_t widen_fp4(uint32_t w, float scale) {
+  uint4 o;
+  o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0));
+  o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1));
+  o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2));
+  o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3));
+  return as_bf16x8(o);
+}
+
 // One direct global -> LDS load: lane l's 16 bytes at `g` land at LDS byte
 // address lds_addr + 16*l (lds_addr must be wave-uniform; it goes in M0).
 // Issued from inline asm so the compiler's own wait-count pass does not see

@@ -89,8 +89,20 @@ hipError_t launch_grouped_gemm_fp8_paired(int mb, bool swiglu, const uint16_t* A
 hipError_t launch_quantize_fp8(const uint16_t* w, uint8_t* q, float* scales, int E, int N, int K,
                                hipStream_t stream);
 
+// 4-bit expert weights (ffn_fp4.hip): code and scale fragments.
+int ffn_fp4_choose_mb(int64_t rows, int E);
+hipError_t launch_grouped_gemm_fp4(int mb, bool swiglu, const uint16_t* A, const int32_t* gather,
+                                   int topk, const uint8_t* Q, const uint8_t* S, uint16_t* C,
+                                   const int32_t* plan, int max_tiles, int K, int n_out,
+                                   int up_row0, hipStream_t stream, const GemmBounds& bounds);
+hipError_t launch_quantize_fp4(const uint16_t* w, uint8_t* q, uint8_t* s, int E, int N, int K,
+                               hipStream_t stream);
+hipError_t launch_pack_fp4(const uint8_t* codes, const uint8_t* scales, uint8_t* q, uint8_t* s,
+                           int E, int N, int K, hipStream_t stream);
+
 // Checked builds: each translation unit's check-flag word, read and cleared
 // (always 0 in the normal build).
+uint32_t check_flags_ffn_fp4();
 uint32_t check_flags_permute();
 uint32_t check_flags_ffn();
 uint32_t check_flags_combine();
@@ -128,6 +140,26 @@ hipError_t launch_route_backward(const uint16_t* x, const float* wr, const int32
                                  const uint16_t* add, float* grad_w, int accumulate,
                                  uint16_t* grad_x, int64_t T, int H, int topk, int renormalize,
                                  void* dz, int32_t* plan, float* part, hipStream_t stream);
+
+// Routing from logits (select.hip); fp32: the logits are fp32, else bf16.
+constexpr int kSelectMaxExperts = 1024, kSelectMaxTopk = 32, kSelectMaxGroups = 64;
+struct SelectShape {
+  int experts, groups, topk_groups, group_best, topk, softmax, renormalize;
+};
+// logits: `parts` arrays [T, E] to be added in order; zout (fp32 [T, E]) and
+// bias may be null
+hipError_t launch_select_experts(bool fp32, const void* logits, int parts, const float* bias,
+                                 int32_t* ids, float* w, float* zout, int64_t T,
+                                 const SelectShape& c, hipStream_t stream);
+// grad (of the weights) or load (of the balance loss) may be null, not both;
+// grad_loss null: 1
+hipError_t launch_select_backward(bool fp32, const void* logits, const int32_t* ids,
+                                  const float* grad, const float* load, const float* grad_loss,
+                                  void* out, int64_t T, const SelectShape& c, hipStream_t stream);
+size_t balance_ws(int64_t T, int E);
+hipError_t launch_balance_loss(bool fp32, const void* logits, const int32_t* ids, float coef,
+                               float* loss, float* load, void* ws, int64_t T, const SelectShape& c,
+                               hipStream_t stream);
 
 // AdamW (adamw.hip).
 constexpr int kAdamTensors = 40;  // tensors per launch: their list is the kernel's argument

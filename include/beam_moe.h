@@ -87,8 +87,8 @@ typedef struct moe_config {
   int32_t weight_layout;  /* expert weight storage: MOE_LAYOUT_ROW_MAJOR or
                              MOE_LAYOUT_PACKED (written by moe_pack_weights) for
                              the bf16 expert calls, MOE_LAYOUT_FP8_PACKED for the
-                             *_fp8 calls; calls that read no expert weights
-                             accept any of the three                              */
+                             *_fp8 calls, MOE_LAYOUT_FP4_PACKED for the *_fp4
+                             calls; calls that read no expert weights accept any */
 } moe_config_t;
 
 /* Expert weight layouts. */
@@ -98,8 +98,10 @@ enum moe_weight_layout {
                                 [N/16][K/32][64][8]: the 16 x 32 bf16 operand tiles of
                                 the gfx950 matrix cores, lane-ordered, consecutive
                                 along K (see moe_pack_weights)                        */
-  MOE_LAYOUT_FP8_PACKED = 2  /* E4M3FN codes plus fp32 per-row scales (see
+  MOE_LAYOUT_FP8_PACKED = 2, /* E4M3FN codes plus fp32 per-row scales (see
                                 moe_quantize_fp8)                                     */
+  MOE_LAYOUT_FP4_PACKED = 4  /* E2M1 codes plus E8M0 scales per 32 weights (see
+                                moe_quantize_fp4); 3 names no layout                  */
 };
 
 /* Bytes of workspace `entry` needs for `cfg` (written to *bytes). */
@@ -286,6 +288,70 @@ int moe_layer_forward_fp8(const moe_config_t* cfg, const uint16_t* x, const floa
                           const float* sel_bias, const uint8_t* q_gate_up, const float* s_gate_up,
                           const uint8_t* q_down, const float* s_down, uint16_t* out,
                           int32_t* topk_ids_out, float* topk_w_out,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * 4-bit expert weights with group scales (E2M1 codes with one E8M0 scale per 32
+ * weights, the microscaling format MXFP4): 4.25 bits per weight.
+ *
+ * Each expert matrix row n (output channel) has E2M1 codes q[n, k] (1 sign, 2
+ * exponent, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6) and one E8M0 scale s[n,
+ * k / 32]; the matrix the GEMMs use is w[n, k] = 2^(s - 127) * q[n, k], exact
+ * in bf16 (s = 255 is NaN; a value past the largest bf16 is infinite).
+ * Activations stay bf16, accumulation fp32.  The router, selection, permutation
+ * and combine are the bf16 path's.
+ *
+ * Row-major form (moe_pack_fp4's input): codes [E, N, K / 2], two per byte, the
+ * lower k in the low half; scales [E, N, K / 32].
+ * Packed form (MOE_LAYOUT_FP4_PACKED), the same sizes: each expert's codes as
+ * [N/16][K/128][64][4][4 bytes], entry (b, t, l, s) holding the codes of row
+ * 16b + l%16 at k = 128t + 32s + 8(l/16) .. +7, lower k in lower bits; its
+ * scales as [N/16][K/128][16][4 bytes], entry (b, t, r, s) that of row 16b + r
+ * at k = 128t + 32s.
+ *   q_gate_up [E, 2*I, H / 2] bytes, s_gate_up [E, 2*I, H / 32]
+ *   q_down    [E, H, I / 2]   bytes, s_down    [E, H, I / 32]
+ * Codes and scales are 16-byte aligned.  The *_fp4 calls require
+ * cfg->weight_layout == MOE_LAYOUT_FP4_PACKED (else MOE_ERR_INVALID_ARG); their
+ * workspace sizes are the ones moe_workspace_bytes gives for that layout and
+ * MOE_ENTRY_EXPERT_FFN, MOE_ENTRY_EXPERT_STAGE and MOE_ENTRY_LAYER.
+ */
+/*
+ * Quantise row-major bf16 expert weights into the packed form.  The scale of a
+ * group is the least power of two, at least 2^-126, by which its largest
+ * magnitude is at most 7 (so that no weight is off by more than half a step);
+ * codes are to the nearest, ties to the even code, magnitudes above 6 to 6.  A
+ * group with an infinity or a NaN gets the scale NaN.
+ *   w_gate_up, w_down  row-major bf16 inputs [E, 2I, H], [E, H, I]
+ *   q_*, s_*           outputs as above; must not overlap the inputs or each other
+ * Either set (w, q, s) may be all NULL to skip it.  num_tokens and
+ * weight_layout are ignored.
+ */
+int moe_quantize_fp4(const moe_config_t* cfg, const uint16_t* w_gate_up, const uint16_t* w_down,
+                     uint8_t* q_gate_up, uint8_t* s_gate_up, uint8_t* q_down, uint8_t* s_down,
+                     void* stream);
+/* The packed form of row-major codes c_* and scales r_* (arguments otherwise as
+ * in moe_quantize_fp4). */
+int moe_pack_fp4(const moe_config_t* cfg, const uint8_t* c_gate_up, const uint8_t* r_gate_up,
+                 const uint8_t* c_down, const uint8_t* r_down, uint8_t* q_gate_up,
+                 uint8_t* s_gate_up, uint8_t* q_down, uint8_t* s_down, void* stream);
+
+/* moe_expert_ffn, moe_expert_gate_up, moe_expert_down and moe_layer_forward
+ * with 4-bit expert weights (arguments as in those calls). */
+int moe_expert_ffn_fp4(const moe_config_t* cfg, const uint16_t* x, const int32_t* perm_src,
+                       const int32_t* offsets, const uint8_t* q_gate_up, const uint8_t* s_gate_up,
+                       const uint8_t* q_down, const uint8_t* s_down, uint16_t* y_perm,
+                       void* workspace, size_t workspace_bytes, void* stream);
+int moe_expert_gate_up_fp4(const moe_config_t* cfg, const uint16_t* x, const int32_t* perm_src,
+                           const int32_t* offsets, const uint8_t* q_gate_up,
+                           const uint8_t* s_gate_up, uint16_t* h,
+                           void* workspace, size_t workspace_bytes, void* stream);
+int moe_expert_down_fp4(const moe_config_t* cfg, const uint16_t* h, const int32_t* offsets,
+                        const uint8_t* q_down, const uint8_t* s_down, uint16_t* y_perm,
+                        void* workspace, size_t workspace_bytes, void* stream);
+int moe_layer_forward_fp4(const moe_config_t* cfg, const uint16_t* x, const float* w_router,
+                          const float* sel_bias, const uint8_t* q_gate_up,
+                          const uint8_t* s_gate_up, const uint8_t* q_down, const uint8_t* s_down,
+                          uint16_t* out, int32_t* topk_ids_out, float* topk_w_out,
                           void* workspace, size_t workspace_bytes, void* stream);
 
 /*
@@ -487,6 +553,105 @@ typedef struct moe_adamw {
 /* `tensors`: host array, read during the call.  Tensors must not overlap. */
 int moe_adamw_step(const moe_adamw_t* opt, const moe_adamw_tensor_t* tensors, int num_tensors,
                    void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Routing from logits: softmax or sigmoid scores over any number of experts,
+ * its gradient, and the loss that balances the experts' load.
+ *
+ * With z the logits of a token and b an optional selection bias:
+ *   s_e = 1 / (1 + exp(-z_e))              MOE_SCORE_SIGMOID
+ *   s_e = exp(z_e) / sum_i exp(z_i)        MOE_SCORE_SOFTMAX
+ *   v_e = s_e + b_e
+ * A group's score is the sum of its group_best (1 or 2) largest v; the
+ * topk_groups best groups are kept and the topk largest v in them chosen, in
+ * descending order.  Values are compared in 64 bits; without a bias experts
+ * are ordered by their logits.  Ties go to the lower index.
+ *   A logit of -inf masks its expert, and so does a bias of -inf or NaN: it is
+ * never chosen.  Where fewer than topk experts are left, the last slots get id
+ * -1 and weight 0, as moe_permute and moe_combine drop them.  A logit of +inf
+ * counts as the largest finite number.  A NaN logit is not chosen and makes
+ * its row's weights, and its row's part of the gradient and of the loss, NaN.
+ *
+ * Limits: num_experts <= 1024, num_groups <= 64 (a divisor of num_experts),
+ * topk <= 32, num_tokens < 2^26; others return MOE_ERR_UNSUPPORTED.  Logits and
+ * their gradient are dense [T, E] of logits_dtype and need only the alignment
+ * of their elements.  Outputs that overlap an input or each other are refused.
+ */
+enum moe_score { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };
+
+typedef struct moe_select_config {
+  int64_t num_tokens;   /* T >= 0                                                */
+  int32_t num_experts;  /* E                                                     */
+  int32_t num_groups;   /* groups of E / num_groups contiguous experts           */
+  int32_t topk_groups;  /* groups kept                                           */
+  int32_t group_best;   /* 1 or 2: values that a group's score adds              */
+  int32_t topk;         /* at most the experts of the kept groups                */
+  int32_t score;        /* moe_score                                             */
+  int32_t renormalize;  /* 1: weight = s over the sum of the chosen s; 0: s      */
+  int32_t logits_dtype; /* moe_dtype                                             */
+} moe_select_config_t;
+
+/*
+ *   logits    [T, E]
+ *   sel_bias  [E] fp32 or NULL: for choosing only
+ *   topk_ids  [T, topk] int32 out, topk_w [T, topk] fp32 out
+ */
+int moe_select(const moe_select_config_t* cfg, const void* logits, const float* sel_bias,
+               int32_t* topk_ids, float* topk_w, void* stream);
+
+/*
+ * moe_select on the logits of the block's router, x . W_r^T in FP32 as
+ * moe_route computes them.  cfg gives num_tokens and hidden (shapes as in
+ * moe_route), sel the selection, with cfg's num_tokens, 256 experts and fp32
+ * logits.
+ *   logits  [T, E] fp32 out or NULL: what moe_select_backward starts from
+ * Workspace MOE_ENTRY_ROUTE of cfg.
+ */
+int moe_route_select(const moe_config_t* cfg, const moe_select_config_t* sel, const uint16_t* x,
+                     const float* w_router, const float* sel_bias, int32_t* topk_ids,
+                     float* topk_w, float* logits, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/*
+ * Balance loss over the rows with an expert (an id in [0, E); T' of them).
+ * With n_e the pairs of expert e, n their sum, and q the scores over their sum
+ * over all experts (the softmax itself, or the sigmoids normalised):
+ *   f_e = E n_e / n,   P_e = sum_t q_te / T',   loss = coef * sum_e f_e P_e
+ *   load_e = coef f_e / T'
+ * load is the loss's derivative by every q_te (f is a count: no gradient).
+ *   topk_ids  [T, topk] int32 in
+ *   loss      [1] fp32 out, load [E] fp32 out (zeros without such rows)
+ * Sums by expert are fp32 within a workgroup's tokens and 64 bits across them,
+ * in a fixed order.  With no tokens nothing is written.  Workspace:
+ * moe_balance_workspace_bytes.  Reads num_tokens, num_experts, topk, score and
+ * logits_dtype of cfg.
+ */
+int moe_balance_workspace_bytes(const moe_select_config_t* cfg, size_t* bytes);
+int moe_balance_loss(const moe_select_config_t* cfg, const void* logits, const int32_t* topk_ids,
+                     float coef, float* loss, float* load, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of the weights of moe_select, and of moe_balance_loss, with respect
+ * to all logits.  With g = grad_topk_w and C a row's slots that name an expert:
+ *   sigmoid:                dz_e = s_e (1 - s_e) sum_{j of e} g_j
+ *   sigmoid, renormalized:  dz_e = (1 - s_e) sum_{j of e} w_j (g_j - sum_C g_i w_i)
+ *   softmax:                dz_e = s_e (sum_{j of e} g_j - sum_C g_i s_i)
+ *   softmax, renormalized:  dz_e = sum_{j of e} w_j (g_j - sum_C g_i w_i)
+ *   balance loss:           + grad_loss q_e (load_e - sum_i load_i q_i), times
+ *                           (1 - s_e) for the sigmoid
+ * Rows without such a slot get zeros.  The selection has no gradient.
+ *   topk_ids     [T, topk] int32, in any order, repeated ones added up
+ *   grad_topk_w  [T, topk] fp32, or NULL with load: no gradient of the weights
+ *   load         [E] fp32 of moe_balance_loss, or NULL: no balance loss
+ *   grad_loss    [1] fp32 on the device, or NULL: 1 (only with load)
+ *   grad_logits  [T, E] out
+ * Reads num_tokens, num_experts, topk, score, renormalize and logits_dtype of cfg.
+ */
+int moe_select_backward(const moe_select_config_t* cfg, const void* logits,
+                        const int32_t* topk_ids, const float* grad_topk_w, const float* load,
+                        const float* grad_loss, void* grad_logits, void* stream);
 
 /* Static description of a status code; never NULL. */
 const char* moe_status_string(int status);
