@@ -121,121 +121,408 @@ __global__ __launch_bounds__(256) void pack_fp4_kernel(const uint8_t* __restrict
 }
 
 // ---------------------------------------------------------------------------
-// A work item is an m-tile of up to 64 rows of one expert times 256 of its
-// weight rows (gate/up: 128 gate rows and the matching up rows).  Wave w of
-// four takes column blocks 4w .. 4w + 3 (gate/up: gate blocks 2w, 2w + 1 and
-// their up blocks).  Operands go straight from global memory to registers.
-constexpr int kRowBlocks = 4;
-constexpr int kColBlocks = 4;  // per wave
+// The grouped GEMM.  A work item is an m-tile (up to 16 MB rows of one expert)
+// times 256 of its weight rows (gate/up: 128 gate rows and the matching up
+// rows), walked by a persistent grid.
+//
+// Waves form RG row groups x 4 column groups: a wave computes 4 column blocks
+// (gate/up: 2 gate blocks and their up blocks) for its share of the item's
+// 16-row blocks.  Codes, scales and rows are staged in LDS by direct loads:
+//   W stage q: 128 k of the 16 blocks' code fragments (16 KB) and scales (1 KB),
+//              in slot q % SW
+//   A stage p: 64 k of the item's rows, 2 KB per row block, in slot p % SA; each
+//              row's 128 bytes with its 16-byte chunks swizzled by (row / 2) % 8,
+//              so that the 16 rows of an operand read hit distinct banks
+// A wave reads its codes of 128 k once (16 bytes per block and lane) and widens
+// them to bf16 operands in registers, 8 codes per MFMA step.
+//
+// Schedule.  Iteration p (64 k, two MFMA steps) waits for A(p + 1), and W((p + 1)
+// / 2) where that is new, passes a barrier, and refills the slots that every
+// wave has read by then: A(p + SA), then W(p / 2 + SW) for even p.  The loads
+// before the loop are those of iterations below 0 in the same order, so one
+// rule gives every wait (younger below).  A workgroup issues its next item's
+// first loads before the current item's outputs are written.
+constexpr int kBlocks = 16;      // weight-row blocks of an item
+constexpr int kCols = 4;         // column blocks per wave
+constexpr int kColGroups = kBlocks / kCols;
+constexpr int kSlotW = kBlocks * (kCodeB + kScaleB);
+constexpr int kBlockA = 2048;    // bytes of 64 k of a row block
 
-template <bool SWIGLU>
-__global__ __launch_bounds__(256) void gemm_fp4_kernel(
-    const uint16_t* __restrict__ A, const int32_t* __restrict__ gather, int topk,
-    const uint8_t* __restrict__ Q, const uint8_t* __restrict__ S, uint16_t* __restrict__ C,
-    const int32_t* __restrict__ plan, int max_tiles, int K, int n_out, int up_row0,
-    GemmBounds bounds) {
-  (void)bounds;
-  constexpr int HALF = SWIGLU ? kColBlocks / 2 : kColBlocks;
-  constexpr int WCOLS = 4 * HALF * 16;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane & 15, g = lane >> 4;
-  const int* plan_expert = plan + 4;
-  const int* plan_row0 = plan_expert + max_tiles;
-  const int* plan_rows = plan_row0 + max_tiles;
-  const int nt_n = n_out / WCOLS;
-  const int total = plan[0] * nt_n;
-  const int nst = K / kStageK;
-  const int64_t wrows = SWIGLU ? 2 * (int64_t)n_out : n_out;
-  for (int q = blockIdx.x; q < total; q += gridDim.x) {
-    const int tile = q / nt_n, ntile = q - tile * nt_n;
-    const int e = BEAM_CLAMP(plan_expert[tile], 0, bounds.n_experts - 1, kCheckPlanRows);
-    const int row0 = plan_row0[tile], nrows = plan_rows[tile];
-    const int nrb = (nrows + 15) >> 4;
-    const uint16_t* arow[kRowBlocks];
+// One direct global -> LDS load of 4 bytes per lane (see lds_dma16_sv).
+__device__ __forceinline__ void lds_dma4_sv(const void* base, uint32_t off, uint32_t lds_addr) {
+  lds_addr = __builtin_amdgcn_readfirstlane(lds_addr);
+  uint32_t saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %1, %3\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "v"(off), "s"(lds_addr), "s"(base)
+      : "memory");
+}
+
+__device__ __forceinline__ int a_chunk(int row) { return (row >> 1) & 7; }
+
+struct Fp4Args {
+  const uint16_t* A;
+  const int32_t* gather;
+  int topk;
+  const uint8_t* Q;
+  const uint8_t* S;
+  uint16_t* C;
+  const int32_t* plan;
+  int max_tiles, K, n_out, up_row0;
+  GemmBounds bounds;
+};
+
+template <int MB, int RG, int SA, int SW, bool SWIGLU>
+struct Fp4Gemm {
+  static constexpr int NW = kColGroups * RG;
+  static constexpr int NBL = kCols / RG;              // code fragments a wave loads per W stage
+  static constexpr int AMAX = (MB + NW - 1) / NW;     // row blocks a wave loads per A stage
+  static constexpr int RB = (MB + RG - 1) / RG;       // row blocks a wave computes, at most
+  static constexpr int HALF = SWIGLU ? kCols / 2 : kCols;
+  static constexpr int WCOLS = kColGroups * HALF * 16;
+  static constexpr int kLoadsW = NBL + 1;             // direct loads of a W stage per wave
+  static constexpr int kLds = SW * kSlotW + SA * MB * kBlockA;
+  static_assert(SA % 2 == 1 && 2 * SW > SA, "the waits count W stages by this");
+  static_assert(kLds <= 160 * 1024, "LDS");
+
+  const Fp4Args& a;
+  uint8_t* lds;
+  int lane, wave, r, g, cg, rg;
+  int nst, nw;                 // A and W stages of an item
+  // the item whose loads are in flight
+  int row0, nrows, ntile, na;
+  int src[AMAX][2];            // rows of A that this lane loads
+  const uint8_t* code[NBL];    // wave-uniform
+  const uint8_t* scale;
+  uint32_t scale_off;
+
+  __device__ __forceinline__ Fp4Gemm(const Fp4Args& args, uint8_t* mem) : a(args), lds(mem) {
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    r = lane & 15;
+    g = lane >> 4;
+    cg = wave % kColGroups;
+    rg = wave / kColGroups;
+    nst = a.K / 64;
+    nw = a.K / kStageK;
+  }
+
+  // first weight row of column block j of this wave
+  __device__ __forceinline__ int weight_row(int j) const {
+    return ntile * WCOLS + (cg * HALF + j % HALF) * 16 + (j >= HALF ? a.up_row0 : 0);
+  }
+
+  __device__ __forceinline__ uint32_t lds_base() const {
+    return (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)lds);
+  }
+
+  __device__ __forceinline__ void issue_a(int p) {
+    const int k0 = p * 64;
+    const uint32_t slot = lds_base() + SW * kSlotW + (uint32_t)(p % SA) * (MB * kBlockA);
 #pragma unroll
-    for (int i = 0; i < kRowBlocks; ++i) {
-      const int row = row0 + min(16 * i + r, nrows - 1);
-      const int src = gather
-          ? gather[BEAM_CLAMP(row, 0, bounds.n_rows - 1, kCheckGatherIndex)] / topk : row;
-      arow[i] = A + (size_t)BEAM_CLAMP(src, 0, bounds.n_src - 1, kCheckTokenIndex) * K + 8 * g;
-    }
-    // column block j of this wave: its first weight row
-    int64_t frag[kColBlocks];
+    for (int j = 0; j < AMAX; ++j)
+      if (j < na) {
 #pragma unroll
-    for (int j = 0; j < kColBlocks; ++j) {
-      const int col = ntile * WCOLS + (wave * HALF + j % HALF) * 16 + (j >= HALF ? up_row0 : 0);
-      frag[j] = ((int64_t)e * (wrows / 16) + BEAM_CLAMP(col / 16, 0, wrows / 16 - 1,
-                                                         kCheckWeightOffset)) * nst;
-    }
-    f32x4_t acc[kRowBlocks][kColBlocks];
-#pragma unroll
-    for (int i = 0; i < kRowBlocks; ++i)
-#pragma unroll
-      for (int j = 0; j < kColBlocks; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    for (int st = 0; st < nst; ++st) {
-      uint4 code[kColBlocks];
-      uint32_t scale[kColBlocks];
-#pragma unroll
-      for (int j = 0; j < kColBlocks; ++j) {
-        code[j] = ld16(Q + (frag[j] + st) * kCodeB + 16 * lane);
-        scale[j] = *reinterpret_cast<const uint32_t*>(S + (frag[j] + st) * kScaleB + 4 * r);
-      }
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        bf16x8_t b[kColBlocks];
-#pragma unroll
-        for (int j = 0; j < kColBlocks; ++j) {
-          const uint32_t w = s == 0 ? code[j].x : s == 1 ? code[j].y : s == 2 ? code[j].z : code[j].w;
-          b[j] = widen_fp4(w, e8m0_value((scale[j] >> (8 * s)) & 255u));
+        for (int hf = 0; hf < 2; ++hf) {
+          const int chunk = (lane & 7) ^ a_chunk(hf * 8 + (lane >> 3));
+          lds_dma16(a.A + (size_t)src[j][hf] * a.K + k0 + 8 * chunk,
+                    slot + (uint32_t)(wave + NW * j) * kBlockA + hf * 1024);
         }
+      }
+  }
+  __device__ __forceinline__ void issue_w(int q) {
+    BEAM_CHECK(q >= 0 && q < nw, kCheckWeightOffset);
+    const uint32_t slot = lds_base() + (uint32_t)(q % SW) * kSlotW;
 #pragma unroll
-        for (int i = 0; i < kRowBlocks; ++i)
-          if (i < nrb) {
-            const bf16x8_t a = as_bf16x8(ld16(arow[i] + st * kStageK + 32 * s));
+    for (int t = 0; t < NBL; ++t)
+      lds_dma16_sv<true>(code[t] + (size_t)q * kCodeB, (uint32_t)lane * 16u,
+                         slot + (uint32_t)(cg * kCols + rg + RG * t) * kCodeB);
+    // every wave of a column group loads its four blocks' scales: the same
+    // bytes to the same place, so that all waves count alike
+    lds_dma4_sv(scale + (size_t)q * kScaleB, scale_off,
+                slot + kBlocks * kCodeB + (uint32_t)(cg * kCols) * kScaleB);
+  }
+  // loads of iteration p
+  __device__ __forceinline__ void issue(int p) {
+    if (p + SA >= 0 && p + SA < nst) issue_a(p + SA);
+    if ((p & 1) == 0) {
+      const int q = (p >> 1) + SW;
+      if (q >= 0 && q < nw) issue_w(q);
+    }
+  }
+  // Waits for A(p + 1), and so for every older load: as many of this wave's
+  // loads may stay in flight as were issued after it, namely A(p + 2) .. A(p +
+  // SA - 1) and the W stages of the even iterations p + 1 - SA .. p - 1.
+  __device__ __forceinline__ void wait_next(int p) {
+    constexpr int kA = SA - 2, kW = (SA - 1) / 2;
+    const int last_w = ((p + 1) >> 1) - 1 + SW;  // of the latest even iteration below p
+    if (p + SA - 1 < nst && last_w < nw) {
+      if (na == AMAX) wait_vm<2 * AMAX * kA + kLoadsW * kW>();
+      else wait_vm<2 * (AMAX - 1) * kA + kLoadsW * kW>();
+    } else {
+      const int as = min(max(nst - 2 - p, 0), kA);
+      const int ws = min(max(nw - 1 - (last_w - kW), 0), kW);
+      wait_vm_dyn<0, 2 * AMAX * kA + kLoadsW * kW>(2 * na * as + kLoadsW * ws);
+    }
+  }
+
+  // Takes item `tile`, `nt` and issues its first loads.
+  __device__ __forceinline__ void start(int tile, int nt) {
+    const int* plan_expert = a.plan + 4;
+    const int* plan_row0 = plan_expert + a.max_tiles;
+    const int* plan_rows = plan_row0 + a.max_tiles;
+    const int e = BEAM_CLAMP(plan_expert[tile], 0, a.bounds.n_experts - 1, kCheckPlanRows);
+    row0 = plan_row0[tile];
+    nrows = plan_rows[tile];
+    ntile = nt;
+    BEAM_CHECK(nrows >= 1 && nrows <= 16 * MB && row0 >= 0 &&
+                   (int64_t)row0 + nrows <= a.bounds.n_rows, kCheckPlanRows);
+    const int nrb = (nrows + 15) >> 4;
+    na = (nrb - wave + NW - 1) / NW;
+    // Rows past the tile repeat its last.  The gather's indices are scalar
+    // loads of uniform addresses, which the vector memory counter that the
+    // rings are waited on with does not count.
 #pragma unroll
-            for (int j = 0; j < kColBlocks; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], a, acc[i][j], 0, 0, 0);
-          }
+    for (int j = 0; j < AMAX; ++j) {
+      const int blk = __builtin_amdgcn_readfirstlane((wave + NW * j) * 16);
+      if (a.gather) {
+        const __attribute__((address_space(4))) int32_t* cgather =
+            (const __attribute__((address_space(4))) int32_t*)a.gather;
+        int v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          v[k] = cgather[BEAM_CLAMP(row0 + min(blk + k, nrows - 1), 0, a.bounds.n_rows - 1,
+                                    kCheckGatherIndex)];
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          int x = v[8 * hf];
+#pragma unroll
+          for (int k = 1; k < 8; ++k) x = (lane >> 3) == k ? v[8 * hf + k] : x;
+          src[j][hf] = BEAM_CLAMP(x / a.topk, 0, a.bounds.n_src - 1, kCheckTokenIndex);
+        }
+      } else {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+          src[j][hf] = BEAM_CLAMP(row0 + min(blk + 8 * hf + (lane >> 3), nrows - 1), 0,
+                                  a.bounds.n_src - 1, kCheckTokenIndex);
       }
     }
-    // The weights are the first operand: lane (r, g) holds output columns
-    // 4g .. 4g + 3 of row r.
+    const int64_t blocks = (SWIGLU ? 2 * (int64_t)a.n_out : a.n_out) / 16;
+    const int64_t first = (int64_t)e * blocks;
 #pragma unroll
-    for (int i = 0; i < kRowBlocks; ++i) {
-      const int row = 16 * i + r;
-      if (row >= nrows) continue;
+    for (int t = 0; t < NBL; ++t)
+      code[t] = a.Q + (first + BEAM_CLAMP(weight_row(rg + RG * t) >> 4, 0, blocks - 1,
+                                          kCheckWeightOffset)) * nw * kCodeB;
+    scale = a.S + first * nw * kScaleB;
+    // lane l loads the scales of row l % 16 of column block l / 16
+    int block = 0;
 #pragma unroll
-      for (int j = 0; j < HALF; ++j) {
+    for (int j = 0; j < kCols; ++j) block = g == j ? weight_row(j) >> 4 : block;
+    scale_off = (uint32_t)block * (uint32_t)(nw * kScaleB) + (uint32_t)r * 4u;
+    constexpr int kFirst = SA > 2 * SW ? SA : 2 * SW;
+#pragma unroll
+    for (int p = -kFirst; p < 0; ++p) issue(p);
+  }
+
+  // One item with this wave's `rb` row blocks from block row_off; then `next`
+  // starts the following one, and the outputs are written.
+  template <int N, class Next>
+  __device__ __forceinline__ void item(int row_off, Next next) {
+    constexpr int NX = N > 0 ? N : 1;
+    f32x4_t acc[NX][kCols];
+#pragma unroll
+    for (int i = 0; i < NX; ++i)
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    uint4 af[NX], cw[kCols];
+    uint32_t sw[kCols];
+    // this lane's operand (row r, chunk g) inside a row block's 2 KB; the second
+    // 32 k (chunk 4 + g) flips bit 6
+    const int aoff = (r >> 3) * 1024 + (r & 7) * 128 + ((g ^ a_chunk(r)) << 4);
+    auto read_a = [&](int p, int half, int i) {
+      return *reinterpret_cast<const uint4*>(lds + SW * kSlotW + (p % SA) * (MB * kBlockA) +
+                                             (row_off + i) * kBlockA + (aoff ^ (half << 6)));
+    };
+    auto read_w = [&](int q) {
+      const uint8_t* sl = lds + (q % SW) * kSlotW;
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) {
+        cw[j] = *reinterpret_cast<const uint4*>(sl + (cg * kCols + j) * kCodeB + 16 * lane);
+        sw[j] = *reinterpret_cast<const uint32_t*>(sl + kBlocks * kCodeB +
+                                                   (cg * kCols + j) * kScaleB + 4 * r);
+      }
+    };
+    auto widen = [&](int s, bf16x8_t (&b)[kCols]) {
+#pragma unroll
+      for (int j = 0; j < kCols; ++j)
+        b[j] = widen_fp4(s == 0 ? cw[j].x : s == 1 ? cw[j].y : s == 2 ? cw[j].z : cw[j].w,
+                         e8m0_value((sw[j] >> (8 * s)) & 255u));
+    };
+    auto mfmas = [&](const bf16x8_t (&b)[kCols], bool more, int p, int half) {
+      if constexpr (N > 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+          for (int j = 0; j < kCols; ++j)
+            acc[i][j] =
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], as_bf16x8(af[i]), acc[i][j], 0, 0, 0);
+          if (more) af[i] = read_a(p, half, i);
+        }
+      }
+    };
+    auto pass = [&](int p) {  // makes A(p + 1) (and its W stage) visible, refills
+      wait_next(p);
+      wait_lgkm0();
+      stage_barrier();
+    };
+
+    pass(-1);
+    if constexpr (N > 0) {
+      read_w(0);
+#pragma unroll
+      for (int i = 0; i < N; ++i) af[i] = read_a(0, 0, i);
+    }
+    for (int q = 0; q < nw; ++q) {
+      const int p = 2 * q;
+      const bool more = q + 1 < nw;
+      bf16x8_t b[kCols];
+      widen(0, b);
+      mfmas(b, true, p, 1);
+      widen(1, b);
+      pass(p);
+      issue(p);
+      mfmas(b, true, p + 1, 0);
+      widen(2, b);
+      mfmas(b, true, p + 1, 1);
+      widen(3, b);
+      if (more) {
+        pass(p + 1);
+        issue(p + 1);
+        if constexpr (N > 0) read_w(q + 1);
+      }
+      mfmas(b, more, p + 2, 0);
+    }
+    wait_lgkm0();
+    stage_barrier();  // every wave is done with the rings
+
+    const int out_row0 = row0, out_rows = nrows, col0 = ntile * WCOLS + cg * HALF * 16;
+    next();
+
+    // The weights are the first operand: lane (r, g) holds output columns 4g ..
+    // 4g + 3 of row r of each 16 x 16 block.  Blocks j and j + 1 trade halves
+    // between lane rows, so that a lane stores 8 columns at once; a lane whose
+    // row lies past the tile gets an offset outside the store's range.
+    if constexpr (N > 0) {
+      const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(
+          a.C + (size_t)out_row0 * a.n_out, 0, out_rows * a.n_out * 2, kBufferRsrcWord3);
+      int er = r, eg = g;  // opaque: the offsets are formed here, not kept through the loop
+      asm volatile("" : "+v"(er), "+v"(eg));
+      auto outputs = [&](int i, int j) {
         float o[4];
 #pragma unroll
         for (int v = 0; v < 4; ++v)
           o[v] = SWIGLU ? silu_mul(acc[i][j][v], acc[i][j + (SWIGLU ? HALF : 0)][v]) : acc[i][j][v];
-        const int col = ntile * WCOLS + (wave * HALF + j) * 16 + 4 * g;
-        *reinterpret_cast<uint2*>(C + (size_t)(row0 + row) * n_out + col) =
-            make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+        return u32x2_t{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
+      };
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int row = (row_off + i) * 16 + er;
+#pragma unroll
+        for (int j = 0; j < HALF; j += 2) {
+          const u32x2_t d0 = outputs(i, j), d1 = outputs(i, j + 1);
+          const auto sx = __builtin_amdgcn_permlane16_swap(d0[0], d1[0], false, false);
+          const auto sy = __builtin_amdgcn_permlane16_swap(d0[1], d1[1], false, false);
+          const int col = col0 + (j + (eg & 1)) * 16 + 4 * (eg & ~1);
+          const uint32_t off = row < out_rows ? (uint32_t)(row * a.n_out + col) * 2u : 0x80000000u;
+          const u32x4_t d = {sx[0], sy[0], sx[1], sy[1]};
+          __builtin_amdgcn_raw_buffer_store_b128(d, out, off, 0, 0);
+        }
       }
     }
   }
+
+  template <int N, class Next>
+  __device__ __forceinline__ void dispatch(int n, int row_off, Next next) {
+    if constexpr (N <= RB) {
+      if (n == N) item<N>(row_off, next);
+      else dispatch<N + 1>(n, row_off, next);
+    }
+  }
+
+  __device__ __forceinline__ void run() {
+    const int nt_n = a.n_out / WCOLS;
+    const int total = a.plan[0] * nt_n;
+    const int grid = balanced_grid(total, gridDim.x), per_xcd = grid / 8;
+    if ((int)blockIdx.x >= grid) return;  // whole workgroup
+    int q = (blockIdx.x % 8) * per_xcd + blockIdx.x / 8;
+    if (q >= total) return;
+    start(q / nt_n, q % nt_n);
+    while (q < total) {
+      q += grid;
+      // row group 0 takes the first half of the item's row blocks, rounded up
+      const int nrb = (nrows + 15) >> 4, half = RG == 1 ? nrb : (nrb + 1) / 2;
+      dispatch<0>(rg == 0 ? half : nrb - half, rg == 0 ? 0 : half, [&]() {
+        if (q < total) start(q / nt_n, q % nt_n);
+      });
+    }
+  }
+};
+
+template <int MB, int RG, int SA, int SW, bool SWIGLU>
+__global__ __launch_bounds__(256 * RG, 1) void gemm_fp4_kernel(Fp4Args args) {
+  using G = Fp4Gemm<MB, RG, SA, SW, SWIGLU>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[G::kLds];
+  G(args, lds).run();
 }
 
-// ---------------------------------------------------------------------------
-int ffn_fp4_choose_mb(int64_t, int) { return kRowBlocks; }
+template <int MB, int RG, int SA, int SW, bool SWIGLU>
+static hipError_t launch_fp4(const Fp4Args& args, hipStream_t stream) {
+  using G = Fp4Gemm<MB, RG, SA, SW, SWIGLU>;
+  auto kern = gemm_fp4_kernel<MB, RG, SA, SW, SWIGLU>;
+  static int resident = 0;  // workgroups that the device holds, fixed per build
+  if (resident == 0) {
+    int dev = 0, n = 0, occ = 0;
+    hipError_t err = hipGetDevice(&dev);
+    if (err == hipSuccess) err = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev);
+    if (err == hipSuccess) err = hipOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, 64 * G::NW, 0);
+    if (err != hipSuccess) return err;
+    resident = n * (occ > 0 ? occ : 1);
+  }
+  const int64_t grid = persistent_grid(resident, (int64_t)args.max_tiles * (args.n_out / G::WCOLS));
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(64 * G::NW), 0, stream, args);
+  return hipGetLastError();
+}
+
+// m-tile height from the mean rows per expert.
+int ffn_fp4_choose_mb(int64_t rows, int E) {
+  const int64_t mean = rows / (E > 0 ? E : 1);
+  if (mean <= 24) return 2;
+  if (mean <= 80) return 8;
+  return 12;
+}
 
 hipError_t launch_grouped_gemm_fp4(int mb, bool swiglu, const uint16_t* A, const int32_t* gather,
                                    int topk, const uint8_t* Q, const uint8_t* S, uint16_t* C,
                                    const int32_t* plan, int max_tiles, int K, int n_out,
                                    int up_row0, hipStream_t stream, const GemmBounds& bounds) {
-  if (mb != kRowBlocks) return hipErrorInvalidValue;
-  const int64_t items = (int64_t)max_tiles * (n_out / (swiglu ? 128 : 256));
-  const int64_t grid = persistent_grid(1024, items);
-  if (swiglu)
-    hipLaunchKernelGGL(gemm_fp4_kernel<true>, dim3((unsigned)grid), dim3(256), 0, stream, A,
-                       gather, topk, Q, S, C, plan, max_tiles, K, n_out, up_row0, bounds);
-  else
-    hipLaunchKernelGGL(gemm_fp4_kernel<false>, dim3((unsigned)grid), dim3(256), 0, stream, A,
-                       gather, topk, Q, S, C, plan, max_tiles, K, n_out, up_row0, bounds);
-  return hipGetLastError();
+  const Fp4Args args{A, gather, topk, Q, S, C, plan, max_tiles, K, n_out, up_row0, bounds};
+#define BEAM_FP4_CASE(MBV, RGV, SAV, SWV)                                \
+  case MBV:                                                              \
+    return swiglu ? launch_fp4<MBV, RGV, SAV, SWV, true>(args, stream)   \
+                  : launch_fp4<MBV, RGV, SAV, SWV, false>(args, stream);
+  switch (mb) {
+    BEAM_FP4_CASE(2, 1, 3, 4)
+    BEAM_FP4_CASE(8, 2, 3, 5)
+    BEAM_FP4_CASE(12, 2, 3, 4)
+    default:
+      return hipErrorInvalidValue;
+  }
+#undef BEAM_FP4_CASE
 }
 
 // A grid of at most 2^20 workgroups, whose threads walk on from there.
