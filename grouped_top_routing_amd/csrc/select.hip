@@ -10,7 +10,10 @@
 //   balance   coef * sum_e f_e P_e, f the experts' share of the pairs, P their
 //             mean (normalised) score
 //
-// One wavefront handles one token: lane l holds experts l, l + 64, ...
+// One wavefront handles one token: lane l holds experts l, l + 64, ... (V of
+// them), so that rows of any length and alignment are read in whole lines.
+// Sums and maxima over the token run on DPP moves and end in scalar registers;
+// an arg-max is the maximum, then the first lane of a ballot that holds it.
 #include <type_traits>
 
 #include "common.h"
@@ -20,7 +23,8 @@ namespace beam {
 
 namespace {
 
-constexpr int kWaves = 4;  // tokens per workgroup
+constexpr int kWaves = 4;         // tokens per workgroup
+constexpr int kBalanceWaves = 16;
 
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
 __device__ __forceinline__ float load_logit(const uint16_t* p) { return bf16_to_f32(*p); }
@@ -31,20 +35,54 @@ __device__ __forceinline__ void store_logit(uint16_t* p, float v) { *p = (uint16
 // (NaN stays NaN, -inf masks its expert).
 __device__ __forceinline__ float finite_top(float z) { return z > 3.4028234e38f ? 3.4028234e38f : z; }
 
-template <class T>
-__device__ __forceinline__ T wave_sum(T v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
-  return v;
+// One DPP move of a value of one or two registers; lanes without a source (or in
+// rows outside ROWS) get `none`.
+template <int CTRL, int ROWS, class T>
+__device__ __forceinline__ T dpp(T none, T v) {
+  if constexpr (sizeof(T) == 4) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none),
+                                                             __builtin_bit_cast(int, v), CTRL,
+                                                             ROWS, 0xf, false));
+  } else {
+    struct Two { int lo, hi; };
+    const Two n = __builtin_bit_cast(Two, none), x = __builtin_bit_cast(Two, v);
+    const Two o = {__builtin_amdgcn_update_dpp(n.lo, x.lo, CTRL, ROWS, 0xf, false),
+                   __builtin_amdgcn_update_dpp(n.hi, x.hi, CTRL, ROWS, 0xf, false)};
+    return __builtin_bit_cast(T, o);
+  }
 }
 template <class T>
-__device__ __forceinline__ T wave_max(T v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    const T o = __shfl_xor(v, off);
-    v = o > v ? o : v;
+__device__ __forceinline__ T lane_value(T v, int lane) {
+  if constexpr (sizeof(T) == 4) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+  } else {
+    struct Two { int lo, hi; };
+    const Two x = __builtin_bit_cast(Two, v);
+    const Two o = {__builtin_amdgcn_readlane(x.lo, lane), __builtin_amdgcn_readlane(x.hi, lane)};
+    return __builtin_bit_cast(T, o);
   }
-  return v;
+}
+// Reduction over the wave, by rows of 16 lanes (row_shr 1, 2, 4, 8), then across
+// them (row_bcast 15, 31); lane 63 ends with it.
+template <class T, class F>
+__device__ __forceinline__ T wave_reduce(T v, T none, F f) {
+  v = f(v, dpp<0x111, 0xf>(none, v));
+  v = f(v, dpp<0x112, 0xf>(none, v));
+  v = f(v, dpp<0x114, 0xf>(none, v));
+  v = f(v, dpp<0x118, 0xf>(none, v));
+  v = f(v, dpp<0x142, 0xa>(none, v));
+  v = f(v, dpp<0x143, 0xc>(none, v));
+  return lane_value(v, 63);
+}
+template <class T>
+__device__ __forceinline__ T wave_sum(T v) {
+  return wave_reduce(v, T(0), [](T a, T b) { return a + b; });
+}
+__device__ __forceinline__ float top_of(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double top_of(double a, double b) { return fmax(a, b); }
+template <class T>
+__device__ __forceinline__ T wave_max(T v) {
+  return wave_reduce(v, T(-INFINITY), [](T a, T b) { return top_of(a, b); });
 }
 
 // Logits of a token: the sum of `parts` arrays of `stride` elements (the
@@ -52,14 +90,12 @@ __device__ __forceinline__ T wave_max(T v) {
 template <class Z>
 __device__ __forceinline__ float gather_logit(const Z* z, int parts, int64_t stride, int64_t at) {
   float v = load_logit(z + at);
+#pragma unroll 4
   for (int p = 1; p < parts; ++p) v += load_logit(z + p * stride + at);
   return v;
 }
 
 // log of the sigmoid, without cancellation or overflow
-__device__ __forceinline__ double log_sigmoid(double z) {
-  return (z < 0.0 ? z : 0.0) - log1p(exp(-fabs(z)));
-}
 __device__ __forceinline__ float log_sigmoid(float z) {
   return fminf(z, 0.f) - log1pf(expf(-fabsf(z)));
 }
@@ -73,152 +109,221 @@ __device__ __forceinline__ float share_of(float z, float top, int softmax) {
   return sigmoidf_(z);
 }
 
+// Scores in 32 or 64 bits, 0 for a masked expert.
+__device__ __forceinline__ float exp_of(float v) { return expf(v); }
+__device__ __forceinline__ double exp_of(double v) { return exp(v); }
+template <int V, class T>
+__device__ __forceinline__ void scores(const float (&z)[V], float top, int softmax, T (&s)[V]) {
+  T total = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (softmax) s[i] = z[i] > -INFINITY ? exp_of((T)z[i] - (T)top) : (T)0;
+    else s[i] = (T)1 / ((T)1 + exp_of(-(T)z[i]));
+    total += s[i];
+  }
+  if (softmax) {
+    total = wave_sum(total);
+    if (total > (T)0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] /= total;
+    }
+  }
+}
+
+// The kept groups of a token, one bit per group at bit g * sub, from its values
+// in `values` (LDS of this wave, masked experts at -inf).  Lanes in `sub`s share
+// a group; T is float or double, and `near` is set where two groups at the border
+// are no further apart than `slack`.
+template <class T>
+__device__ __forceinline__ uint64_t kept_groups(const T* values, const SelectShape& c, int sub,
+                                                int lane, T slack, bool& near) {
+  const int size = c.experts / c.groups, mine = lane / sub;
+  T m1 = -INFINITY, m2 = -INFINITY;
+  if (mine < c.groups)
+    for (int j = lane % sub; j < size; j += sub) {
+      const T x = values[mine * size + j];
+      m2 = top_of(m2, x < m1 ? x : m1);
+      m1 = top_of(m1, x);
+    }
+  for (int off = 1; off < sub; off <<= 1) {
+    const T a = __shfl_xor(m1, off), b = __shfl_xor(m2, off);
+    m2 = top_of(a < m1 ? a : m1, top_of(m2, b));
+    m1 = top_of(m1, a);
+  }
+  const T total = c.group_best == 2 && m2 > -INFINITY ? m1 + m2 : m1;
+  int rank = 0;
+  for (int g = 0; g < c.groups; ++g) {
+    const T o = lane_value(total, g * sub);
+    rank += o > total || (o == total && g < mine) ? 1 : 0;
+  }
+  const bool live = mine < c.groups, keep = live && rank < c.topk_groups;
+  const T worst = -wave_max(keep ? -total : (T)-INFINITY);
+  const T next = wave_max(live && !keep ? total : (T)-INFINITY);
+  near = near || (next > -INFINITY && !(worst - next > slack));
+  return __ballot(keep && lane % sub == 0);
+}
+
+// The topk experts with the largest `order`, one after the other (the lower index
+// of equals): lane j gets the j-th's index (or -1) and logit.  `near` is set where two
+// neighbours in the order, the first that is left out among them, are no further
+// apart than `slack` (negative: not asked).
+template <int V, class T>
+__device__ __forceinline__ void choose(T (&order)[V], const float (&z)[V], int topk, int lane,
+                                       T slack, int& id, float& logit, bool& near) {
+  id = -1;
+  T before = INFINITY;
+  for (int j = 0; j <= topk; ++j) {
+    if (j == topk && slack < (T)0) break;
+    T best = order[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) best = top_of(best, order[i]);
+    best = wave_max(best);
+    if (!(best > -INFINITY)) break;
+    near = near || !(before - best > slack);
+    if (j == topk) break;
+    before = best;
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (!found) {
+        const uint64_t at = __ballot(order[i] == best);
+        if (at) {
+          const int owner = __builtin_ctzll(at);
+          found = true;
+          const float zw = lane_value(z[i], owner);
+          if (lane == owner) order[i] = -INFINITY;
+          if (lane == j) {
+            id = owner + 64 * i;
+            logit = zw;
+          }
+        }
+      }
+    }
+  }
+}
+
 }  // namespace
 
-// Selection.  Scores and selection values are taken in 64 bits: two experts
-// whose values differ by less than an fp32 rounding are ordered by the values,
-// not by the roundings.  Without a bias experts are ordered by their logits.
+// Selection.  Two experts (or groups) whose values differ by less than an fp32
+// rounding are ordered by the values, not by the roundings: values are compared
+// in fp32, and a token whose order has a gap within their errors is done again in
+// 64 bits.  Without a bias experts are ordered by their logits, and only groups
+// need scores.
+//
+// Bound: with s_max the row's largest score, a score carries at most 48 U s_max
+// (U = 2^-24; exponential 2 U, its argument's rounding U |d| at exp(-|d|), a sum
+// over the experts 22 U and its arguments' mean 7 U, a quotient; 1e-36 where
+// scores leave fp32's range), v one rounding more; two of them differ by twice
+// that, sums of two by twice again.
 template <class Z, int V>
 __global__ __launch_bounds__(64 * kWaves) void select_experts_kernel(
     const Z* __restrict__ logits, int parts, const float* __restrict__ bias,
     int32_t* __restrict__ ids, float* __restrict__ wout, float* __restrict__ zout, int64_t T,
     SelectShape c) {
-  __shared__ double values[kWaves][V * 64];
-  __shared__ double totals[kWaves][64];
-  __shared__ uint8_t kept[kWaves][64];
+  __shared__ double mem[kWaves][V * 64];  // values of one token per wave
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t t = (int64_t)blockIdx.x * kWaves + wave;
-  const bool live = t < T;
+  if (t >= T) return;  // the whole wave; waves share nothing
   const int E = c.experts;
 
-  float z[V];
+  float z[V], top = -INFINITY;
   bool nan = false;
-  float top = -INFINITY;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int e = lane + 64 * i;
-    z[i] = -INFINITY;
-    if (live && e < E) {
-      z[i] = gather_logit(logits, parts, T * E, t * E + e);
-      if (zout) zout[t * E + e] = z[i];
-      z[i] = finite_top(z[i]);
-    }
-    if (z[i] != z[i]) {
-      nan = true;
-      z[i] = -INFINITY;
-    }
+    z[i] = e < E ? gather_logit(logits, parts, T * E, t * E + e) : -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = lane + 64 * i;
+    if (zout && e < E) zout[t * E + e] = z[i];
+    nan = nan || z[i] != z[i];
+    z[i] = z[i] != z[i] ? -INFINITY : finite_top(z[i]);
     top = fmaxf(top, z[i]);
   }
   nan = __any(nan);
   top = wave_max(top);
-  double s[V], total = 0.0;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const double d = z[i];
-    if (c.softmax) s[i] = z[i] > -INFINITY ? exp(d - top) : 0.0;
-    else s[i] = 1.0 / (1.0 + exp(-d));
-    total += s[i];
-  }
-  if (c.softmax) {
-    total = wave_sum(total);
-    if (total > 0.0) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) s[i] /= total;
-    }
-  }
-  double v[V], order[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + 64 * i;
-    v[i] = s[i];
-    if (bias && e < E) v[i] += (double)bias[e];
-    if (!(z[i] > -INFINITY) || v[i] != v[i]) v[i] = -INFINITY;
-    order[i] = bias ? v[i] : (double)z[i];
-  }
 
-  if (c.topk_groups < c.groups) {
-    const int size = E / c.groups;
+  const bool grouped = c.topk_groups < c.groups;
+  int sub = 64;  // lanes per group
+  while (sub > 1 && (64 / sub) < c.groups) sub >>= 1;
+  const uint32_t by_size = ((1u << 20) + E / c.groups - 1) / (E / c.groups);  // e / size, e < 1024
+
+  float s[V];
+  if (bias || grouped) scores(z, top, c.softmax, s);
+  int id = -1;
+  float w = 0.f;  // of the lane's slot: its expert's logit, then its weight
+  // T is float, or double where float cannot tell
+  auto pick = [&](auto zero, float slack, bool& near) {
+    using T = decltype(zero);
+    T v[V], order[V];
+    if (bias || grouped) {
+      if constexpr (sizeof(T) == 8) scores(z, top, c.softmax, v);
 #pragma unroll
-    for (int i = 0; i < V; ++i) values[wave][lane + 64 * i] = v[i];
-    __syncthreads();
-    double mine = -INFINITY;
-    if (lane < c.groups) {
-      double m1 = -INFINITY, m2 = -INFINITY;
-      for (int j = 0; j < size; ++j) {
-        const double x = values[wave][lane * size + j];
-        m2 = fmax(m2, fmin(m1, x));
-        m1 = fmax(m1, x);
+      for (int i = 0; i < V; ++i) {
+        const int e = lane + 64 * i;
+        if constexpr (sizeof(T) == 4) v[i] = s[i];
+        if (bias) v[i] += e < E ? (T)bias[e] : (T)0;
+        if (!(z[i] > -INFINITY) || v[i] != v[i]) v[i] = -INFINITY;
       }
-      mine = c.group_best == 2 && m2 > -INFINITY ? m1 + m2 : m1;
     }
-    totals[wave][lane] = mine;
-    __syncthreads();
-    int rank = 0;
-    for (int g = 0; g < c.groups; ++g) {
-      const double o = totals[wave][g];
-      rank += o > mine || (o == mine && g < lane) ? 1 : 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) order[i] = bias ? v[i] : (T)z[i];
+    if (grouped) {
+      T* values = reinterpret_cast<T*>(mem[wave]);
+#pragma unroll
+      for (int i = 0; i < V; ++i) values[lane + 64 * i] = v[i];
+      compiler_fence();  // a wave's LDS accesses are done in order
+      const uint64_t kept = kept_groups(values, c, sub, lane, (T)(2.f * slack), near);
+      compiler_fence();
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const uint32_t e = lane + 64 * i, g = (e * by_size) >> 20;
+        if (!((kept >> ((g * sub) & 63)) & 1)) order[i] = -INFINITY;
+      }
     }
-    kept[wave][lane] = rank < c.topk_groups;
-    __syncthreads();
+    choose(order, z, c.topk, lane, bias ? (T)slack : (T)-1, id, w, near);
+  };
+  bool near = false;
+  if (!bias && !grouped) {
+    pick(0.f, 0.f, near);
+  } else {
+    float s_max = 0.f, v_max = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = lane + 64 * i;
-      if (e < E && !kept[wave][e / size]) order[i] = -INFINITY;
+      const float b = bias && e < E ? bias[e] : 0.f;
+      s_max = fmaxf(s_max, s[i]);
+      if (fabsf(b) < INFINITY) v_max = fmaxf(v_max, s[i] + fabsf(b));
+    }
+    const float slack =
+        2.f * 5.9604645e-8f * (48.f * wave_max(s_max) + 2.f * wave_max(v_max)) + 1e-36f;
+    pick(0.f, slack, near);
+    if (near) {
+      near = false;
+      pick(0.0, 0.f, near);
     }
   }
 
-  int my_id = -1;
-  float my_z = -INFINITY;
-  double my_s = 0.0;
-  for (int j = 0; j < c.topk; ++j) {
-    double best = order[0];
-    int at = lane;
-#pragma unroll
-    for (int i = 1; i < V; ++i)
-      if (order[i] > best) {
-        best = order[i];
-        at = lane + 64 * i;
-      }
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
-      const double ob = __shfl_xor(best, off);
-      const int oa = __shfl_xor(at, off);
-      if (ob > best || (ob == best && oa < at)) {
-        best = ob;
-        at = oa;
-      }
-    }
-    if (!(best > -INFINITY)) break;  // the same in every lane
-    const int owner = at & 63;
-    double sw = 0.0;
-    float zw = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (at >> 6 == i) {
-        sw = s[i];
-        zw = z[i];
-        if (lane == owner) order[i] = -INFINITY;
-      }
-    sw = __shfl(sw, owner);
-    zw = __shfl(zw, owner);
-    if (lane == j) {
-      my_id = at;
-      my_s = sw;
-      my_z = zw;
-    }
-  }
+  // by logarithms: scores that underflow still have a ratio
   if (c.renormalize) {
-    // by logarithms: scores that underflow still have a ratio
-    double l = -INFINITY;
-    if (my_id >= 0) l = c.softmax ? (double)my_z : log_sigmoid((double)my_z);
-    const double m = wave_max(l);
-    my_s = my_id >= 0 ? exp(l - m) : 0.0;
-    const double sum = wave_sum(my_s);
-    if (sum > 0.0) my_s /= sum;
+    if (!c.softmax) w = log_sigmoid(w);
+    const float m = wave_max(id >= 0 ? w : -INFINITY);
+    w = id >= 0 ? expf(w - m) : 0.f;
+    const float sum = wave_sum(w);
+    if (sum > 0.f) w /= sum;
+  } else if (!c.softmax) {
+    w = id >= 0 ? sigmoidf_(w) : 0.f;
+  } else {
+    float total = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) total += z[i] > -INFINITY ? expf(z[i] - top) : 0.f;
+    total = wave_sum(total);
+    w = id >= 0 ? expf(w - top) / total : 0.f;
   }
-  if (live && lane < c.topk) {
-    ids[t * c.topk + lane] = my_id;
-    wout[t * c.topk + lane] = nan ? __builtin_nanf("") : (float)my_s;
+  if (lane < c.topk) {
+    ids[t * c.topk + lane] = id;
+    wout[t * c.topk + lane] = nan ? __builtin_nanf("") : w;
   }
 }
 
@@ -299,12 +404,12 @@ __global__ __launch_bounds__(64 * kWaves) void select_backward_kernel(
     const float dot = c.renormalize || c.softmax ? wave_sum(id >= 0 ? g * w : 0.f) : 0.f;
     const float each = c.renormalize ? w * (g - dot) : g;
     for (int j = 0; j < c.topk; ++j) {
-      const int e = __shfl(id, j);
-      const float a = __shfl(each, j);
+      const int e = lane_value(id, j);
+      const float a = lane_value(each, j);
       if (e < 0) continue;
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (e == lane + 64 * i) dz[i] += a;
+        if (e >> 6 == i) dz[i] += lane == (e & 63) ? a : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -337,40 +442,46 @@ __global__ __launch_bounds__(64 * kWaves) void select_backward_kernel(
 }
 
 // Balance loss, first pass: a workgroup sums the normalised scores of its
-// tokens by expert (registers, then LDS, in a fixed order) and counts their
-// pairs (integer atomics in LDS).  part: [blocks][E] sums, [blocks][E] counts,
-// [blocks] rows with an expert.
+// tokens by expert (a wave's tokens in registers, then the waves in LDS, in a
+// fixed order) and counts their pairs (integer atomics in LDS).  part: [blocks][E]
+// sums, [blocks][E] counts, [blocks] rows with an expert.
 template <class Z, int V>
-__global__ __launch_bounds__(64 * kWaves) void balance_part_kernel(
+__global__ __launch_bounds__(64 * kBalanceWaves) void balance_part_kernel(
     const Z* __restrict__ logits, const int32_t* __restrict__ ids, float* __restrict__ part,
-    int64_t T, int per, SelectShape c) {
-  __shared__ float sums[kWaves][V * 64];
+    int64_t T, int64_t per, SelectShape c) {
+  __shared__ float sums[kBalanceWaves][V * 64];
   __shared__ int counts[V * 64];
-  __shared__ int rows[kWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ int rows[kBalanceWaves];
+  constexpr int kThreads = 64 * kBalanceWaves;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int E = c.experts;
-  for (int e = threadIdx.x; e < V * 64; e += 64 * kWaves) counts[e] = 0;
+  for (int e = threadIdx.x; e < V * 64; e += kThreads) counts[e] = 0;
   __syncthreads();
   float sum[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) sum[i] = 0.f;
   int mine = 0;
-  const int64_t first = (int64_t)blockIdx.x * per;
-  for (int64_t t = first + wave; t < first + per && t < T; t += kWaves) {
-    int id = -1;
-    if (lane < c.topk) {
-      id = ids[t * c.topk + lane];
-      if (id < 0 || id >= E) id = -1;
-      else atomicAdd(&counts[id], 1);
-    }
-    if (!__any(id >= 0)) continue;
-    ++mine;
-    float z[V], p[V], top = -INFINITY, total = 0.f;
-    bool nan = false;
+  const int64_t first = (int64_t)blockIdx.x * per, last = first + per < T ? first + per : T;
+  auto load = [&](int64_t t, float (&z)[V], int& id) {  // of a token, if there is one
+    if (t >= last) return;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int e = lane + 64 * i;
-      z[i] = e < E ? finite_top(load_logit(logits + t * E + e)) : -INFINITY;
+      z[i] = e < E ? load_logit(logits + t * E + e) : -INFINITY;
+    }
+    id = lane < c.topk ? ids[t * c.topk + lane] : -1;
+  };
+  auto add = [&](float (&z)[V], int id) {
+    const bool on = id >= 0 && id < E;
+    if (on) atomicAdd(&counts[id], 1);
+    if (!__any(on)) return;
+    ++mine;
+    float p[V], top = -INFINITY, total = 0.f;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      z[i] = finite_top(z[i]);
       nan = nan || z[i] != z[i];
       top = fmaxf(top, z[i]);
     }
@@ -385,6 +496,17 @@ __global__ __launch_bounds__(64 * kWaves) void balance_part_kernel(
     const float inv = nan ? __builtin_nanf("") : total > 0.f ? 1.f / total : 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) sum[i] += p[i] * inv;
+  };
+  // the next token's logits are on their way while one is added
+  float za[V], zb[V];
+  int ia = -1, ib = -1;
+  int64_t t = first + wave;
+  load(t, za, ia);
+  for (; t < last; t += 2 * kBalanceWaves) {
+    load(t + kBalanceWaves, zb, ib);
+    add(za, ia);
+    load(t + 2 * kBalanceWaves, za, ia);
+    if (t + kBalanceWaves < last) add(zb, ib);
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) sums[wave][lane + 64 * i] = sum[i];
@@ -393,43 +515,58 @@ __global__ __launch_bounds__(64 * kWaves) void balance_part_kernel(
   const int64_t B = gridDim.x;
   int32_t* pc = reinterpret_cast<int32_t*>(part) + B * E;
   int32_t* pr = pc + B * E;
-  for (int e = threadIdx.x; e < E; e += 64 * kWaves) {
+  for (int e = threadIdx.x; e < E; e += kThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += sums[w][e];
+    for (int w = 0; w < kBalanceWaves; ++w) v += sums[w][e];
     part[(int64_t)blockIdx.x * E + e] = v;
     pc[(int64_t)blockIdx.x * E + e] = counts[e];
   }
   if (threadIdx.x == 0) {
     int n = 0;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) n += rows[w];
+    for (int w = 0; w < kBalanceWaves; ++w) n += rows[w];
     pr[blockIdx.x] = n;
   }
 }
 
-// Second pass, one workgroup: the sums over the first pass's workgroups, the
-// load vector and the loss (64 bits).
+// Second pass, one workgroup: the sums over the first pass's workgroups in 64
+// bits (1024 / E threads per expert take every so-many-th of them, and are added
+// in order), the load vector and the loss.
 __global__ __launch_bounds__(1024) void balance_join_kernel(const float* __restrict__ part, int B,
                                                             int E, float coef,
                                                             float* __restrict__ loss,
                                                             float* __restrict__ load) {
+  __shared__ double psum[1024];
+  __shared__ int64_t nsum[1024];
   __shared__ double dsum[16];
-  __shared__ int64_t isum[16];
-  __shared__ int64_t rsum[16];
+  __shared__ int64_t isum[16], rsum[16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int32_t* pc = reinterpret_cast<const int32_t*>(part) + (int64_t)B * E;
   const int32_t* pr = pc + (int64_t)B * E;
+  const int ways = 1024 / E, way = threadIdx.x / E, e = threadIdx.x - way * E;
   double p = 0.0;
   int64_t n = 0, r = 0;
-  const int e = threadIdx.x;
-  if (e < E)
-    for (int b = 0; b < B; ++b) {
+  if (way < ways) {
+#pragma unroll 8
+    for (int b = way; b < B; b += ways) {
       p += (double)part[(int64_t)b * E + e];
       n += pc[(int64_t)b * E + e];
     }
+  }
+  psum[threadIdx.x] = p;
+  nsum[threadIdx.x] = n;
   for (int b = threadIdx.x; b < B; b += 1024) r += pr[b];
-  int64_t ns = wave_sum(n);
+  __syncthreads();
+  const bool owner = (int)threadIdx.x < E;
+  p = 0.0;
+  n = 0;
+  if (owner)
+    for (int w = 0; w < ways; ++w) {
+      p += psum[w * E + threadIdx.x];
+      n += nsum[w * E + threadIdx.x];
+    }
+  const int64_t ns = wave_sum(n);
   r = wave_sum(r);
   if (lane == 0) {
     isum[wave] = ns;
@@ -437,14 +574,15 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(const float* __restr
   }
   __syncthreads();
   int64_t pairs = 0, rows = 0;
+#pragma unroll
   for (int w = 0; w < 16; ++w) {
     pairs += isum[w];
     rows += rsum[w];
   }
   const double f = pairs > 0 ? (double)E * (double)n / (double)pairs : 0.0;
   const double l = rows > 0 ? (double)coef * f / (double)rows : 0.0;
-  if (e < E) load[e] = (float)l;
-  double d = wave_sum(e < E && rows > 0 ? l * p : 0.0);
+  if (owner) load[threadIdx.x] = (float)l;
+  const double d = wave_sum(owner && rows > 0 ? l * p : 0.0);
   if (lane == 0) dsum[wave] = d;
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -502,12 +640,13 @@ hipError_t launch_select_backward(bool fp32, const void* logits, const int32_t* 
   });
 }
 
-// Workgroups of the first pass, and the tokens of each.
+// Workgroups of the first pass (at most 128: the second one adds them up), and
+// the tokens of each.
 static int64_t balance_per(int64_t T) {
-  const int64_t per = (T + 255) / 256;
-  return (per + kWaves - 1) / kWaves * kWaves;
+  const int64_t per = (T + 127) / 128;
+  return per < kBalanceWaves ? kBalanceWaves : per;
 }
-static int64_t balance_blocks(int64_t T) { return T > 0 ? (T + balance_per(T) - 1) / balance_per(T) : 0; }
+static int64_t balance_blocks(int64_t T) { return (T + balance_per(T) - 1) / balance_per(T); }
 
 size_t balance_ws(int64_t T, int E) {
   const int64_t B = balance_blocks(T);
@@ -522,13 +661,13 @@ hipError_t launch_balance_loss(bool fp32, const void* logits, const int32_t* ids
   const hipError_t err = by_experts(c.experts, [&](auto v) {
     constexpr int V = decltype(v)::value;
     if (fp32)
-      hipLaunchKernelGGL((balance_part_kernel<float, V>), dim3((unsigned)B), dim3(64 * kWaves), 0,
-                         stream, static_cast<const float*>(logits), ids, part, T,
-                         (int)balance_per(T), c);
+      hipLaunchKernelGGL((balance_part_kernel<float, V>), dim3((unsigned)B),
+                         dim3(64 * kBalanceWaves), 0, stream, static_cast<const float*>(logits),
+                         ids, part, T, balance_per(T), c);
     else
-      hipLaunchKernelGGL((balance_part_kernel<uint16_t, V>), dim3((unsigned)B), dim3(64 * kWaves),
-                         0, stream, static_cast<const uint16_t*>(logits), ids, part, T,
-                         (int)balance_per(T), c);
+      hipLaunchKernelGGL((balance_part_kernel<uint16_t, V>), dim3((unsigned)B),
+                         dim3(64 * kBalanceWaves), 0, stream,
+                         static_cast<const uint16_t*>(logits), ids, part, T, balance_per(T), c);
     return hipGetLastError();
   });
   if (err != hipSuccess) return err;
