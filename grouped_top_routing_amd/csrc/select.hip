@@ -78,11 +78,24 @@ template <class T>
 __device__ __forceinline__ T wave_sum(T v) {
   return wave_reduce(v, T(0), [](T a, T b) { return a + b; });
 }
+// Keys that order as unsigned numbers like the floats they stand for, 0 below all
+// of them (-inf is 0x7fffff; -0 counts as 0): a maximum of keys is one DPP
+// instruction per step.
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const int u = __float_as_int(v + 0.f);
+  return (uint32_t)(u ^ (u >> 31 | (int)0x80000000));
+}
+__device__ __forceinline__ float of_key(uint32_t k) {
+  return __uint_as_float((int)k < 0 ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ uint32_t wave_max_key(uint32_t k) {
+  return wave_reduce(k, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
 __device__ __forceinline__ float top_of(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ double top_of(double a, double b) { return fmax(a, b); }
-template <class T>
-__device__ __forceinline__ T wave_max(T v) {
-  return wave_reduce(v, T(-INFINITY), [](T a, T b) { return top_of(a, b); });
+__device__ __forceinline__ float wave_max(float v) { return of_key(wave_max_key(key_of(v))); }
+__device__ __forceinline__ double wave_max(double v) {
+  return wave_reduce(v, (double)-INFINITY, [](double a, double b) { return fmax(a, b); });
 }
 
 // Logits of a token: the sum of `parts` arrays of `stride` elements (the
@@ -163,43 +176,55 @@ __device__ __forceinline__ uint64_t kept_groups(const T* values, const SelectSha
   return __ballot(keep && lane % sub == 0);
 }
 
+// What choose() works on: fp32 values as keys, fp64 values as they are.
+__device__ __forceinline__ uint32_t handle_of(float v) { return v > -INFINITY ? key_of(v) : 0u; }
+__device__ __forceinline__ double handle_of(double v) { return v; }
+__device__ __forceinline__ bool handles_one(uint32_t h) { return h != 0; }
+__device__ __forceinline__ bool handles_one(double h) { return h > -INFINITY; }
+__device__ __forceinline__ uint32_t wave_max_handle(uint32_t h) { return wave_max_key(h); }
+__device__ __forceinline__ double wave_max_handle(double h) { return wave_max(h); }
+__device__ __forceinline__ uint32_t top_of(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
 // The topk experts with the largest `order`, one after the other (the lower index
-// of equals): lane j gets the j-th's index (or -1) and logit.  `near` is set where two
+// of equals): lane j gets the j-th's index, or -1.  `near` is set where two
 // neighbours in the order, the first that is left out among them, are no further
-// apart than `slack` (negative: not asked).
+// apart than `slack` (negative: not asked; fp32 only).
 template <int V, class T>
-__device__ __forceinline__ void choose(T (&order)[V], const float (&z)[V], int topk, int lane,
-                                       T slack, int& id, float& logit, bool& near) {
-  id = -1;
-  T before = INFINITY;
+__device__ __forceinline__ int choose(const T (&order)[V], int topk, int lane, float slack,
+                                      bool& near) {
+  using H = decltype(handle_of(T(0)));
+  H h[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) h[i] = handle_of(order[i]);
+  const H none = handle_of((T)-INFINITY);
+  int id = -1;
+  float before = INFINITY;
   for (int j = 0; j <= topk; ++j) {
-    if (j == topk && slack < (T)0) break;
-    T best = order[0];
+    if (j == topk && slack < 0.f) break;
+    H best = h[0];
 #pragma unroll
-    for (int i = 1; i < V; ++i) best = top_of(best, order[i]);
-    best = wave_max(best);
-    if (!(best > -INFINITY)) break;
-    near = near || !(before - best > slack);
-    if (j == topk) break;
-    before = best;
-    bool found = false;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if (!found) {
-        const uint64_t at = __ballot(order[i] == best);
-        if (at) {
-          const int owner = __builtin_ctzll(at);
-          found = true;
-          const float zw = lane_value(z[i], owner);
-          if (lane == owner) order[i] = -INFINITY;
-          if (lane == j) {
-            id = owner + 64 * i;
-            logit = zw;
-          }
-        }
+    for (int i = 1; i < V; ++i) best = top_of(best, h[i]);
+    best = wave_max_handle(best);
+    if (!handles_one(best)) break;
+    if constexpr (sizeof(T) == 4) {
+      if (slack >= 0.f) {
+        const float v = of_key(best);
+        near = near || !(before - v > slack);
+        before = v;
       }
     }
+    if (j == topk) break;
+    int at = -1;  // the lowest index of those that hold it
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i) {
+      const uint64_t held = __ballot(h[i] == best);
+      at = held ? __builtin_ctzll(held) + 64 * i : at;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) h[i] = lane + 64 * i == at ? none : h[i];
+    id = lane == j ? at : id;
   }
+  return id;
 }
 
 }  // namespace
@@ -242,7 +267,7 @@ __global__ __launch_bounds__(64 * kWaves) void select_experts_kernel(
     top = fmaxf(top, z[i]);
   }
   nan = __any(nan);
-  top = wave_max(top);
+  const bool raw = c.softmax && !c.renormalize;
 
   const bool grouped = c.topk_groups < c.groups;
   int sub = 64;  // lanes per group
@@ -250,9 +275,9 @@ __global__ __launch_bounds__(64 * kWaves) void select_experts_kernel(
   const uint32_t by_size = ((1u << 20) + E / c.groups - 1) / (E / c.groups);  // e / size, e < 1024
 
   float s[V];
+  if (bias || grouped || raw) top = wave_max(top);
   if (bias || grouped) scores(z, top, c.softmax, s);
   int id = -1;
-  float w = 0.f;  // of the lane's slot: its expert's logit, then its weight
   // T is float, or double where float cannot tell
   auto pick = [&](auto zero, float slack, bool& near) {
     using T = decltype(zero);
@@ -282,7 +307,7 @@ __global__ __launch_bounds__(64 * kWaves) void select_experts_kernel(
         if (!((kept >> ((g * sub) & 63)) & 1)) order[i] = -INFINITY;
       }
     }
-    choose(order, z, c.topk, lane, bias ? (T)slack : (T)-1, id, w, near);
+    id = choose(order, c.topk, lane, bias && sizeof(T) == 4 ? slack : -1.f, near);
   };
   bool near = false;
   if (!bias && !grouped) {
@@ -305,14 +330,21 @@ __global__ __launch_bounds__(64 * kWaves) void select_experts_kernel(
     }
   }
 
-  // by logarithms: scores that underflow still have a ratio
+  // the chosen logits, then the weights (by logarithms: scores that underflow
+  // still have a ratio)
+  float w = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float zi = __shfl(z[i], id & 63);
+    w = id >> 6 == i ? zi : w;
+  }
   if (c.renormalize) {
     if (!c.softmax) w = log_sigmoid(w);
     const float m = wave_max(id >= 0 ? w : -INFINITY);
     w = id >= 0 ? expf(w - m) : 0.f;
     const float sum = wave_sum(w);
     if (sum > 0.f) w /= sum;
-  } else if (!c.softmax) {
+  } else if (!raw) {
     w = id >= 0 ? sigmoidf_(w) : 0.f;
   } else {
     float total = 0.f;
