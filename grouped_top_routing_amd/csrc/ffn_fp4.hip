@@ -10,11 +10,13 @@
 // step.
 //
 // Packed layout (moe_quantize_fp4, moe_pack_fp4): each expert's [N, K] matrix
-// is stored as [N/16][K/128] fragments.  A code fragment is [64 lanes][4][4
-// bytes]: lane l, word s holds the 8 codes of row 16b + l%16 at k = 128 st +
-// 32 s + 8 (l/16) .. +7 (lower k in lower bits), so that one 16-byte read per
-// lane brings its operands of four MFMA steps.  A scale fragment is [16 rows]
+// is stored as [N/16][K/128] fragments.  A code fragment is [2][64 lanes][2][4
+// bytes]: half h, lane l, word s holds the 8 codes of row 16b + l%16 at k = 128 t
+// + 64 h + 32 s + 8 (l/16) .. +7 (lower k in lower bits), so that one 8-byte read
+// per lane brings its operands of two MFMA steps.  A scale fragment is [16 rows]
 // [4 bytes], one byte per 32 k.
+#include <type_traits>
+
 #include "common.h"
 #include "kernels.h"
 
@@ -87,7 +89,8 @@ __global__ __launch_bounds__(256) void quantize_fp4_kernel(const uint16_t* __res
       uint32_t word = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) word |= e2m1_rne(v[8 * c + j] * inv) << (4 * j);
-      *reinterpret_cast<uint32_t*>(q + frag * kCodeB + (c * 16 + r) * 16 + step * 4) = word;
+      *reinterpret_cast<uint32_t*>(q + frag * kCodeB + (step >> 1) * (kCodeB / 2) +
+                                   (c * 16 + r) * 8 + (step & 1) * 4) = word;
     }
   }
 }
@@ -108,12 +111,14 @@ __global__ __launch_bounds__(256) void pack_fp4_kernel(const uint8_t* __restrict
     const int st = (int)(frag - block * per);
     const int64_t row = block * 16 + r;
     const uint8_t* src = codes + row * (K / 2) + st * 64 + 4 * c;
-    uint4 v;
-    v.x = *reinterpret_cast<const uint32_t*>(src);
-    v.y = *reinterpret_cast<const uint32_t*>(src + 16);
-    v.z = *reinterpret_cast<const uint32_t*>(src + 32);
-    v.w = *reinterpret_cast<const uint32_t*>(src + 48);
-    st16(q + i * 16, v);
+    uint2 lo, hi;
+    lo.x = *reinterpret_cast<const uint32_t*>(src);
+    lo.y = *reinterpret_cast<const uint32_t*>(src + 16);
+    hi.x = *reinterpret_cast<const uint32_t*>(src + 32);
+    hi.y = *reinterpret_cast<const uint32_t*>(src + 48);
+    uint8_t* dst = q + frag * kCodeB + l * 8;
+    *reinterpret_cast<uint2*>(dst) = lo;
+    *reinterpret_cast<uint2*>(dst + kCodeB / 2) = hi;
     if (c == 0)
       *reinterpret_cast<uint32_t*>(s + frag * kScaleB + r * 4) =
           *reinterpret_cast<const uint32_t*>(scales + row * (K / 32) + st * 4);
@@ -133,14 +138,17 @@ __global__ __launch_bounds__(256) void pack_fp4_kernel(const uint8_t* __restrict
 //   A stage p: 64 k of the item's rows, 2 KB per row block, in slot p % SA; each
 //              row's 128 bytes with its 16-byte chunks swizzled by (row / 2) % 8,
 //              so that the 16 rows of an operand read hit distinct banks
-// A wave reads its codes of 128 k once (16 bytes per block and lane) and widens
-// them to bf16 operands in registers, 8 codes per MFMA step.
+// A wave reads its codes of 64 k once (8 bytes per block and lane) and widens them
+// to bf16 operands in registers, one MFMA step ahead and between the MFMAs of the
+// step before: an MFMA holds the matrix cores for 16 cycles and the issue port for
+// 4, so that the conversions fit beside it.
 //
 // Schedule.  Iteration p (64 k, two MFMA steps) waits for A(p + 1), and W((p + 1)
 // / 2) where that is new, passes a barrier, and refills the slots that every
-// wave has read by then: A(p + SA), then W(p / 2 + SW) for even p.  The loads
-// before the loop are those of iterations below 0 in the same order, so one
-// rule gives every wait (younger below).  A workgroup issues its next item's
+// wave has read by then: A(p + SA), then for odd p W((p - 1) / 2 + SW) (codes of
+// stage p are read after the barrier of iteration p - 1).  The loads before the
+// loop are those of iterations below 0 in the same order, so one rule gives every
+// wait (wait_next).  A workgroup issues its next item's
 // first loads before the current item's outputs are written.
 constexpr int kBlocks = 16;      // weight-row blocks of an item
 constexpr int kCols = 4;         // column blocks per wave
@@ -186,8 +194,9 @@ struct Fp4Gemm {
   static constexpr int HALF = SWIGLU ? kCols / 2 : kCols;
   static constexpr int WCOLS = kColGroups * HALF * 16;
   static constexpr int kLoadsW = NBL + 1;             // direct loads of a W stage per wave
-  static constexpr int kLds = SW * kSlotW + SA * MB * kBlockA;
-  static_assert(SA % 2 == 1 && 2 * SW > SA, "the waits count W stages by this");
+  static constexpr int kSlotA = MB * kBlockA;
+  static constexpr int kLds = SW * kSlotW + SA * kSlotA;
+  static_assert(SA % 2 == 1 && 2 * SW > SA + 1, "a W stage is issued before the A stage it is waited with");
   static_assert(kLds <= 160 * 1024, "LDS");
 
   const Fp4Args& a;
@@ -196,10 +205,11 @@ struct Fp4Gemm {
   int nst, nw;                 // A and W stages of an item
   // the item whose loads are in flight
   int row0, nrows, ntile, na;
-  int src[AMAX][2];            // rows of A that this lane loads
-  const uint8_t* code[NBL];    // wave-uniform
+  const uint16_t* arow[AMAX][2];  // this lane's 16 bytes of stage 0 of the rows it loads
+  const uint8_t* code;            // expert's codes and scales, at the next W stage
   const uint8_t* scale;
-  uint32_t scale_off;
+  uint32_t code_off[NBL], scale_off;
+  uint32_t next_a, next_w;        // slots that the next stages go to (bytes into the ring)
 
   __device__ __forceinline__ Fp4Gemm(const Fp4Args& args, uint8_t* mem) : a(args), lds(mem) {
     lane = threadIdx.x & 63;
@@ -222,45 +232,42 @@ struct Fp4Gemm {
   }
 
   __device__ __forceinline__ void issue_a(int p) {
-    const int k0 = p * 64;
-    const uint32_t slot = lds_base() + SW * kSlotW + (uint32_t)(p % SA) * (MB * kBlockA);
+    const uint32_t slot = lds_base() + SW * kSlotW + next_a + (uint32_t)wave * kBlockA;
 #pragma unroll
     for (int j = 0; j < AMAX; ++j)
       if (j < na) {
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const int chunk = (lane & 7) ^ a_chunk(hf * 8 + (lane >> 3));
-          lds_dma16(a.A + (size_t)src[j][hf] * a.K + k0 + 8 * chunk,
-                    slot + (uint32_t)(wave + NW * j) * kBlockA + hf * 1024);
-        }
+        lds_dma16(arow[j][0] + p * 64, slot + NW * j * kBlockA);
+        lds_dma16(arow[j][1] + p * 64, slot + NW * j * kBlockA + 1024);
       }
+    next_a = next_a + kSlotA == SA * kSlotA ? 0 : next_a + kSlotA;
   }
   __device__ __forceinline__ void issue_w(int q) {
     BEAM_CHECK(q >= 0 && q < nw, kCheckWeightOffset);
-    const uint32_t slot = lds_base() + (uint32_t)(q % SW) * kSlotW;
+    const uint32_t slot = lds_base() + next_w;
 #pragma unroll
     for (int t = 0; t < NBL; ++t)
-      lds_dma16_sv<true>(code[t] + (size_t)q * kCodeB, (uint32_t)lane * 16u,
-                         slot + (uint32_t)(cg * kCols + rg + RG * t) * kCodeB);
+      lds_dma16_sv<true>(code, code_off[t], slot + (uint32_t)(cg * kCols + rg + RG * t) * kCodeB);
     // every wave of a column group loads its four blocks' scales: the same
     // bytes to the same place, so that all waves count alike
-    lds_dma4_sv(scale + (size_t)q * kScaleB, scale_off,
-                slot + kBlocks * kCodeB + (uint32_t)(cg * kCols) * kScaleB);
+    lds_dma4_sv(scale, scale_off, slot + kBlocks * kCodeB + (uint32_t)(cg * kCols) * kScaleB);
+    code += kCodeB;
+    scale += kScaleB;
+    next_w = next_w + kSlotW == SW * kSlotW ? 0 : next_w + kSlotW;
   }
   // loads of iteration p
   __device__ __forceinline__ void issue(int p) {
     if (p + SA >= 0 && p + SA < nst) issue_a(p + SA);
-    if ((p & 1) == 0) {
-      const int q = (p >> 1) + SW;
+    if (p & 1) {
+      const int q = ((p - 1) >> 1) + SW;
       if (q >= 0 && q < nw) issue_w(q);
     }
   }
   // Waits for A(p + 1), and so for every older load: as many of this wave's
   // loads may stay in flight as were issued after it, namely A(p + 2) .. A(p +
-  // SA - 1) and the W stages of the even iterations p + 1 - SA .. p - 1.
+  // SA - 1) and the W stages of the odd iterations p + 1 - SA .. p - 1.
   __device__ __forceinline__ void wait_next(int p) {
     constexpr int kA = SA - 2, kW = (SA - 1) / 2;
-    const int last_w = ((p + 1) >> 1) - 1 + SW;  // of the latest even iteration below p
+    const int last_w = (p >> 1) - 1 + SW;  // of the latest odd iteration below p
     if (p + SA - 1 < nst && last_w < nw) {
       if (na == AMAX) wait_vm<2 * AMAX * kA + kLoadsW * kW>();
       else wait_vm<2 * (AMAX - 1) * kA + kLoadsW * kW>();
@@ -290,47 +297,49 @@ struct Fp4Gemm {
 #pragma unroll
     for (int j = 0; j < AMAX; ++j) {
       const int blk = __builtin_amdgcn_readfirstlane((wave + NW * j) * 16);
+      int v[16];
       if (a.gather) {
         const __attribute__((address_space(4))) int32_t* cgather =
             (const __attribute__((address_space(4))) int32_t*)a.gather;
-        int v[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k)
           v[k] = cgather[BEAM_CLAMP(row0 + min(blk + k, nrows - 1), 0, a.bounds.n_rows - 1,
                                     kCheckGatherIndex)];
+      }
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          int x = v[8 * hf];
+      for (int hf = 0; hf < 2; ++hf) {
+        int x = row0 + min(blk + 8 * hf + (lane >> 3), nrows - 1);
+        if (a.gather) {
+          x = v[8 * hf];
 #pragma unroll
           for (int k = 1; k < 8; ++k) x = (lane >> 3) == k ? v[8 * hf + k] : x;
-          src[j][hf] = BEAM_CLAMP(x / a.topk, 0, a.bounds.n_src - 1, kCheckTokenIndex);
+          x /= a.topk;
         }
-      } else {
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-          src[j][hf] = BEAM_CLAMP(row0 + min(blk + 8 * hf + (lane >> 3), nrows - 1), 0,
-                                  a.bounds.n_src - 1, kCheckTokenIndex);
+        x = BEAM_CLAMP(x, 0, a.bounds.n_src - 1, kCheckTokenIndex);
+        arow[j][hf] = a.A + (size_t)x * a.K + 8 * ((lane & 7) ^ a_chunk(hf * 8 + (lane >> 3)));
       }
     }
     const int64_t blocks = (SWIGLU ? 2 * (int64_t)a.n_out : a.n_out) / 16;
-    const int64_t first = (int64_t)e * blocks;
+    code = a.Q + e * blocks * nw * kCodeB;
+    scale = a.S + e * blocks * nw * kScaleB;
 #pragma unroll
     for (int t = 0; t < NBL; ++t)
-      code[t] = a.Q + (first + BEAM_CLAMP(weight_row(rg + RG * t) >> 4, 0, blocks - 1,
-                                          kCheckWeightOffset)) * nw * kCodeB;
-    scale = a.S + first * nw * kScaleB;
+      code_off[t] = (uint32_t)BEAM_CLAMP(weight_row(rg + RG * t) >> 4, 0, blocks - 1,
+                                         kCheckWeightOffset) * (uint32_t)(nw * kCodeB) +
+                    (uint32_t)lane * 16u;
     // lane l loads the scales of row l % 16 of column block l / 16
     int block = 0;
 #pragma unroll
     for (int j = 0; j < kCols; ++j) block = g == j ? weight_row(j) >> 4 : block;
     scale_off = (uint32_t)block * (uint32_t)(nw * kScaleB) + (uint32_t)r * 4u;
+    next_a = next_w = 0;
     constexpr int kFirst = SA > 2 * SW ? SA : 2 * SW;
 #pragma unroll
     for (int p = -kFirst; p < 0; ++p) issue(p);
   }
 
-  // One item with this wave's `rb` row blocks from block row_off; then `next`
-  // starts the following one, and the outputs are written.
+  // One item with this wave's N row blocks from block row_off; then `next` starts
+  // the following one, and the outputs are written.
   template <int N, class Next>
   __device__ __forceinline__ void item(int row_off, Next next) {
     constexpr int NX = N > 0 ? N : 1;
@@ -339,73 +348,121 @@ struct Fp4Gemm {
     for (int i = 0; i < NX; ++i)
 #pragma unroll
       for (int j = 0; j < kCols; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    uint4 af[NX], cw[kCols];
+    uint4 af[NX];
+    uint2 cw[kCols];
     uint32_t sw[kCols];
+    bf16x8_t b0[kCols], b1[kCols];
     // this lane's operand (row r, chunk g) inside a row block's 2 KB; the second
     // 32 k (chunk 4 + g) flips bit 6
+    const uint8_t* abase = lds + SW * kSlotW + row_off * kBlockA;
     const int aoff = (r >> 3) * 1024 + (r & 7) * 128 + ((g ^ a_chunk(r)) << 4);
-    auto read_a = [&](int p, int half, int i) {
-      return *reinterpret_cast<const uint4*>(lds + SW * kSlotW + (p % SA) * (MB * kBlockA) +
-                                             (row_off + i) * kBlockA + (aoff ^ (half << 6)));
+    const uint8_t* wbase = lds + cg * kCols * kCodeB + 8 * lane;
+    const uint8_t* sbase = lds + kBlocks * kCodeB + cg * kCols * kScaleB + 4 * r;
+    auto read_a = [&](uint32_t slot, int half, int i) {
+      return *reinterpret_cast<const uint4*>(abase + slot + i * kBlockA + (aoff ^ (half << 6)));
     };
-    auto read_w = [&](int q) {
-      const uint8_t* sl = lds + (q % SW) * kSlotW;
-#pragma unroll
-      for (int j = 0; j < kCols; ++j) {
-        cw[j] = *reinterpret_cast<const uint4*>(sl + (cg * kCols + j) * kCodeB + 16 * lane);
-        sw[j] = *reinterpret_cast<const uint32_t*>(sl + kBlocks * kCodeB +
-                                                   (cg * kCols + j) * kScaleB + 4 * r);
-      }
-    };
-    auto widen = [&](int s, bf16x8_t (&b)[kCols]) {
-#pragma unroll
-      for (int j = 0; j < kCols; ++j)
-        b[j] = widen_fp4(s == 0 ? cw[j].x : s == 1 ? cw[j].y : s == 2 ? cw[j].z : cw[j].w,
-                         e8m0_value((sw[j] >> (8 * s)) & 255u));
-    };
-    auto mfmas = [&](const bf16x8_t (&b)[kCols], bool more, int p, int half) {
+    // codes of half a W stage, and with its first half its scales
+    auto read_w = [&](uint32_t slot, int half) {
       if constexpr (N > 0) {
 #pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+          cw[j] = *reinterpret_cast<const uint2*>(wbase + slot + j * kCodeB + half * (kCodeB / 2));
+          if (half == 0) sw[j] = *reinterpret_cast<const uint32_t*>(sbase + slot + j * kScaleB);
+        }
+      }
+    };
+    // operands of step s (of the 128 k that sw covers) of column block j
+    auto widen = [&](int s, int j) {
+      return widen_fp4(s & 1 ? cw[j].y : cw[j].x, e8m0_value((sw[j] >> (8 * s)) & 255u));
+    };
+    // One MFMA step on b and af.  Row block by row block af is read again from
+    // `slot`, and step s (the next one) is widened into bn, LATE row blocks after
+    // its codes were read.
+    auto step = [&](const bf16x8_t (&b)[kCols], bf16x8_t (&bn)[kCols], int s, uint32_t slot,
+                    int half, auto late) {
+      if constexpr (N > 0) {
+        constexpr int LATE = decltype(late)::value < N ? decltype(late)::value : N - 1;
+        int done = 0;
+#pragma unroll
         for (int i = 0; i < N; ++i) {
+          const int upto = i < LATE ? 0 : (i - LATE + 1) * kCols / (N - LATE);
 #pragma unroll
           for (int j = 0; j < kCols; ++j)
             acc[i][j] =
                 __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], as_bf16x8(af[i]), acc[i][j], 0, 0, 0);
-          if (more) af[i] = read_a(p, half, i);
+          af[i] = read_a(slot, half, i);
+#pragma unroll
+          for (int j = 0; j < kCols; ++j)
+            if (j >= done && j < upto) bn[j] = widen(s, j);
+          // of this row block: an MFMA, its share of the conversions, and so on
+          const int n = (6 * (upto - done) + kCols - 1) / kCols;
+          done = upto;
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            if (n <= 0) continue;
+            if (n <= 2) __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+            else if (n <= 3) __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+            else __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
+        // computed here, not sunk to their use behind the next barrier
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) asm volatile("" : "+v"(bn[j]));
       }
     };
-    auto pass = [&](int p) {  // makes A(p + 1) (and its W stage) visible, refills
+    using Late0 = std::integral_constant<int, 0>;
+    using Late1 = std::integral_constant<int, 1>;
+    auto pass = [&](int p) {  // makes A(p + 1) (and its W stage) visible
       wait_next(p);
       wait_lgkm0();
       stage_barrier();
     };
 
+    uint32_t as = 0, ws = 0;  // slots of A(2q) and W(q)
     pass(-1);
     if constexpr (N > 0) {
-      read_w(0);
+      read_w(0, 0);
 #pragma unroll
       for (int i = 0; i < N; ++i) af[i] = read_a(0, 0, i);
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) b0[j] = widen(0, j);
     }
-    for (int q = 0; q < nw; ++q) {
+    int q = 0;
+    for (; q + 1 < nw; ++q) {  // iterations 2q and 2q + 1
       const int p = 2 * q;
-      const bool more = q + 1 < nw;
-      bf16x8_t b[kCols];
-      widen(0, b);
-      mfmas(b, true, p, 1);
-      widen(1, b);
+      const uint32_t as1 = as + kSlotA == SA * kSlotA ? 0 : as + kSlotA;
+      const uint32_t as2 = as1 + kSlotA == SA * kSlotA ? 0 : as1 + kSlotA;
+      const uint32_t ws1 = ws + kSlotW == SW * kSlotW ? 0 : ws + kSlotW;
+      step(b0, b1, 1, as, 1, Late0{});
       pass(p);
+      read_w(ws, 1);
       issue(p);
-      mfmas(b, true, p + 1, 0);
-      widen(2, b);
-      mfmas(b, true, p + 1, 1);
-      widen(3, b);
-      if (more) {
-        pass(p + 1);
-        issue(p + 1);
-        if constexpr (N > 0) read_w(q + 1);
+      step(b1, b0, 2, as1, 0, Late1{});
+      step(b0, b1, 3, as1, 1, Late0{});
+      pass(p + 1);
+      read_w(ws1, 0);
+      issue(p + 1);
+      step(b1, b0, 0, as2, 0, Late1{});
+      as = as2;
+      ws = ws1;
+    }
+    {  // the last W stage
+      const uint32_t as1 = as + kSlotA == SA * kSlotA ? 0 : as + kSlotA;
+      step(b0, b1, 1, as, 1, Late0{});
+      pass(2 * q);
+      read_w(ws, 1);
+      step(b1, b0, 2, as1, 0, Late1{});
+      step(b0, b1, 3, as1, 1, Late0{});
+      if constexpr (N > 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int j = 0; j < kCols; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[j], as_bf16x8(af[i]),
+                                                                acc[i][j], 0, 0, 0);
       }
-      mfmas(b, more, p + 2, 0);
     }
     wait_lgkm0();
     stage_barrier();  // every wave is done with the rings

@@ -304,8 +304,8 @@ int moe_layer_forward_fp8(const moe_config_t* cfg, const uint16_t* x, const floa
  * Row-major form (moe_pack_fp4's input): codes [E, N, K / 2], two per byte, the
  * lower k in the low half; scales [E, N, K / 32].
  * Packed form (MOE_LAYOUT_FP4_PACKED), the same sizes: each expert's codes as
- * [N/16][K/128][64][4][4 bytes], entry (b, t, l, s) holding the codes of row
- * 16b + l%16 at k = 128t + 32s + 8(l/16) .. +7, lower k in lower bits; its
+ * [N/16][K/128][2][64][2][4 bytes], entry (b, t, h, l, s) holding the codes of
+ * row 16b + l%16 at k = 128t + 64h + 32s + 8(l/16) .. +7, lower k in lower bits; its
  * scales as [N/16][K/128][16][4 bytes], entry (b, t, r, s) that of row 16b + r
  * at k = 128t + 32s.
  *   q_gate_up [E, 2*I, H / 2] bytes, s_gate_up [E, 2*I, H / 32]

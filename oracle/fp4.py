@@ -55,14 +55,14 @@ def to_bytes(codes):
 def pack_codes(codes):
     """[.., N, K] codes in fragment order, as bytes [.., N, K / 2]."""
     *lead, N, K = codes.shape
-    out = np.zeros((*lead, N // 16, K // 128, 64, 4, 4), np.uint8)
+    out = np.zeros((*lead, N // 16, K // 128, 2, 64, 2, 4), np.uint8)
     for lane in range(64):
         r, g = lane % 16, lane // 16
         for s in range(4):
             for b in range(4):
                 k = 32 * s + 8 * g + 2 * b
                 c = codes.reshape(*lead, N // 16, 16, K // 128, 128)
-                out[..., lane, s, b] = c[..., r, :, k] | (c[..., r, :, k + 1] << 4)
+                out[..., s // 2, lane, s % 2, b] = c[..., r, :, k] | (c[..., r, :, k + 1] << 4)
     return out.reshape(*lead, N, K // 2)
 
 

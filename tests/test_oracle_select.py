@@ -136,12 +136,12 @@ def test_fragment_order():
     rng = np.random.default_rng(1)
     codes = rng.integers(0, 16, size=(2, 32, 256)).astype(np.uint8)
     scales = rng.integers(0, 256, size=(2, 32, 8)).astype(np.uint8)
-    q = fp4.pack_codes(codes).reshape(2, 2, 2, 64, 16)
+    q = fp4.pack_codes(codes).reshape(2, 2, 2, 2, 64, 8)
     s = fp4.pack_scales(scales).reshape(2, 2, 2, 16, 4)
     for _ in range(200):
         e, n, k = rng.integers(2), rng.integers(32), rng.integers(256)
         b, r, t = n // 16, n % 16, k // 128
         step, g, i = k % 128 // 32, k % 32 // 8, k % 8
-        byte = q[e, b, t, 16 * g + r, 4 * step + i // 2]
+        byte = q[e, b, t, step // 2, 16 * g + r, 4 * (step % 2) + i // 2]
         assert (byte >> (4 * (i & 1))) & 15 == codes[e, n, k]
         assert s[e, b, t, r, step] == scales[e, n, k // 32]
