@@ -246,18 +246,24 @@ struct Fp4Matrix {
   bool ok() const { return q && s && aligned16(q) && aligned16(s); }
 };
 
+int do_plan_fp4(const moe_config_t* c, const int32_t* offsets, int32_t* plan, hipStream_t s) {
+  const int mb = mb_for_fp4(c);
+  return ffn_fp4_planned(mb) ? do_plan(c, offsets, plan, mb, s) : MOE_OK;
+}
+
 int do_gate_up_fp4(const moe_config_t* c, const uint16_t* x, const int32_t* psrc,
-                   const int32_t* plan, const Fp4Matrix& w, uint16_t* h, hipStream_t s) {
+                   const int32_t* offsets, const int32_t* plan, const Fp4Matrix& w, uint16_t* h,
+                   hipStream_t s) {
   return hip_status(launch_grouped_gemm_fp4(mb_for_fp4(c), true, x, psrc, c->topk, w.q, w.s, h,
-                                            plan, (int)max_tiles_for(c), c->hidden,
+                                            offsets, plan, (int)max_tiles_for(c), c->hidden,
                                             c->intermediate, c->intermediate, s,
                                             bounds_of(c, true)));
 }
 
-int do_down_fp4(const moe_config_t* c, const uint16_t* h, const int32_t* plan, const Fp4Matrix& w,
-                uint16_t* y, hipStream_t s) {
+int do_down_fp4(const moe_config_t* c, const uint16_t* h, const int32_t* offsets,
+                const int32_t* plan, const Fp4Matrix& w, uint16_t* y, hipStream_t s) {
   return hip_status(launch_grouped_gemm_fp4(mb_for_fp4(c), false, h, nullptr, c->topk, w.q, w.s, y,
-                                            plan, (int)max_tiles_for(c), c->intermediate,
+                                            offsets, plan, (int)max_tiles_for(c), c->intermediate,
                                             c->hidden, 0, s, bounds_of(c, false)));
 }
 
@@ -266,10 +272,10 @@ int do_ffn_fp4(const moe_config_t* c, const uint16_t* x, const int32_t* psrc,
                void* scratch, hipStream_t s) {
   int32_t* plan = static_cast<int32_t*>(scratch);
   uint16_t* h = reinterpret_cast<uint16_t*>(static_cast<char*>(scratch) + plan_bytes(c));
-  int st = do_plan(c, offsets, plan, mb_for_fp4(c), s);
+  int st = do_plan_fp4(c, offsets, plan, s);
   if (st) return st;
-  if ((st = do_gate_up_fp4(c, x, psrc, plan, gu, h, s))) return st;
-  return do_down_fp4(c, h, plan, down, y, s);
+  if ((st = do_gate_up_fp4(c, x, psrc, offsets, plan, gu, h, s))) return st;
+  return do_down_fp4(c, h, offsets, plan, down, y, s);
 }
 
 // Bytes of a code and a scale array of n weights.
@@ -809,8 +815,8 @@ int moe_expert_gate_up_fp4(const moe_config_t* cfg, const uint16_t* x, const int
   if ((st = device_ready())) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   int32_t* plan = static_cast<int32_t*>(workspace);
-  if ((st = do_plan(cfg, offsets, plan, mb_for_fp4(cfg), s))) return st;
-  return do_gate_up_fp4(cfg, x, perm_src, plan, gu, h, s);
+  if ((st = do_plan_fp4(cfg, offsets, plan, s))) return st;
+  return do_gate_up_fp4(cfg, x, perm_src, offsets, plan, gu, h, s);
 }
 
 int moe_expert_down_fp4(const moe_config_t* cfg, const uint16_t* h, const int32_t* offsets,
@@ -826,8 +832,8 @@ int moe_expert_down_fp4(const moe_config_t* cfg, const uint16_t* h, const int32_
   if ((st = device_ready())) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   int32_t* plan = static_cast<int32_t*>(workspace);
-  if ((st = do_plan(cfg, offsets, plan, mb_for_fp4(cfg), s))) return st;
-  return do_down_fp4(cfg, h, plan, down, y_perm, s);
+  if ((st = do_plan_fp4(cfg, offsets, plan, s))) return st;
+  return do_down_fp4(cfg, h, offsets, plan, down, y_perm, s);
 }
 
 int moe_layer_forward_fp4(const moe_config_t* cfg, const uint16_t* x, const float* w_router,

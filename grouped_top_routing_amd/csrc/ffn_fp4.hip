@@ -127,33 +127,35 @@ __global__ __launch_bounds__(256) void pack_fp4_kernel(const uint8_t* __restrict
 
 // ---------------------------------------------------------------------------
 // The grouped GEMM.  A work item is an m-tile (up to 16 MB rows of one expert)
-// times 256 of its weight rows (gate/up: 128 gate rows and the matching up
+// times 64 CG of its weight rows (gate/up: 32 CG gate rows and the matching up
 // rows), walked by a persistent grid.
 //
-// Waves form RG row groups x 4 column groups: a wave computes 4 column blocks
+// Waves form RG row groups x CG column groups: a wave computes 4 column blocks
 // (gate/up: 2 gate blocks and their up blocks) for its share of the item's
-// 16-row blocks.  Codes, scales and rows are staged in LDS by direct loads:
-//   W stage q: 128 k of the 16 blocks' code fragments (16 KB) and scales (1 KB),
-//              in slot q % SW
-//   A stage p: 64 k of the item's rows, 2 KB per row block, in slot p % SA; each
-//              row's 128 bytes with its 16-byte chunks swizzled by (row / 2) % 8,
-//              so that the 16 rows of an operand read hit distinct banks
-// A wave reads its codes of 64 k once (8 bytes per block and lane) and widens them
-// to bf16 operands in registers, one MFMA step ahead and between the MFMAs of the
-// step before: an MFMA holds the matrix cores for 16 cycles and the issue port for
-// 4, so that the conversions fit beside it.
+// 16-row blocks.  Up to 96 rows RG is 1 and a CU holds two workgroups of CG 4,
+// which meet at no barrier: one's MFMAs run while the other waits, issues loads or
+// writes its outputs.  Taller tiles have RG 2 and a CU to themselves: they load the
+// weights of more rows once, and a row block is read from LDS by four waves, not
+// eight.  A few tokens' items are single waves (CG 1), so that one token's eight
+// experts still fill the CUs.
 //
-// Schedule.  Iteration p (64 k, two MFMA steps) waits for A(p + 1), and W((p + 1)
-// / 2) where that is new, passes a barrier, and refills the slots that every
-// wave has read by then: A(p + SA), then for odd p W((p - 1) / 2 + SW) (codes of
-// stage p are read after the barrier of iteration p - 1).  The loads before the
-// loop are those of iterations below 0 in the same order, so one rule gives every
-// wait (wait_next).  A workgroup issues its next item's
-// first loads before the current item's outputs are written.
-constexpr int kBlocks = 16;      // weight-row blocks of an item
+// Codes, scales and rows are staged in LDS by direct loads, 64 k at a time in a
+// ring of S slots: per column block half a code fragment (512 bytes) and the scales
+// of 128 k (64 bytes), per row block 2 KB: a row's 128 bytes with their 16-byte chunks
+// swizzled by (row / 2) % 8, so that the 16 rows of an operand read hit distinct
+// banks.  A wave reads its codes of a stage once (8 bytes per block and lane) and
+// widens them to bf16 operands in registers, one MFMA step ahead and between the
+// MFMAs of the step before: an MFMA holds the matrix cores for 16 cycles and the
+// issue port for 4, so that the conversions fit beside it.
+//
+// Schedule.  Stage p is two MFMA steps.  After the first one the wave waits for
+// stage p + 1 and for its own LDS reads, passes the barrier, refills the slot of
+// stage p (which every wave has read by then) with stage p + S, reads the codes of
+// stage p + 1, and takes the second step while it reads that stage's rows.  A
+// workgroup issues its next item's first S stages before the current item's outputs
+// are written.
 constexpr int kCols = 4;         // column blocks per wave
-constexpr int kColGroups = kBlocks / kCols;
-constexpr int kSlotW = kBlocks * (kCodeB + kScaleB);
+constexpr int kHalfB = kCodeB / 2;  // codes of a block's 64 k
 constexpr int kBlockA = 2048;    // bytes of 64 k of a row block
 
 // One direct global -> LDS load of 4 bytes per lane (see lds_dma16_sv).
@@ -182,44 +184,103 @@ struct Fp4Args {
   uint16_t* C;
   const int32_t* plan;
   int max_tiles, K, n_out, up_row0;
+  const int32_t* offsets;
   GemmBounds bounds;
 };
 
-template <int MB, int RG, int SA, int SW, bool SWIGLU>
+// Where the items' rows are.  A plan that was built before (tile_plan_kernel) ...
+struct PlanTiles {
+  const int* at;
+  int max_tiles;
+  __device__ __forceinline__ PlanTiles(const Fp4Args& a, int) : at(a.plan), max_tiles(a.max_tiles) {}
+  __device__ __forceinline__ int count() const { return at[0]; }
+  __device__ __forceinline__ void get(int tile, int& e, int& row0, int& nrows) const {
+    e = at[4 + tile];
+    row0 = at[4 + max_tiles + tile];
+    nrows = at[4 + 2 * max_tiles + tile];
+  }
+};
+// ... or, for 16-row tiles, worked out by each single-wave workgroup: lane l holds
+// experts 4l .. 4l + 3 of 256, their first rows and the number of their first tile.
+// One token's call is a launch shorter by it (plan 2.3 us and its gap).
+struct OwnTiles {
+  int lane, first[4], row[5], total;
+  __device__ __forceinline__ OwnTiles(const Fp4Args& a, int lane_) : lane(lane_) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) row[i] = a.offsets[4 * lane + i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      first[i] = n;
+      n += (row[i + 1] - row[i] + 15) >> 4;
+    }
+    int upto = n;  // tiles of the lanes up to this one
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int v = __shfl_up(upto, off);
+      upto += lane >= off ? v : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) first[i] += upto - n;
+    total = __builtin_amdgcn_readlane(upto, 63);
+  }
+  __device__ __forceinline__ int count() const { return total; }
+  __device__ __forceinline__ void get(int tile, int& e, int& row0, int& nrows) const {
+    e = row0 = 0;
+    nrows = 1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = row[i] + 16 * (tile - first[i]);  // the tile's first row, if it is this expert's
+      const uint64_t has = __ballot(tile >= first[i] && r < row[i + 1]);
+      if (has) {
+        const int l = __builtin_ctzll(has);
+        e = 4 * l + i;
+        row0 = __builtin_amdgcn_readlane(r, l);
+        nrows = min(16, __builtin_amdgcn_readlane(row[i + 1], l) - row0);
+      }
+    }
+  }
+};
+
+template <int MB, int RG, int CG, int S, bool SWIGLU>
 struct Fp4Gemm {
-  static constexpr int NW = kColGroups * RG;
-  static constexpr int NBL = kCols / RG;              // code fragments a wave loads per W stage
-  static constexpr int AMAX = (MB + NW - 1) / NW;     // row blocks a wave loads per A stage
+  static constexpr int NW = CG * RG;
+  static constexpr int kBlocks = CG * kCols;          // weight-row blocks of an item
+  static constexpr int kSlotW = kBlocks * (kHalfB + kScaleB);
+  static constexpr int AMAX = (MB + NW - 1) / NW;     // row blocks a wave loads
   static constexpr int RB = (MB + RG - 1) / RG;       // row blocks a wave computes, at most
+  static constexpr int kLoadsW = kCols / 2 / RG + 1;  // a wave's code and scale loads of a stage
   static constexpr int HALF = SWIGLU ? kCols / 2 : kCols;
-  static constexpr int WCOLS = kColGroups * HALF * 16;
-  static constexpr int kLoadsW = NBL + 1;             // direct loads of a W stage per wave
-  static constexpr int kSlotA = MB * kBlockA;
-  static constexpr int kLds = SW * kSlotW + SA * kSlotA;
-  static_assert(SA % 2 == 1 && 2 * SW > SA + 1, "a W stage is issued before the A stage it is waited with");
-  static_assert(kLds <= 160 * 1024, "LDS");
+  static constexpr int WCOLS = CG * HALF * 16;
+  static constexpr int kSlot = kSlotW + MB * kBlockA;
+  static constexpr int kLds = S * kSlot;
+  static_assert(S >= 3 && (S - 1) * (2 * AMAX + kLoadsW) < 64, "vmcnt holds 6 bits");
+  static_assert((RG == 1 || RG == 2) && kLds <= NW * 20 * 1024, "eight waves per CU");
+
+  using Tiles = std::conditional_t<NW == 1 && MB == 1, OwnTiles, PlanTiles>;
 
   const Fp4Args& a;
   uint8_t* lds;
+  Tiles tiles;
   int lane, wave, r, g, cg, rg;
-  int nst, nw;                 // A and W stages of an item
+  int nst;                        // stages of an item (even)
   // the item whose loads are in flight
   int row0, nrows, ntile, na;
   const uint16_t* arow[AMAX][2];  // this lane's 16 bytes of stage 0 of the rows it loads
-  const uint8_t* code;            // expert's codes and scales, at the next W stage
-  const uint8_t* scale;
-  uint32_t code_off[NBL], scale_off;
-  uint32_t next_a, next_w;        // slots that the next stages go to (bytes into the ring)
+  const uint8_t* code;            // the expert's codes, at the next stage to load
+  const uint8_t* scale;           // its scales
+  uint32_t code_off[kCols / 2 / RG], scale_off;
+  uint32_t next;                  // its slot (bytes into the ring)
 
-  __device__ __forceinline__ Fp4Gemm(const Fp4Args& args, uint8_t* mem) : a(args), lds(mem) {
+  __device__ __forceinline__ Fp4Gemm(const Fp4Args& args, uint8_t* mem)
+      : a(args), lds(mem), tiles(args, threadIdx.x & 63) {
     lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     r = lane & 15;
     g = lane >> 4;
-    cg = wave % kColGroups;
-    rg = wave / kColGroups;
+    cg = wave % CG;
+    rg = wave / CG;
     nst = a.K / 64;
-    nw = a.K / kStageK;
   }
 
   // first weight row of column block j of this wave
@@ -227,65 +288,55 @@ struct Fp4Gemm {
     return ntile * WCOLS + (cg * HALF + j % HALF) * 16 + (j >= HALF ? a.up_row0 : 0);
   }
 
-  __device__ __forceinline__ uint32_t lds_base() const {
-    return (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)lds);
-  }
-
-  __device__ __forceinline__ void issue_a(int p) {
-    const uint32_t slot = lds_base() + SW * kSlotW + next_a + (uint32_t)wave * kBlockA;
+  // Loads of stage p, the next one.
+  __device__ __forceinline__ void issue(int p) {
+    BEAM_CHECK(p >= 0 && p < nst, kCheckWeightOffset);
+    const uint32_t slot =
+        (uint32_t)(uintptr_t)((__attribute__((address_space(3))) uint8_t*)lds) + next;
+#pragma unroll
+    for (int t = 0; t < kCols / 2 / RG; ++t)  // a pair of column blocks, 32 lanes each
+      lds_dma16_sv<true>(code, code_off[t],
+                         slot + (uint32_t)(cg * kCols + 2 * (rg + RG * t)) * kHalfB);
+    // (RG 2: both waves of a column group load its four blocks' scales, the same
+    // bytes to the same place, so that all waves count alike)
+    lds_dma4_sv(scale, scale_off, slot + kBlocks * kHalfB + (uint32_t)(cg * kCols) * kScaleB);
 #pragma unroll
     for (int j = 0; j < AMAX; ++j)
       if (j < na) {
-        lds_dma16(arow[j][0] + p * 64, slot + NW * j * kBlockA);
-        lds_dma16(arow[j][1] + p * 64, slot + NW * j * kBlockA + 1024);
+        const uint32_t to = slot + kSlotW + (uint32_t)(wave + NW * j) * kBlockA;
+        lds_dma16(arow[j][0] + p * 64, to);
+        lds_dma16(arow[j][1] + p * 64, to + 1024);
       }
-    next_a = next_a + kSlotA == SA * kSlotA ? 0 : next_a + kSlotA;
+    code += kHalfB;
+    scale += p & 1 ? kScaleB : 0;
+    next = next + kSlot == kLds ? 0 : next + kSlot;
   }
-  __device__ __forceinline__ void issue_w(int q) {
-    BEAM_CHECK(q >= 0 && q < nw, kCheckWeightOffset);
-    const uint32_t slot = lds_base() + next_w;
-#pragma unroll
-    for (int t = 0; t < NBL; ++t)
-      lds_dma16_sv<true>(code, code_off[t], slot + (uint32_t)(cg * kCols + rg + RG * t) * kCodeB);
-    // every wave of a column group loads its four blocks' scales: the same
-    // bytes to the same place, so that all waves count alike
-    lds_dma4_sv(scale, scale_off, slot + kBlocks * kCodeB + (uint32_t)(cg * kCols) * kScaleB);
-    code += kCodeB;
-    scale += kScaleB;
-    next_w = next_w + kSlotW == SW * kSlotW ? 0 : next_w + kSlotW;
-  }
-  // loads of iteration p
-  __device__ __forceinline__ void issue(int p) {
-    if (p + SA >= 0 && p + SA < nst) issue_a(p + SA);
-    if (p & 1) {
-      const int q = ((p - 1) >> 1) + SW;
-      if (q >= 0 && q < nw) issue_w(q);
+
+  // Waits until at most `stages` stages of this wave's loads are in flight.
+  template <int STAGES, int NA = AMAX>
+  __device__ __forceinline__ void wait_stages() {
+    if constexpr (NA == 0) {
+      wait_vm<STAGES * kLoadsW>();
+    } else {
+      if (na == NA) wait_vm<STAGES*(2 * NA + kLoadsW)>();
+      else wait_stages<STAGES, NA - 1>();
     }
   }
-  // Waits for A(p + 1), and so for every older load: as many of this wave's
-  // loads may stay in flight as were issued after it, namely A(p + 2) .. A(p +
-  // SA - 1) and the W stages of the odd iterations p + 1 - SA .. p - 1.
-  __device__ __forceinline__ void wait_next(int p) {
-    constexpr int kA = SA - 2, kW = (SA - 1) / 2;
-    const int last_w = (p >> 1) - 1 + SW;  // of the latest odd iteration below p
-    if (p + SA - 1 < nst && last_w < nw) {
-      if (na == AMAX) wait_vm<2 * AMAX * kA + kLoadsW * kW>();
-      else wait_vm<2 * (AMAX - 1) * kA + kLoadsW * kW>();
+  template <int STAGES>
+  __device__ __forceinline__ void wait_stages_dyn(int stages) {
+    if constexpr (STAGES == 0) {
+      wait_vm<0>();
     } else {
-      const int as = min(max(nst - 2 - p, 0), kA);
-      const int ws = min(max(nw - 1 - (last_w - kW), 0), kW);
-      wait_vm_dyn<0, 2 * AMAX * kA + kLoadsW * kW>(2 * na * as + kLoadsW * ws);
+      if (stages >= STAGES) wait_stages<STAGES>();
+      else wait_stages_dyn<STAGES - 1>(stages);
     }
   }
 
-  // Takes item `tile`, `nt` and issues its first loads.
+  // Takes item `tile`, `nt` and issues its first stages.
   __device__ __forceinline__ void start(int tile, int nt) {
-    const int* plan_expert = a.plan + 4;
-    const int* plan_row0 = plan_expert + a.max_tiles;
-    const int* plan_rows = plan_row0 + a.max_tiles;
-    const int e = BEAM_CLAMP(plan_expert[tile], 0, a.bounds.n_experts - 1, kCheckPlanRows);
-    row0 = plan_row0[tile];
-    nrows = plan_rows[tile];
+    int e;
+    tiles.get(tile, e, row0, nrows);
+    e = BEAM_CLAMP(e, 0, a.bounds.n_experts - 1, kCheckPlanRows);
     ntile = nt;
     BEAM_CHECK(nrows >= 1 && nrows <= 16 * MB && row0 >= 0 &&
                    (int64_t)row0 + nrows <= a.bounds.n_rows, kCheckPlanRows);
@@ -293,7 +344,7 @@ struct Fp4Gemm {
     na = (nrb - wave + NW - 1) / NW;
     // Rows past the tile repeat its last.  The gather's indices are scalar
     // loads of uniform addresses, which the vector memory counter that the
-    // rings are waited on with does not count.
+    // ring is waited on with does not count.
 #pragma unroll
     for (int j = 0; j < AMAX; ++j) {
       const int blk = __builtin_amdgcn_readfirstlane((wave + NW * j) * 16);
@@ -320,32 +371,34 @@ struct Fp4Gemm {
       }
     }
     const int64_t blocks = (SWIGLU ? 2 * (int64_t)a.n_out : a.n_out) / 16;
-    code = a.Q + e * blocks * nw * kCodeB;
-    scale = a.S + e * blocks * nw * kScaleB;
+    const int nfrag = a.K / kStageK;
+    code = a.Q + e * blocks * nfrag * kCodeB;
+    scale = a.S + e * blocks * nfrag * kScaleB;
 #pragma unroll
-    for (int t = 0; t < NBL; ++t)
-      code_off[t] = (uint32_t)BEAM_CLAMP(weight_row(rg + RG * t) >> 4, 0, blocks - 1,
-                                         kCheckWeightOffset) * (uint32_t)(nw * kCodeB) +
-                    (uint32_t)lane * 16u;
+    for (int t = 0; t < kCols / 2 / RG; ++t)
+      code_off[t] = (uint32_t)BEAM_CLAMP(weight_row(2 * (rg + RG * t) + (lane >> 5)) >> 4, 0,
+                                         blocks - 1, kCheckWeightOffset) *
+                        (uint32_t)(nfrag * kCodeB) +
+                    (uint32_t)(lane & 31) * 16u;
     // lane l loads the scales of row l % 16 of column block l / 16
     int block = 0;
 #pragma unroll
     for (int j = 0; j < kCols; ++j) block = g == j ? weight_row(j) >> 4 : block;
-    scale_off = (uint32_t)block * (uint32_t)(nw * kScaleB) + (uint32_t)r * 4u;
-    next_a = next_w = 0;
-    constexpr int kFirst = SA > 2 * SW ? SA : 2 * SW;
+    scale_off = (uint32_t)block * (uint32_t)(nfrag * kScaleB) + (uint32_t)r * 4u;
+    next = 0;
 #pragma unroll
-    for (int p = -kFirst; p < 0; ++p) issue(p);
+    for (int p = 0; p < S; ++p)
+      if (p < nst) issue(p);
   }
 
-  // One item with this wave's N row blocks from block row_off; then `next` starts
+  // One item with this wave's N row blocks from block row_off; then `then` starts
   // the following one, and the outputs are written.
-  template <int N, class Next>
-  __device__ __forceinline__ void item(int row_off, Next next) {
+  template <int N, class Then>
+  __device__ __forceinline__ void item(int row_off, Then then) {
     constexpr int NX = N > 0 ? N : 1;
     f32x4_t acc[NX][kCols];
 #pragma unroll
-    for (int i = 0; i < NX; ++i)
+    for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int j = 0; j < kCols; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     uint4 af[NX];
@@ -354,21 +407,20 @@ struct Fp4Gemm {
     bf16x8_t b0[kCols], b1[kCols];
     // this lane's operand (row r, chunk g) inside a row block's 2 KB; the second
     // 32 k (chunk 4 + g) flips bit 6
-    const uint8_t* abase = lds + SW * kSlotW + row_off * kBlockA;
+    const uint8_t* abase = lds + kSlotW + row_off * kBlockA;
     const int aoff = (r >> 3) * 1024 + (r & 7) * 128 + ((g ^ a_chunk(r)) << 4);
-    const uint8_t* wbase = lds + cg * kCols * kCodeB + 8 * lane;
-    const uint8_t* sbase = lds + kBlocks * kCodeB + cg * kCols * kScaleB + 4 * r;
+    const uint8_t* wbase = lds + cg * kCols * kHalfB + 8 * lane;
+    const uint8_t* sbase = lds + kBlocks * kHalfB + cg * kCols * kScaleB + 4 * r;
     auto read_a = [&](uint32_t slot, int half, int i) {
       return *reinterpret_cast<const uint4*>(abase + slot + i * kBlockA + (aoff ^ (half << 6)));
     };
-    // codes of half a W stage, and with its first half its scales
-    auto read_w = [&](uint32_t slot, int half) {
-      if constexpr (N > 0) {
+    // a stage's codes, and in even stages the scales of two
+    auto read_w = [&](uint32_t slot, bool scales) {
+      if constexpr (N == 0) return;
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) {
-          cw[j] = *reinterpret_cast<const uint2*>(wbase + slot + j * kCodeB + half * (kCodeB / 2));
-          if (half == 0) sw[j] = *reinterpret_cast<const uint32_t*>(sbase + slot + j * kScaleB);
-        }
+      for (int j = 0; j < kCols; ++j) {
+        cw[j] = *reinterpret_cast<const uint2*>(wbase + slot + j * kHalfB);
+        if (scales) sw[j] = *reinterpret_cast<const uint32_t*>(sbase + slot + j * kScaleB);
       }
     };
     // operands of step s (of the 128 k that sw covers) of column block j
@@ -380,140 +432,142 @@ struct Fp4Gemm {
     // its codes were read.
     auto step = [&](const bf16x8_t (&b)[kCols], bf16x8_t (&bn)[kCols], int s, uint32_t slot,
                     int half, auto late) {
-      if constexpr (N > 0) {
-        constexpr int LATE = decltype(late)::value < N ? decltype(late)::value : N - 1;
-        int done = 0;
+      if constexpr (N == 0) return;
+      constexpr int LATE = decltype(late)::value < NX ? decltype(late)::value : NX - 1;
+      int done = 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int upto = i < LATE ? 0 : (i - LATE + 1) * kCols / (N - LATE);
+      for (int i = 0; i < N; ++i) {
+        const int upto = i < LATE ? 0 : (i - LATE + 1) * kCols / (NX - LATE);
 #pragma unroll
-          for (int j = 0; j < kCols; ++j)
-            acc[i][j] =
-                __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], as_bf16x8(af[i]), acc[i][j], 0, 0, 0);
-          af[i] = read_a(slot, half, i);
+        for (int j = 0; j < kCols; ++j)
+          acc[i][j] =
+              __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], as_bf16x8(af[i]), acc[i][j], 0, 0, 0);
+        af[i] = read_a(slot, half, i);
 #pragma unroll
-          for (int j = 0; j < kCols; ++j)
-            if (j >= done && j < upto) bn[j] = widen(s, j);
-          // of this row block: an MFMA, its share of the conversions, and so on
-          const int n = (6 * (upto - done) + kCols - 1) / kCols;
-          done = upto;
+        for (int j = 0; j < kCols; ++j)
+          if (j >= done && j < upto) bn[j] = widen(s, j);
+        // of this row block: an MFMA, its share of the conversions, and so on
+        const int n = (6 * (upto - done) + kCols - 1) / kCols;
+        done = upto;
 #pragma unroll
-          for (int j = 0; j < kCols; ++j) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            if (n <= 0) continue;
-            if (n <= 2) __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
-            else if (n <= 3) __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
-            else __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
-          }
-          __builtin_amdgcn_sched_barrier(0);
+        for (int j = 0; j < kCols; ++j) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          if (n <= 0) continue;
+          if (n <= 2) __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+          else if (n <= 3) __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+          else __builtin_amdgcn_sched_group_barrier(0x002, 6, 0);
         }
-        // computed here, not sunk to their use behind the next barrier
-#pragma unroll
-        for (int j = 0; j < kCols; ++j) asm volatile("" : "+v"(bn[j]));
+        __builtin_amdgcn_sched_barrier(0);
       }
+      // computed here, not sunk to their use behind the next barrier
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) asm volatile("" : "+v"(bn[j]));
     };
     using Late0 = std::integral_constant<int, 0>;
     using Late1 = std::integral_constant<int, 1>;
-    auto pass = [&](int p) {  // makes A(p + 1) (and its W stage) visible
-      wait_next(p);
+    auto pass = [&]() {  // this wave's reads have landed; every wave's loads are visible
       wait_lgkm0();
       stage_barrier();
     };
+    auto after = [](uint32_t slot) { return slot + kSlot == kLds ? 0u : slot + kSlot; };
 
-    uint32_t as = 0, ws = 0;  // slots of A(2q) and W(q)
-    pass(-1);
-    if constexpr (N > 0) {
-      read_w(0, 0);
+    uint32_t at = 0;  // slot of the current stage
+    wait_stages_dyn<S - 1>(nst - 1);
+    pass();
+    read_w(0, true);
 #pragma unroll
-      for (int i = 0; i < N; ++i) af[i] = read_a(0, 0, i);
+    for (int i = 0; i < N; ++i) af[i] = read_a(0, 0, i);
+    if constexpr (N > 0) {
 #pragma unroll
       for (int j = 0; j < kCols; ++j) b0[j] = widen(0, j);
     }
-    int q = 0;
-    for (; q + 1 < nw; ++q) {  // iterations 2q and 2q + 1
-      const int p = 2 * q;
-      const uint32_t as1 = as + kSlotA == SA * kSlotA ? 0 : as + kSlotA;
-      const uint32_t as2 = as1 + kSlotA == SA * kSlotA ? 0 : as1 + kSlotA;
-      const uint32_t ws1 = ws + kSlotW == SW * kSlotW ? 0 : ws + kSlotW;
-      step(b0, b1, 1, as, 1, Late0{});
-      pass(p);
-      read_w(ws, 1);
-      issue(p);
-      step(b1, b0, 2, as1, 0, Late1{});
-      step(b0, b1, 3, as1, 1, Late0{});
-      pass(p + 1);
-      read_w(ws1, 0);
-      issue(p + 1);
-      step(b1, b0, 0, as2, 0, Late1{});
-      as = as2;
-      ws = ws1;
-    }
-    {  // the last W stage
-      const uint32_t as1 = as + kSlotA == SA * kSlotA ? 0 : as + kSlotA;
-      step(b0, b1, 1, as, 1, Late0{});
-      pass(2 * q);
-      read_w(ws, 1);
-      step(b1, b0, 2, as1, 0, Late1{});
-      step(b0, b1, 3, as1, 1, Late0{});
-      if constexpr (N > 0) {
+    // stages p and p + 1 (p even); ALL: with stages p + S and p + 1 + S to come
+    int p = 0;
+    auto turn = [&](auto all) {
+      constexpr bool ALL = decltype(all)::value;
+      const uint32_t at1 = after(at), at2 = after(at1);
+      step(b0, b1, 1, at, 1, Late0{});
+      if constexpr (ALL) wait_stages<S - 2>();
+      else wait_stages_dyn<S - 2>(nst - 2 - p);
+      pass();
+      read_w(at1, false);
+      if (ALL || p + S < nst) issue(p + S);
+      step(b1, b0, 2, at1, 0, Late1{});
+      step(b0, b1, 3, at1, 1, Late0{});
+      if constexpr (ALL) wait_stages<S - 2>();
+      else wait_stages_dyn<S - 2>(nst - 3 - p);
+      pass();
+      read_w(at2, true);
+      if (ALL || p + 1 + S < nst) issue(p + 1 + S);
+      step(b1, b0, 0, at2, 0, Late1{});
+      at = at2;
+      p += 2;
+    };
+    for (; p + 1 + S < nst; ) turn(std::true_type{});
+    for (; p + 2 < nst; ) turn(std::false_type{});
+    {  // the last two stages
+      const uint32_t at1 = after(at);
+      step(b0, b1, 1, at, 1, Late0{});
+      wait_vm<0>();
+      pass();
+      read_w(at1, false);
+      step(b1, b0, 2, at1, 0, Late1{});
+      step(b0, b1, 3, at1, 1, Late0{});
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+      for (int i = 0; i < N; ++i)
 #pragma unroll
-          for (int j = 0; j < kCols; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[j], as_bf16x8(af[i]),
-                                                                acc[i][j], 0, 0, 0);
-      }
+        for (int j = 0; j < kCols; ++j)
+          acc[i][j] =
+              __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[j], as_bf16x8(af[i]), acc[i][j], 0, 0, 0);
     }
-    wait_lgkm0();
-    stage_barrier();  // every wave is done with the rings
+    pass();  // every wave is done with the ring
 
     const int out_row0 = row0, out_rows = nrows, col0 = ntile * WCOLS + cg * HALF * 16;
-    next();
+    then();
 
     // The weights are the first operand: lane (r, g) holds output columns 4g ..
     // 4g + 3 of row r of each 16 x 16 block.  Blocks j and j + 1 trade halves
     // between lane rows, so that a lane stores 8 columns at once; a lane whose
     // row lies past the tile gets an offset outside the store's range.
-    if constexpr (N > 0) {
-      const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(
-          a.C + (size_t)out_row0 * a.n_out, 0, out_rows * a.n_out * 2, kBufferRsrcWord3);
-      int er = r, eg = g;  // opaque: the offsets are formed here, not kept through the loop
-      asm volatile("" : "+v"(er), "+v"(eg));
-      auto outputs = [&](int i, int j) {
-        float o[4];
+    if constexpr (N == 0) return;
+    const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(
+        a.C + (size_t)out_row0 * a.n_out, 0, out_rows * a.n_out * 2, kBufferRsrcWord3);
+    int er = r, eg = g;  // opaque: the offsets are formed here, not kept through the loop
+    asm volatile("" : "+v"(er), "+v"(eg));
+    auto outputs = [&](int i, int j) {
+      float o[4];
 #pragma unroll
-        for (int v = 0; v < 4; ++v)
-          o[v] = SWIGLU ? silu_mul(acc[i][j][v], acc[i][j + (SWIGLU ? HALF : 0)][v]) : acc[i][j][v];
-        return u32x2_t{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
-      };
+      for (int v = 0; v < 4; ++v)
+        o[v] = SWIGLU ? silu_mul(acc[i][j][v], acc[i][j + (SWIGLU ? HALF : 0)][v]) : acc[i][j][v];
+      return u32x2_t{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
+    };
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int row = (row_off + i) * 16 + er;
+    for (int i = 0; i < N; ++i) {
+      const int row = (row_off + i) * 16 + er;
 #pragma unroll
-        for (int j = 0; j < HALF; j += 2) {
-          const u32x2_t d0 = outputs(i, j), d1 = outputs(i, j + 1);
-          const auto sx = __builtin_amdgcn_permlane16_swap(d0[0], d1[0], false, false);
-          const auto sy = __builtin_amdgcn_permlane16_swap(d0[1], d1[1], false, false);
-          const int col = col0 + (j + (eg & 1)) * 16 + 4 * (eg & ~1);
-          const uint32_t off = row < out_rows ? (uint32_t)(row * a.n_out + col) * 2u : 0x80000000u;
-          const u32x4_t d = {sx[0], sy[0], sx[1], sy[1]};
-          __builtin_amdgcn_raw_buffer_store_b128(d, out, off, 0, 0);
-        }
+      for (int j = 0; j < HALF; j += 2) {
+        const u32x2_t d0 = outputs(i, j), d1 = outputs(i, j + 1);
+        const auto sx = __builtin_amdgcn_permlane16_swap(d0[0], d1[0], false, false);
+        const auto sy = __builtin_amdgcn_permlane16_swap(d0[1], d1[1], false, false);
+        const int col = col0 + (j + (eg & 1)) * 16 + 4 * (eg & ~1);
+        const uint32_t off = row < out_rows ? (uint32_t)(row * a.n_out + col) * 2u : 0x80000000u;
+        const u32x4_t d = {sx[0], sy[0], sx[1], sy[1]};
+        __builtin_amdgcn_raw_buffer_store_b128(d, out, off, 0, 0);
       }
     }
   }
 
-  template <int N, class Next>
-  __device__ __forceinline__ void dispatch(int n, int row_off, Next next) {
+  template <int N, class Then>
+  __device__ __forceinline__ void dispatch(int n, int row_off, Then then) {
     if constexpr (N <= RB) {
-      if (n == N) item<N>(row_off, next);
-      else dispatch<N + 1>(n, row_off, next);
+      if (n == N) item<N>(row_off, then);
+      else dispatch<N + 1>(n, row_off, then);
     }
   }
 
   __device__ __forceinline__ void run() {
     const int nt_n = a.n_out / WCOLS;
-    const int total = a.plan[0] * nt_n;
+    const int total = tiles.count() * nt_n;
     const int grid = balanced_grid(total, gridDim.x), per_xcd = grid / 8;
     if ((int)blockIdx.x >= grid) return;  // whole workgroup
     int q = (blockIdx.x % 8) * per_xcd + blockIdx.x / 8;
@@ -523,24 +577,24 @@ struct Fp4Gemm {
       q += grid;
       // row group 0 takes the first half of the item's row blocks, rounded up
       const int nrb = (nrows + 15) >> 4, half = RG == 1 ? nrb : (nrb + 1) / 2;
-      dispatch<0>(rg == 0 ? half : nrb - half, rg == 0 ? 0 : half, [&]() {
+      dispatch<RG == 1 ? 1 : 0>(rg == 0 ? half : nrb - half, rg == 0 ? 0 : half, [&]() {
         if (q < total) start(q / nt_n, q % nt_n);
       });
     }
   }
 };
 
-template <int MB, int RG, int SA, int SW, bool SWIGLU>
-__global__ __launch_bounds__(256 * RG, 1) void gemm_fp4_kernel(Fp4Args args) {
-  using G = Fp4Gemm<MB, RG, SA, SW, SWIGLU>;
+template <int MB, int RG, int CG, int S, bool SWIGLU>
+__global__ __launch_bounds__(64 * CG * RG, 2) void gemm_fp4_kernel(Fp4Args args) {
+  using G = Fp4Gemm<MB, RG, CG, S, SWIGLU>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[G::kLds];
   G(args, lds).run();
 }
 
-template <int MB, int RG, int SA, int SW, bool SWIGLU>
+template <int MB, int RG, int CG, int S, bool SWIGLU>
 static hipError_t launch_fp4(const Fp4Args& args, hipStream_t stream) {
-  using G = Fp4Gemm<MB, RG, SA, SW, SWIGLU>;
-  auto kern = gemm_fp4_kernel<MB, RG, SA, SW, SWIGLU>;
+  using G = Fp4Gemm<MB, RG, CG, S, SWIGLU>;
+  auto kern = gemm_fp4_kernel<MB, RG, CG, S, SWIGLU>;
   static int resident = 0;  // workgroups that the device holds, fixed per build
   if (resident == 0) {
     int dev = 0, n = 0, occ = 0;
@@ -555,27 +609,36 @@ static hipError_t launch_fp4(const Fp4Args& args, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// m-tile height from the mean rows per expert.
+// m-tile height from the mean rows per expert.  Times of the three calls at the
+// Beam shape (hidden 5120, intermediate 2560) in us, tiles of 16 / 64 / 96 / 192
+// rows: 1 token 50 / 55 / 63 / 59, 32 tokens 612 / 612 / 640 / 737, 512 tokens 1333
+// / 1004 / 1053 / 1201, 1400 tokens - / 1237 / 1284 / 1521, 2000 tokens - / 1774 /
+// 1471 / 1711, 3200 tokens - / 2449 / 2387 / 2069.
 int ffn_fp4_choose_mb(int64_t rows, int E) {
   const int64_t mean = rows / (E > 0 ? E : 1);
-  if (mean <= 24) return 2;
-  if (mean <= 80) return 8;
+  if (rows <= E / 4) return 1;
+  if (mean <= 50) return 4;
+  if (mean <= 80) return 6;
   return 12;
 }
 
+bool ffn_fp4_planned(int mb) { return mb != 1; }
+
 hipError_t launch_grouped_gemm_fp4(int mb, bool swiglu, const uint16_t* A, const int32_t* gather,
                                    int topk, const uint8_t* Q, const uint8_t* S, uint16_t* C,
-                                   const int32_t* plan, int max_tiles, int K, int n_out,
-                                   int up_row0, hipStream_t stream, const GemmBounds& bounds) {
-  const Fp4Args args{A, gather, topk, Q, S, C, plan, max_tiles, K, n_out, up_row0, bounds};
-#define BEAM_FP4_CASE(MBV, RGV, SAV, SWV)                                \
+                                   const int32_t* offsets, const int32_t* plan, int max_tiles,
+                                   int K, int n_out, int up_row0, hipStream_t stream,
+                                   const GemmBounds& bounds) {
+  const Fp4Args args{A, gather, topk, Q, S, C, plan, max_tiles, K, n_out, up_row0, offsets, bounds};
+#define BEAM_FP4_CASE(MBV, RGV, CGV, SV)                                 \
   case MBV:                                                              \
-    return swiglu ? launch_fp4<MBV, RGV, SAV, SWV, true>(args, stream)   \
-                  : launch_fp4<MBV, RGV, SAV, SWV, false>(args, stream);
+    return swiglu ? launch_fp4<MBV, RGV, CGV, SV, true>(args, stream)    \
+                  : launch_fp4<MBV, RGV, CGV, SV, false>(args, stream);
   switch (mb) {
-    BEAM_FP4_CASE(2, 1, 3, 4)
-    BEAM_FP4_CASE(8, 2, 3, 5)
-    BEAM_FP4_CASE(12, 2, 3, 4)
+    BEAM_FP4_CASE(1, 1, 1, 4)
+    BEAM_FP4_CASE(4, 1, 4, 4)
+    BEAM_FP4_CASE(6, 1, 4, 3)
+    BEAM_FP4_CASE(12, 2, 4, 4)
     default:
       return hipErrorInvalidValue;
   }

@@ -91,10 +91,13 @@ hipError_t launch_quantize_fp8(const uint16_t* w, uint8_t* q, float* scales, int
 
 // 4-bit expert weights (ffn_fp4.hip): code and scale fragments.
 int ffn_fp4_choose_mb(int64_t rows, int E);
+// whether the GEMM at m-tile height 16 * mb reads the plan (else the offsets)
+bool ffn_fp4_planned(int mb);
 hipError_t launch_grouped_gemm_fp4(int mb, bool swiglu, const uint16_t* A, const int32_t* gather,
                                    int topk, const uint8_t* Q, const uint8_t* S, uint16_t* C,
-                                   const int32_t* plan, int max_tiles, int K, int n_out,
-                                   int up_row0, hipStream_t stream, const GemmBounds& bounds);
+                                   const int32_t* offsets, const int32_t* plan, int max_tiles,
+                                   int K, int n_out, int up_row0, hipStream_t stream,
+                                   const GemmBounds& bounds);
 hipError_t launch_quantize_fp4(const uint16_t* w, uint8_t* q, uint8_t* s, int E, int N, int K,
                                hipStream_t stream);
 hipError_t launch_pack_fp4(const uint8_t* codes, const uint8_t* scales, uint8_t* q, uint8_t* s,
