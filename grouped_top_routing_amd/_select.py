@@ -127,7 +127,8 @@ def balance_loss(logits, topk_ids, *, score="softmax", coef=1e-2, workspace=None
     cfg = _config(T, E, k, score, True, dt)
     nb = _balance_bytes(T, E, k, score, dt)
     if T == 0:
-        return torch.zeros((), device=dev), torch.zeros(E, device=dev)
+        return (torch.zeros((), dtype=torch.float32, device=dev),
+                torch.zeros(E, dtype=torch.float32, device=dev))
     loss = torch.empty((), dtype=torch.float32, device=dev)
     load = torch.empty(E, dtype=torch.float32, device=dev)
     ws = _scratch(nb, dev, workspace)

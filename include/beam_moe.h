@@ -313,7 +313,9 @@ int moe_layer_forward_fp8(const moe_config_t* cfg, const uint16_t* x, const floa
  * Codes and scales are 16-byte aligned.  The *_fp4 calls require
  * cfg->weight_layout == MOE_LAYOUT_FP4_PACKED (else MOE_ERR_INVALID_ARG); their
  * workspace sizes are the ones moe_workspace_bytes gives for that layout and
- * MOE_ENTRY_EXPERT_FFN, MOE_ENTRY_EXPERT_STAGE and MOE_ENTRY_LAYER.
+ * MOE_ENTRY_EXPERT_FFN, MOE_ENTRY_EXPERT_STAGE and MOE_ENTRY_LAYER.  hidden *
+ * intermediate is below 2^32, each of them at most 2^22 (else
+ * MOE_ERR_UNSUPPORTED).
  */
 /*
  * Quantise row-major bf16 expert weights into the packed form.  The scale of a

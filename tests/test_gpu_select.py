@@ -443,6 +443,12 @@ def test_empty_batches():
     assert ids.shape == (0, 4) and w.shape == (0, 4)
     loss, load = gtr.balance_loss(z, ids)
     assert float(loss) == 0 and load.shape == (64,) and not load.any()
+    torch.set_default_dtype(torch.float64)
+    try:
+        loss, load = gtr.balance_loss(z, ids)
+    finally:
+        torch.set_default_dtype(torch.float32)
+    assert loss.dtype == load.dtype == torch.float32
     assert gtr.select_backward(z, ids, w).shape == (0, 64)
     ids, w, zz = gtr.route_select(torch.zeros(0, 256, dtype=BF, device=DEV),
                                   torch.zeros(256, 256, device=DEV), return_logits=True)

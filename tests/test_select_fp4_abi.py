@@ -147,6 +147,9 @@ def test_fp4_calls_check_layout_configuration_and_pointers(call):
     assert call(_cfg(T=-1)) == INVALID
     assert call(_cfg(T=0, H=500)) == UNSUPPORTED and call(_cfg(T=0, I=100)) == UNSUPPORTED
     assert call(_cfg(T=1 << 28)) == UNSUPPORTED
+    assert call(_cfg(T=0, H=1 << 16, I=1 << 15)) == L.MOE_OK
+    assert call(_cfg(T=0, H=1 << 16, I=1 << 16)) == UNSUPPORTED  # an expert past 32 bits
+    assert call(_cfg(T=0, H=1 << 23)) == UNSUPPORTED and call(_cfg(T=0, I=1 << 23)) == UNSUPPORTED
     assert call(_cfg(), nb=16) == WORKSPACE and call(_cfg(), ws=None) == WORKSPACE
     names = [n for n in inspect.signature(call).parameters if n not in ("c", "nb", "ws")]
     for n in names:
@@ -189,6 +192,9 @@ def test_fp4_weights_check_their_arrays():
     assert q(A, B, C, D, C, P) == INVALID  # one output twice
     assert lib.moe_quantize_fp4(ctypes.byref(gtr.make_config(0, 512, 100)), A, None, B, C, None,
                                 None, None) == UNSUPPORTED
+    big = ctypes.byref(gtr.make_config(0, 1 << 16, 1 << 16))
+    assert lib.moe_quantize_fp4(big, None, None, None, None, None, None, None) == UNSUPPORTED
+    assert lib.moe_pack_fp4(big, *[None] * 8, None) == UNSUPPORTED
     p = lambda *a: lib.moe_pack_fp4(c, *a, None)
     assert p(*[None] * 8) == L.MOE_OK
     assert p(A, B, None, None, C, None, None, None) == INVALID
