@@ -19,7 +19,7 @@ using namespace beam;
 int mb_for(const moe_config_t* c) { return ffn_choose_mb(pairs(c), c->num_experts); }
 int mb_for_fp8(const moe_config_t* c) { return ffn_fp8_choose_mb(pairs(c), c->num_experts); }
 
-int mb_for_fp4(const moe_config_t* c) { return ffn_fp4_choose_mb(pairs(c), c->num_experts); }
+int mb_for_fp4(const moe_config_t* c) { return ffn_fp4_choose_mb(pairs(c), c->num_experts, (int64_t)c->hidden * c->intermediate); }
 
 // Upper bound on the m-tiles of the plan (one workspace size serves the bf16
 // and the fp8 entry points; the 4-bit layout has its own).
@@ -278,9 +278,26 @@ int do_ffn_fp4(const moe_config_t* c, const uint16_t* x, const int32_t* psrc,
   return do_down_fp4(c, h, offsets, plan, down, y, s);
 }
 
+// The kernels address an expert's codes with 32 bits and an m-tile's outputs with
+// 31.
+int validate_fp4(const moe_config_t* c, int layouts) {
+  const int st = validate(c, layouts);
+  if (st) return st;
+  if ((int64_t)c->hidden * c->intermediate >= (int64_t)1 << 32 || c->hidden > 1 << 22 ||
+      c->intermediate > 1 << 22)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 // Bytes of a code and a scale array of n weights.
 int64_t codes4(int64_t n) { return n / 2; }
 int64_t scales4(int64_t n) { return n / 32; }
+// Weights of all experts' down matrices (half of gate/up's), and bytes of the pairs'
+// rows of n columns.
+int64_t fp4_weights(const moe_config_t* c) {
+  return (int64_t)c->num_experts * c->hidden * c->intermediate;
+}
+int64_t rows_bytes(const moe_config_t* c, int64_t n) { return pairs(c) * n * 2; }
 
 // The whole block around an expert-MLP step `ffn(x, psrc, offsets, y, scratch)`.
 template <class Ffn>
@@ -726,7 +743,7 @@ int moe_quantize_fp4(const moe_config_t* cfg, const uint16_t* w_gate_up, const u
   moe_config_t c = cfg ? *cfg : moe_config_t{};
   c.num_tokens = 0;
   c.weight_layout = MOE_LAYOUT_ROW_MAJOR;  // not read here
-  int st = validate(cfg ? &c : nullptr);
+  int st = validate_fp4(cfg ? &c : nullptr, kBf16Layouts);
   if (st) return st;
   const bool gu = w_gate_up || q_gate_up || s_gate_up;
   const bool dn = w_down || q_down || s_down;
@@ -757,7 +774,7 @@ int moe_pack_fp4(const moe_config_t* cfg, const uint8_t* c_gate_up, const uint8_
   moe_config_t c = cfg ? *cfg : moe_config_t{};
   c.num_tokens = 0;
   c.weight_layout = MOE_LAYOUT_ROW_MAJOR;  // not read here
-  int st = validate(cfg ? &c : nullptr);
+  int st = validate_fp4(cfg ? &c : nullptr, kBf16Layouts);
   if (st) return st;
   const bool gu = c_gate_up || r_gate_up || q_gate_up || s_gate_up;
   const bool dn = c_down || r_down || q_down || s_down;
@@ -787,7 +804,7 @@ int moe_expert_ffn_fp4(const moe_config_t* cfg, const uint16_t* x, const int32_t
                        const int32_t* offsets, const uint8_t* q_gate_up, const uint8_t* s_gate_up,
                        const uint8_t* q_down, const uint8_t* s_down, uint16_t* y_perm,
                        void* workspace, size_t workspace_bytes, void* stream) {
-  int st = validate(cfg, kFp4Layouts);
+  int st = validate_fp4(cfg, kFp4Layouts);
   if (st) return st;
   const Fp4Matrix gu{q_gate_up, s_gate_up}, down{q_down, s_down};
   if (!x || !perm_src || !offsets || !y_perm || !gu.ok() || !down.ok()) return MOE_ERR_INVALID_ARG;
@@ -795,6 +812,12 @@ int moe_expert_ffn_fp4(const moe_config_t* cfg, const uint16_t* x, const int32_t
     return MOE_ERR_INVALID_ARG;
   if ((st = check_ws(workspace, workspace_bytes, ffn_ws(cfg)))) return st;
   if (cfg->num_tokens == 0) return MOE_OK;
+  const int64_t w = fp4_weights(cfg);
+  if (!apart({{y_perm, rows_bytes(cfg, cfg->hidden)}, {workspace, (int64_t)ffn_ws(cfg)}},
+             {{x, cfg->num_tokens * cfg->hidden * 2}, {perm_src, pairs(cfg) * 4},
+              {offsets, (cfg->num_experts + 1) * 4}, {q_gate_up, codes4(2 * w)},
+              {s_gate_up, scales4(2 * w)}, {q_down, codes4(w)}, {s_down, scales4(w)}}))
+    return MOE_ERR_INVALID_ARG;
   if ((st = device_ready())) return st;
   return do_ffn_fp4(cfg, x, perm_src, offsets, gu, down, y_perm, workspace,
                     static_cast<hipStream_t>(stream));
@@ -804,7 +827,7 @@ int moe_expert_gate_up_fp4(const moe_config_t* cfg, const uint16_t* x, const int
                            const int32_t* offsets, const uint8_t* q_gate_up,
                            const uint8_t* s_gate_up, uint16_t* h, void* workspace,
                            size_t workspace_bytes, void* stream) {
-  int st = validate(cfg, kFp4Layouts);
+  int st = validate_fp4(cfg, kFp4Layouts);
   if (st) return st;
   const Fp4Matrix gu{q_gate_up, s_gate_up};
   if (!x || !perm_src || !offsets || !h || !gu.ok()) return MOE_ERR_INVALID_ARG;
@@ -812,6 +835,12 @@ int moe_expert_gate_up_fp4(const moe_config_t* cfg, const uint16_t* x, const int
     return MOE_ERR_INVALID_ARG;
   if ((st = check_ws(workspace, workspace_bytes, plan_bytes(cfg)))) return st;
   if (cfg->num_tokens == 0) return MOE_OK;
+  const int64_t w = fp4_weights(cfg);
+  if (!apart({{h, rows_bytes(cfg, cfg->intermediate)}, {workspace, (int64_t)plan_bytes(cfg)}},
+             {{x, cfg->num_tokens * cfg->hidden * 2}, {perm_src, pairs(cfg) * 4},
+              {offsets, (cfg->num_experts + 1) * 4}, {q_gate_up, codes4(2 * w)},
+              {s_gate_up, scales4(2 * w)}}))
+    return MOE_ERR_INVALID_ARG;
   if ((st = device_ready())) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   int32_t* plan = static_cast<int32_t*>(workspace);
@@ -822,13 +851,18 @@ int moe_expert_gate_up_fp4(const moe_config_t* cfg, const uint16_t* x, const int
 int moe_expert_down_fp4(const moe_config_t* cfg, const uint16_t* h, const int32_t* offsets,
                         const uint8_t* q_down, const uint8_t* s_down, uint16_t* y_perm,
                         void* workspace, size_t workspace_bytes, void* stream) {
-  int st = validate(cfg, kFp4Layouts);
+  int st = validate_fp4(cfg, kFp4Layouts);
   if (st) return st;
   const Fp4Matrix down{q_down, s_down};
   if (!h || !offsets || !y_perm || !down.ok()) return MOE_ERR_INVALID_ARG;
   if (!aligned16(h) || !aligned16(y_perm) || !aligned4(offsets)) return MOE_ERR_INVALID_ARG;
   if ((st = check_ws(workspace, workspace_bytes, plan_bytes(cfg)))) return st;
   if (cfg->num_tokens == 0) return MOE_OK;
+  const int64_t w = fp4_weights(cfg);
+  if (!apart({{y_perm, rows_bytes(cfg, cfg->hidden)}, {workspace, (int64_t)plan_bytes(cfg)}},
+             {{h, rows_bytes(cfg, cfg->intermediate)}, {offsets, (cfg->num_experts + 1) * 4},
+              {q_down, codes4(w)}, {s_down, scales4(w)}}))
+    return MOE_ERR_INVALID_ARG;
   if ((st = device_ready())) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   int32_t* plan = static_cast<int32_t*>(workspace);
@@ -841,7 +875,7 @@ int moe_layer_forward_fp4(const moe_config_t* cfg, const uint16_t* x, const floa
                           const uint8_t* s_gate_up, const uint8_t* q_down, const uint8_t* s_down,
                           uint16_t* out, int32_t* topk_ids_out, float* topk_w_out,
                           void* workspace, size_t workspace_bytes, void* stream) {
-  int st = validate(cfg, kFp4Layouts);
+  int st = validate_fp4(cfg, kFp4Layouts);
   if (st) return st;
   const Fp4Matrix gu{q_gate_up, s_gate_up}, down{q_down, s_down};
   if (!layer_args_ok(cfg, x, w_router, sel_bias, out, topk_ids_out, topk_w_out) || !gu.ok() ||

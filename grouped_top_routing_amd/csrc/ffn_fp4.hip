@@ -50,7 +50,7 @@ __device__ __forceinline__ float e8m0_value(uint32_t code) { return __uint_as_fl
 
 }  // namespace
 
-// One thread per 32 consecutive weights of a row.
+// One thread per 32 consecutive weights of a row.  Load time only; bound by HBM.
 __global__ __launch_bounds__(256) void quantize_fp4_kernel(const uint16_t* __restrict__ w,
                                                            uint8_t* __restrict__ q,
                                                            uint8_t* __restrict__ s, int K,
@@ -96,7 +96,8 @@ __global__ __launch_bounds__(256) void quantize_fp4_kernel(const uint16_t* __res
 }
 
 // Row-major codes (two per byte, the lower k in the low half) and scales into
-// fragments: one thread per lane of a fragment.
+// fragments: one thread per lane of a fragment.  Gate/up of 256 experts of 5120 x
+// 2560 (3.6 GB read, 3.6 written) take 1.78 ms, 4 TB/s.
 __global__ __launch_bounds__(256) void pack_fp4_kernel(const uint8_t* __restrict__ codes,
                                                        const uint8_t* __restrict__ scales,
                                                        uint8_t* __restrict__ q,
@@ -154,6 +155,14 @@ __global__ __launch_bounds__(256) void pack_fp4_kernel(const uint8_t* __restrict
 // stage p + 1, and takes the second step while it reads that stage's rows.  A
 // workgroup issues its next item's first S stages before the current item's outputs
 // are written.
+//
+// Measured at 256 experts of 5120 x 2560, gate/up and down in us: 1 token 27 and 14
+// (4.0 TB/s of codes and scales: launch and first latencies), 32 tokens 350 and 178
+// (6.5 TB/s: bound by HBM; a copy of the loop that only loads takes 0.96 of it), 512
+// tokens 605 and 348 (5.8 and 5.2 TB/s, HBM), 4096 tokens 1550 and 800 (1.1
+// PFLOP/s; MFMAs take 52 % of the cycles, load issue and LDS reads do not hide behind
+// them: without the loads 1244, without the MFMAs 960, without the widening no
+// change).
 constexpr int kCols = 4;         // column blocks per wave
 constexpr int kHalfB = kCodeB / 2;  // codes of a block's 64 k
 constexpr int kBlockA = 2048;    // bytes of 64 k of a row block
@@ -609,14 +618,20 @@ static hipError_t launch_fp4(const Fp4Args& args, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// m-tile height from the mean rows per expert.  Times of the three calls at the
-// Beam shape (hidden 5120, intermediate 2560) in us, tiles of 16 / 64 / 96 / 192
-// rows: 1 token 50 / 55 / 63 / 59, 32 tokens 612 / 612 / 640 / 737, 512 tokens 1333
-// / 1004 / 1053 / 1201, 1400 tokens - / 1237 / 1284 / 1521, 2000 tokens - / 1774 /
-// 1471 / 1711, 3200 tokens - / 2449 / 2387 / 2069.
-int ffn_fp4_choose_mb(int64_t rows, int E) {
+// m-tile height from the mean rows per expert.  Times of an MLP call at the Beam
+// shape (hidden 5120, intermediate 2560) in us, tiles of 16 / 64 / 96 / 192 rows:
+// 1 token 43 / 56, 5 tokens 137 / 154, 10 tokens 250 / 240, 32 tokens 584 / 581 /
+// 640 / 737, 512 tokens 1333 / 1004 / 1053 / 1201, 1400 tokens - / 1237 / 1284 /
+// 1521, 2000 tokens - / 1774 / 1471 / 1711, 3200 tokens - / 2449 / 2387 / 2069.
+// Where the experts in use are small (`weights`: hidden * intermediate of each), the
+// launch that 16-row tiles save counts with more rows too, tiles of 16 / 64: 1024 x
+// 512 at 160 rows 25.0 / 27.8, 800 rows 42.9 / 47.5, 2048 rows 52.0 / 49.5; 768 x
+// 384 at 1015 rows 30.1 / 36.2; 2048 x 1024 at 80 rows 52 / 65, 480 rows 139.5 /
+// 139.5, 1600 rows 164 / 154.
+int ffn_fp4_choose_mb(int64_t rows, int E, int64_t weights) {
   const int64_t mean = rows / (E > 0 ? E : 1);
   if (rows <= E / 4) return 1;
+  if (rows <= 4 * E && (rows < E ? rows : E) * weights <= (int64_t)1 << 28) return 1;
   if (mean <= 50) return 4;
   if (mean <= 80) return 6;
   return 12;

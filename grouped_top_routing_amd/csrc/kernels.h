@@ -90,7 +90,7 @@ hipError_t launch_quantize_fp8(const uint16_t* w, uint8_t* q, float* scales, int
                                hipStream_t stream);
 
 // 4-bit expert weights (ffn_fp4.hip): code and scale fragments.
-int ffn_fp4_choose_mb(int64_t rows, int E);
+int ffn_fp4_choose_mb(int64_t rows, int E, int64_t weights);
 // whether the GEMM at m-tile height 16 * mb reads the plan (else the offsets)
 bool ffn_fp4_planned(int mb);
 hipError_t launch_grouped_gemm_fp4(int mb, bool swiglu, const uint16_t* A, const int32_t* gather,

@@ -338,7 +338,8 @@ int moe_pack_fp4(const moe_config_t* cfg, const uint8_t* c_gate_up, const uint8_
                  uint8_t* s_gate_up, uint8_t* q_down, uint8_t* s_down, void* stream);
 
 /* moe_expert_ffn, moe_expert_gate_up, moe_expert_down and moe_layer_forward
- * with 4-bit expert weights (arguments as in those calls). */
+ * with 4-bit expert weights (arguments as in those calls; the expert calls
+ * refuse outputs or a workspace that overlap another argument). */
 int moe_expert_ffn_fp4(const moe_config_t* cfg, const uint16_t* x, const int32_t* perm_src,
                        const int32_t* offsets, const uint8_t* q_gate_up, const uint8_t* s_gate_up,
                        const uint8_t* q_down, const uint8_t* s_down, uint16_t* y_perm,

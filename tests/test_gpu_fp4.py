@@ -154,7 +154,8 @@ def edge_counts(mean):
 LOADS = {"one": [1] + [0] * 255, "last": [0] * 255 + [7], "few": [2, 0, 1] * 85 + [3],
          "edges": edge_counts(0), "edges, mean 60": edge_counts(60),
          "edges, mean 100": edge_counts(100), "edges, mean 200": edge_counts(200),
-         "all to one": [0] * 17 + [1500] + [0] * 238, "sixteens": [16] * 256,
+         "all to one": [0] * 17 + [1500] + [0] * 238,
+         "most to one": [1, 0] * 20 + [800, 17, 0, 33, 64] + [0] * 211, "sixteens": [16] * 256,
          "33 each": [33] * 256}
 
 

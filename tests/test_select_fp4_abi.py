@@ -160,6 +160,19 @@ def test_fp4_calls_check_layout_configuration_and_pointers(call):
             assert call(_cfg(T=0), **{n: MIS}) == INVALID, n
 
 
+@pytest.mark.parametrize("call,written", [(_ffn, "y"), (_gate_up, "h"), (_down, "y")])
+def test_fp4_calls_refuse_overlapping_memory(call, written):
+    at = lambda n: ctypes.c_void_p(n << 44)
+    names = [n for n in inspect.signature(call).parameters if n not in ("c", "nb")]
+    apart = {n: at(i + 1) for i, n in enumerate(names)}
+    for n in names:
+        for out in {written, "ws"} - {n}:
+            assert call(_cfg(), **{**apart, n: apart[out]}) == INVALID, (n, out)
+            assert call(_cfg(T=0), **{**apart, n: apart[out]}) == L.MOE_OK
+    inside = ctypes.c_void_p(apart[written].value + 64 * 8 * 256 * 2 - 16)
+    assert call(_cfg(), **{**apart, "off": inside}) == INVALID
+
+
 def test_bf16_and_fp8_calls_refuse_the_fp4_layout():
     c = ctypes.byref(_cfg(T=0))
     assert gtr.lib().moe_expert_down(c, A, A, A, A, A, BIG, None) == INVALID
