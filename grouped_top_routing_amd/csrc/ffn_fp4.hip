@@ -138,7 +138,8 @@ __global__ __launch_bounds__(256) void pack_fp4_kernel(const uint8_t* __restrict
 // writes its outputs.  Taller tiles have RG 2 and a CU to themselves: they load the
 // weights of more rows once, and a row block is read from LDS by four waves, not
 // eight.  A few tokens' items are single waves (CG 1), so that one token's eight
-// experts still fill the CUs.
+// experts still fill the CUs; of up to 1024 such items KS = 2 waves take half of the k
+// each, in rings of their own, and the first adds the second's sums.
 //
 // Codes, scales and rows are staged in LDS by direct loads, 64 k at a time in a
 // ring of S slots: per column block half a code fragment (512 bytes) and the scales
@@ -156,8 +157,8 @@ __global__ __launch_bounds__(256) void pack_fp4_kernel(const uint8_t* __restrict
 // workgroup issues its next item's first S stages before the current item's outputs
 // are written.
 //
-// Measured at 256 experts of 5120 x 2560, gate/up and down in us: 1 token 27 and 14
-// (4.0 TB/s of codes and scales: launch and first latencies), 32 tokens 350 and 178
+// Measured at 256 experts of 5120 x 2560, gate/up and down in us: 1 token 23 and 12
+// (4.7 TB/s of codes and scales: launch and first latencies), 32 tokens 350 and 178
 // (6.5 TB/s: bound by HBM; a copy of the loop that only loads takes 0.96 of it), 512
 // tokens 605 and 348 (5.8 and 5.2 TB/s, HBM), 4096 tokens 1550 and 800 (1.1
 // PFLOP/s; MFMAs take 52 % of the cycles, load issue and LDS reads do not hide behind
@@ -251,7 +252,7 @@ struct OwnTiles {
   }
 };
 
-template <int MB, int RG, int CG, int S, bool SWIGLU>
+template <int MB, int RG, int CG, int S, int KS, bool SWIGLU>
 struct Fp4Gemm {
   static constexpr int NW = CG * RG;
   static constexpr int kBlocks = CG * kCols;          // weight-row blocks of an item
@@ -264,6 +265,7 @@ struct Fp4Gemm {
   static constexpr int kSlot = kSlotW + MB * kBlockA;
   static constexpr int kLds = S * kSlot;
   static_assert(S >= 3 && (S - 1) * (2 * AMAX + kLoadsW) < 64, "vmcnt holds 6 bits");
+  static_assert(KS == 1 || (NW == 1 && MB == 1 && kCols * 1024 <= kLds), "a wave's sums fit its ring");
   static_assert((RG == 1 || RG == 2) && kLds <= NW * 20 * 1024, "eight waves per CU");
 
   using Tiles = std::conditional_t<NW == 1 && MB == 1, OwnTiles, PlanTiles>;
@@ -272,7 +274,8 @@ struct Fp4Gemm {
   uint8_t* lds;
   Tiles tiles;
   int lane, wave, r, g, cg, rg;
-  int nst;                        // stages of an item (even)
+  int kw;                         // of KS waves that share an item's k
+  int k0, nst;                    // first stage and stages of an item (even)
   // the item whose loads are in flight
   int row0, nrows, ntile, na;
   const uint16_t* arow[AMAX][2];  // this lane's 16 bytes of stage 0 of the rows it loads
@@ -285,11 +288,20 @@ struct Fp4Gemm {
       : a(args), lds(mem), tiles(args, threadIdx.x & 63) {
     lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    k0 = kw = 0;
+    nst = a.K / 64;
+    if constexpr (KS > 1) {  // whole fragments of 128 k; a wave may have none
+      kw = wave;
+      wave = 0;
+      lds += kw * kLds;
+      const int frags = a.K / kStageK;
+      k0 = kw * frags / KS * 2;
+      nst = (kw + 1) * frags / KS * 2 - k0;
+    }
     r = lane & 15;
     g = lane >> 4;
     cg = wave % CG;
     rg = wave / CG;
-    nst = a.K / 64;
   }
 
   // first weight row of column block j of this wave
@@ -376,13 +388,13 @@ struct Fp4Gemm {
           x /= a.topk;
         }
         x = BEAM_CLAMP(x, 0, a.bounds.n_src - 1, kCheckTokenIndex);
-        arow[j][hf] = a.A + (size_t)x * a.K + 8 * ((lane & 7) ^ a_chunk(hf * 8 + (lane >> 3)));
+        arow[j][hf] = a.A + (size_t)x * a.K + k0 * 64 + 8 * ((lane & 7) ^ a_chunk(hf * 8 + (lane >> 3)));
       }
     }
     const int64_t blocks = (SWIGLU ? 2 * (int64_t)a.n_out : a.n_out) / 16;
     const int nfrag = a.K / kStageK;
-    code = a.Q + e * blocks * nfrag * kCodeB;
-    scale = a.S + e * blocks * nfrag * kScaleB;
+    code = a.Q + e * blocks * nfrag * kCodeB + k0 * kHalfB;
+    scale = a.S + e * blocks * nfrag * kScaleB + k0 / 2 * kScaleB;
 #pragma unroll
     for (int t = 0; t < kCols / 2 / RG; ++t)
       code_off[t] = (uint32_t)BEAM_CLAMP(weight_row(2 * (rg + RG * t) + (lane >> 5)) >> 4, 0,
@@ -476,60 +488,77 @@ struct Fp4Gemm {
     using Late1 = std::integral_constant<int, 1>;
     auto pass = [&]() {  // this wave's reads have landed; every wave's loads are visible
       wait_lgkm0();
-      stage_barrier();
+      if constexpr (KS == 1) stage_barrier();
+      else compiler_fence();  // a ring of the wave's own
     };
     auto after = [](uint32_t slot) { return slot + kSlot == kLds ? 0u : slot + kSlot; };
 
-    uint32_t at = 0;  // slot of the current stage
-    wait_stages_dyn<S - 1>(nst - 1);
-    pass();
-    read_w(0, true);
-#pragma unroll
-    for (int i = 0; i < N; ++i) af[i] = read_a(0, 0, i);
-    if constexpr (N > 0) {
-#pragma unroll
-      for (int j = 0; j < kCols; ++j) b0[j] = widen(0, j);
-    }
-    // stages p and p + 1 (p even); ALL: with stages p + S and p + 1 + S to come
-    int p = 0;
-    auto turn = [&](auto all) {
-      constexpr bool ALL = decltype(all)::value;
-      const uint32_t at1 = after(at), at2 = after(at1);
-      step(b0, b1, 1, at, 1, Late0{});
-      if constexpr (ALL) wait_stages<S - 2>();
-      else wait_stages_dyn<S - 2>(nst - 2 - p);
+    if (KS == 1 || nst > 0) {
+      uint32_t at = 0;  // slot of the current stage
+      wait_stages_dyn<S - 1>(nst - 1);
       pass();
-      read_w(at1, false);
-      if (ALL || p + S < nst) issue(p + S);
-      step(b1, b0, 2, at1, 0, Late1{});
-      step(b0, b1, 3, at1, 1, Late0{});
-      if constexpr (ALL) wait_stages<S - 2>();
-      else wait_stages_dyn<S - 2>(nst - 3 - p);
-      pass();
-      read_w(at2, true);
-      if (ALL || p + 1 + S < nst) issue(p + 1 + S);
-      step(b1, b0, 0, at2, 0, Late1{});
-      at = at2;
-      p += 2;
-    };
-    for (; p + 1 + S < nst; ) turn(std::true_type{});
-    for (; p + 2 < nst; ) turn(std::false_type{});
-    {  // the last two stages
-      const uint32_t at1 = after(at);
-      step(b0, b1, 1, at, 1, Late0{});
-      wait_vm<0>();
-      pass();
-      read_w(at1, false);
-      step(b1, b0, 2, at1, 0, Late1{});
-      step(b0, b1, 3, at1, 1, Late0{});
+      read_w(0, true);
 #pragma unroll
-      for (int i = 0; i < N; ++i)
+      for (int i = 0; i < N; ++i) af[i] = read_a(0, 0, i);
+      if constexpr (N > 0) {
 #pragma unroll
-        for (int j = 0; j < kCols; ++j)
-          acc[i][j] =
-              __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[j], as_bf16x8(af[i]), acc[i][j], 0, 0, 0);
+        for (int j = 0; j < kCols; ++j) b0[j] = widen(0, j);
+      }
+      // stages p and p + 1 (p even); ALL: with stages p + S and p + 1 + S to come
+      int p = 0;
+      auto turn = [&](auto all) {
+        constexpr bool ALL = decltype(all)::value;
+        const uint32_t at1 = after(at), at2 = after(at1);
+        step(b0, b1, 1, at, 1, Late0{});
+        if constexpr (ALL) wait_stages<S - 2>();
+        else wait_stages_dyn<S - 2>(nst - 2 - p);
+        pass();
+        read_w(at1, false);
+        if (ALL || p + S < nst) issue(p + S);
+        step(b1, b0, 2, at1, 0, Late1{});
+        step(b0, b1, 3, at1, 1, Late0{});
+        if constexpr (ALL) wait_stages<S - 2>();
+        else wait_stages_dyn<S - 2>(nst - 3 - p);
+        pass();
+        read_w(at2, true);
+        if (ALL || p + 1 + S < nst) issue(p + 1 + S);
+        step(b1, b0, 0, at2, 0, Late1{});
+        at = at2;
+        p += 2;
+      };
+      for (; p + 1 + S < nst; ) turn(std::true_type{});
+      for (; p + 2 < nst; ) turn(std::false_type{});
+      {  // the last two stages
+        const uint32_t at1 = after(at);
+        step(b0, b1, 1, at, 1, Late0{});
+        wait_vm<0>();
+        pass();
+        read_w(at1, false);
+        step(b1, b0, 2, at1, 0, Late1{});
+        step(b0, b1, 3, at1, 1, Late0{});
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+          for (int j = 0; j < kCols; ++j)
+            acc[i][j] =
+                __builtin_amdgcn_mfma_f32_16x16x32_bf16(b1[j], as_bf16x8(af[i]), acc[i][j], 0, 0, 0);
+      }
     }
     pass();  // every wave is done with the ring
+    if constexpr (KS > 1 && N > 0) {  // the waves' sums, added in their order
+      f32x4_t* sums = reinterpret_cast<f32x4_t*>(lds);
+      if (kw > 0)
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) sums[j * 64 + lane] = acc[0][j];
+      __syncthreads();
+      if (kw == 0)
+#pragma unroll
+        for (int w = 1; w < KS; ++w)
+#pragma unroll
+          for (int j = 0; j < kCols; ++j)
+            acc[0][j] += reinterpret_cast<const f32x4_t*>(lds + w * kLds)[j * 64 + lane];
+      __syncthreads();  // read before the next item's loads
+    }
 
     const int out_row0 = row0, out_rows = nrows, col0 = ntile * WCOLS + cg * HALF * 16;
     then();
@@ -539,6 +568,7 @@ struct Fp4Gemm {
     // between lane rows, so that a lane stores 8 columns at once; a lane whose
     // row lies past the tile gets an offset outside the store's range.
     if constexpr (N == 0) return;
+    if (kw > 0) return;
     const __amdgpu_buffer_rsrc_t out = __builtin_amdgcn_make_buffer_rsrc(
         a.C + (size_t)out_row0 * a.n_out, 0, out_rows * a.n_out * 2, kBufferRsrcWord3);
     int er = r, eg = g;  // opaque: the offsets are formed here, not kept through the loop
@@ -593,34 +623,34 @@ struct Fp4Gemm {
   }
 };
 
-template <int MB, int RG, int CG, int S, bool SWIGLU>
-__global__ __launch_bounds__(64 * CG * RG, 2) void gemm_fp4_kernel(Fp4Args args) {
-  using G = Fp4Gemm<MB, RG, CG, S, SWIGLU>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[G::kLds];
+template <int MB, int RG, int CG, int S, int KS, bool SWIGLU>
+__global__ __launch_bounds__(64 * CG * RG * KS, 2) void gemm_fp4_kernel(Fp4Args args) {
+  using G = Fp4Gemm<MB, RG, CG, S, KS, SWIGLU>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[KS * G::kLds];
   G(args, lds).run();
 }
 
-template <int MB, int RG, int CG, int S, bool SWIGLU>
+template <int MB, int RG, int CG, int S, int KS, bool SWIGLU>
 static hipError_t launch_fp4(const Fp4Args& args, hipStream_t stream) {
-  using G = Fp4Gemm<MB, RG, CG, S, SWIGLU>;
-  auto kern = gemm_fp4_kernel<MB, RG, CG, S, SWIGLU>;
+  using G = Fp4Gemm<MB, RG, CG, S, KS, SWIGLU>;
+  auto kern = gemm_fp4_kernel<MB, RG, CG, S, KS, SWIGLU>;
   static int resident = 0;  // workgroups that the device holds, fixed per build
   if (resident == 0) {
     int dev = 0, n = 0, occ = 0;
     hipError_t err = hipGetDevice(&dev);
     if (err == hipSuccess) err = hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev);
-    if (err == hipSuccess) err = hipOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, 64 * G::NW, 0);
+    if (err == hipSuccess) err = hipOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, 64 * G::NW * KS, 0);
     if (err != hipSuccess) return err;
     resident = n * (occ > 0 ? occ : 1);
   }
   const int64_t grid = persistent_grid(resident, (int64_t)args.max_tiles * (args.n_out / G::WCOLS));
-  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(64 * G::NW), 0, stream, args);
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(64 * G::NW * KS), 0, stream, args);
   return hipGetLastError();
 }
 
 // m-tile height from the mean rows per expert.  Times of an MLP call at the Beam
 // shape (hidden 5120, intermediate 2560) in us, tiles of 16 / 64 / 96 / 192 rows:
-// 1 token 43 / 56, 5 tokens 137 / 154, 10 tokens 250 / 240, 32 tokens 584 / 581 /
+// 1 token 39 / 56, 5 tokens 137 / 154, 10 tokens 250 / 240, 32 tokens 584 / 581 /
 // 640 / 737, 512 tokens 1333 / 1004 / 1053 / 1201, 1400 tokens - / 1237 / 1284 /
 // 1521, 2000 tokens - / 1774 / 1471 / 1711, 3200 tokens - / 2449 / 2387 / 2069.
 // Where the experts in use are small (`weights`: hidden * intermediate of each), the
@@ -645,15 +675,22 @@ hipError_t launch_grouped_gemm_fp4(int mb, bool swiglu, const uint16_t* A, const
                                    int K, int n_out, int up_row0, hipStream_t stream,
                                    const GemmBounds& bounds) {
   const Fp4Args args{A, gather, topk, Q, S, C, plan, max_tiles, K, n_out, up_row0, offsets, bounds};
-#define BEAM_FP4_CASE(MBV, RGV, CGV, SV)                                 \
-  case MBV:                                                              \
-    return swiglu ? launch_fp4<MBV, RGV, CGV, SV, true>(args, stream)    \
-                  : launch_fp4<MBV, RGV, CGV, SV, false>(args, stream);
+#define BEAM_FP4_CASE(MBV, RGV, CGV, SV, KSV)                                 \
+  case MBV:                                                                   \
+    return swiglu ? launch_fp4<MBV, RGV, CGV, SV, KSV, true>(args, stream)    \
+                  : launch_fp4<MBV, RGV, CGV, SV, KSV, false>(args, stream);
+  // A token's few items: two waves share each one's k.  In us, one wave / two: 1 token
+  // of 5120 x 2560 (720 items) 42.5 / 38.7, 4 of 1024 x 512 15.8 / 15.2, but 2 of 5120
+  // x 2560 (1360 items, the CUs hold 1024 pairs) 66.8 / 70.9, 100 of 1024 x 512 42.8 /
+  // 49.0; four waves 38.6, 13.7, 73.7, 55.5.
+  if (mb == 1 && (int64_t)max_tiles * (n_out / (swiglu ? 32 : 64)) <= 1024)
+    return swiglu ? launch_fp4<1, 1, 1, 4, 2, true>(args, stream)
+                  : launch_fp4<1, 1, 1, 4, 2, false>(args, stream);
   switch (mb) {
-    BEAM_FP4_CASE(1, 1, 1, 4)
-    BEAM_FP4_CASE(4, 1, 4, 4)
-    BEAM_FP4_CASE(6, 1, 4, 3)
-    BEAM_FP4_CASE(12, 2, 4, 4)
+    BEAM_FP4_CASE(1, 1, 1, 4, 1)
+    BEAM_FP4_CASE(4, 1, 4, 4, 1)
+    BEAM_FP4_CASE(6, 1, 4, 3, 1)
+    BEAM_FP4_CASE(12, 2, 4, 4, 1)
     default:
       return hipErrorInvalidValue;
   }
