@@ -485,7 +485,10 @@ __global__ __launch_bounds__(64 * kWaves) void select_backward_kernel(
 
 // Balance loss, first pass: a workgroup sums the normalised scores of its
 // tokens by expert (a wave's tokens in registers, then the waves in LDS, in a
-// fixed order) and counts their pairs (integer atomics in LDS).  part: [blocks][E]
+// fixed order) and counts their pairs (integer atomics in LDS).  A wave's sum is
+// one of up to 32768 tokens: in 64 bits, and rounded to 32 once, since 32 bits
+// would drift by up to half a step per token where a router's scores are alike
+// (5e-5 of the loss at 4096 tokens a wave).  part: [blocks][E]
 // sums, [blocks][E] counts, [blocks] rows with an expert.  At most 128 workgroups,
 // so that the second pass stays short: 4096 tokens of 256 experts take 5.5 us here and
 // 6.3 there, both latencies of dependent loads rather than their bytes (4.3 MB).
@@ -502,9 +505,9 @@ __global__ __launch_bounds__(64 * kBalanceWaves) void balance_part_kernel(
   const int E = c.experts;
   for (int e = threadIdx.x; e < V * 64; e += kThreads) counts[e] = 0;
   __syncthreads();
-  float sum[V];
+  double sum[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) sum[i] = 0.f;
+  for (int i = 0; i < V; ++i) sum[i] = 0.0;
   int mine = 0;
   const int64_t first = (int64_t)blockIdx.x * per, last = first + per < T ? first + per : T;
   auto load = [&](int64_t t, float (&z)[V], int& id) {  // of a token, if there is one
@@ -539,7 +542,7 @@ __global__ __launch_bounds__(64 * kBalanceWaves) void balance_part_kernel(
     total = wave_sum(total);
     const float inv = nan ? __builtin_nanf("") : total > 0.f ? 1.f / total : 0.f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum[i] += p[i] * inv;
+    for (int i = 0; i < V; ++i) sum[i] += (double)(p[i] * inv);
   };
   // the next token's logits are on their way while one is added
   float za[V], zb[V];
@@ -553,7 +556,7 @@ __global__ __launch_bounds__(64 * kBalanceWaves) void balance_part_kernel(
     if (t + kBalanceWaves < last) add(zb, ib);
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) sums[wave][lane + 64 * i] = sum[i];
+  for (int i = 0; i < V; ++i) sums[wave][lane + 64 * i] = (float)sum[i];
   if (lane == 0) rows[wave] = mine;
   __syncthreads();
   const int64_t B = gridDim.x;

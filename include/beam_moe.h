@@ -625,8 +625,8 @@ int moe_route_select(const moe_config_t* cfg, const moe_select_config_t* sel, co
  * load is the loss's derivative by every q_te (f is a count: no gradient).
  *   topk_ids  [T, topk] int32 in
  *   loss      [1] fp32 out, load [E] fp32 out (zeros without such rows)
- * Sums by expert are fp32 within a workgroup's tokens and 64 bits across them,
- * in a fixed order.  With no tokens nothing is written.  Workspace:
+ * Sums by expert are 64 bits within a wave's tokens, fp32 over the 16 waves of a
+ * workgroup and 64 bits across them, in a fixed order.  With no tokens nothing is written.  Workspace:
  * moe_balance_workspace_bytes.  Reads num_tokens, num_experts, topk, score and
  * logits_dtype of cfg.
  */
