@@ -14,10 +14,18 @@ import torch
 
 from ._lib import (DTYPE_BF16, DTYPE_FP32, ENTRY_ROUTE, MoeError, MoeSelectConfig, _check, lib,
                    make_config, workspace_bytes)
-from ._train import _at, _launch, _need, _scratch
+from ._train import _launch, _need, _scratch
 
 SCORES = {"sigmoid": 0, "softmax": 1}
 _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
+
+# torch gives an empty tensor no address.  The library reads and writes nothing of an
+# empty batch, but checks its arguments as any other's.
+_NOWHERE = 256
+
+
+def _at(t):
+    return None if t is None else t.data_ptr() or _NOWHERE
 
 
 # Configurations are values: one object per distinct set of numbers.
@@ -78,9 +86,7 @@ def select(logits, *, score="softmax", sel_bias=None, num_groups=1, topk_groups=
     cfg = _config(T, E, topk, score, renormalize, dt, num_groups, topk_groups, group_best)
     ids = torch.empty(T, topk, dtype=torch.int32, device=dev)
     w = torch.empty(T, topk, dtype=torch.float32, device=dev)
-    if T:
-        _launch("moe_select", dev, ctypes.byref(cfg), logits.data_ptr(), _at(sel_bias),
-                ids.data_ptr(), w.data_ptr())
+    _launch("moe_select", dev, ctypes.byref(cfg), _at(logits), _at(sel_bias), _at(ids), _at(w))
     return ids, w
 
 
@@ -106,11 +112,9 @@ def route_select(x, w_router, *, score="softmax", sel_bias=None, num_groups=1, t
     ids = torch.empty(T, topk, dtype=torch.int32, device=dev)
     w = torch.empty(T, topk, dtype=torch.float32, device=dev)
     z = torch.empty(T, E, dtype=torch.float32, device=dev) if return_logits else None
-    if T:
-        ws = _scratch(nb, dev, workspace)
-        _launch("moe_route_select", dev, ctypes.byref(cfg), ctypes.byref(sel), x.data_ptr(),
-                w_router.data_ptr(), _at(sel_bias), ids.data_ptr(), w.data_ptr(), _at(z), _at(ws),
-                nb)
+    ws = _scratch(nb, dev, workspace)
+    _launch("moe_route_select", dev, ctypes.byref(cfg), ctypes.byref(sel), _at(x), _at(w_router),
+            _at(sel_bias), _at(ids), _at(w), _at(z), _at(ws), nb)
     return (ids, w, z) if return_logits else (ids, w)
 
 
@@ -126,14 +130,12 @@ def balance_loss(logits, topk_ids, *, score="softmax", coef=1e-2, workspace=None
     k = _need_ids(topk_ids, T, dev)
     cfg = _config(T, E, k, score, True, dt)
     nb = _balance_bytes(T, E, k, score, dt)
-    if T == 0:
-        return (torch.zeros((), dtype=torch.float32, device=dev),
-                torch.zeros(E, dtype=torch.float32, device=dev))
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    load = torch.empty(E, dtype=torch.float32, device=dev)
+    new = torch.empty if T else torch.zeros  # the call writes nothing of no tokens
+    loss = new((), dtype=torch.float32, device=dev)
+    load = new(E, dtype=torch.float32, device=dev)
     ws = _scratch(nb, dev, workspace)
-    _launch("moe_balance_loss", dev, ctypes.byref(cfg), logits.data_ptr(), topk_ids.data_ptr(),
-            float(coef), loss.data_ptr(), load.data_ptr(), _at(ws), nb)
+    _launch("moe_balance_loss", dev, ctypes.byref(cfg), _at(logits), _at(topk_ids), float(coef),
+            _at(loss), _at(load), _at(ws), nb)
     return loss, load
 
 
@@ -160,7 +162,6 @@ def select_backward(logits, topk_ids, grad_topk_w, *, score="softmax", renormali
             raise ValueError(f"grad_loss must have one element, got {grad_loss.numel()}")
     cfg = _config(T, E, k, score, renormalize, dt)
     grad = torch.empty_like(logits)
-    if T:
-        _launch("moe_select_backward", dev, ctypes.byref(cfg), logits.data_ptr(),
-                topk_ids.data_ptr(), _at(grad_topk_w), _at(load), _at(grad_loss), grad.data_ptr())
+    _launch("moe_select_backward", dev, ctypes.byref(cfg), _at(logits), _at(topk_ids),
+            _at(grad_topk_w), _at(load), _at(grad_loss), _at(grad))
     return grad

@@ -1,0 +1,65 @@
+"""CPU-side checks of routing from logits and of the 4-bit expert calls at their
+edges: empty batches, and the workspaces' bounds."""
+import pytest
+import torch
+
+import grouped_top_routing_amd as gtr
+from grouped_top_routing_amd import _select as S
+
+F, I32 = torch.float32, torch.int32
+
+
+@pytest.fixture
+def on_cpu(monkeypatch):
+    """The binding's routing calls with CPU tensors taken for a device's: an
+    empty batch's call reads no memory and needs no device."""
+    monkeypatch.setattr(S, "_need", lambda *a: None)
+    monkeypatch.setattr(S, "_check", lambda *a: None)
+    monkeypatch.setattr(S, "_need_logits", lambda z: (*z.shape, z.dtype, z.device))
+
+    def launch(name, device, *args):
+        status = getattr(gtr.lib(), name)(*args, None)
+        if status:
+            raise gtr.MoeError(status, name)
+
+    monkeypatch.setattr(S, "_launch", launch)
+
+
+def z(E=64, T=0, dtype=F):
+    return torch.zeros(T, E, dtype=dtype)
+
+
+def test_empty_batches_give_empty_results(on_cpu):
+    ids, w = gtr.select(z(), topk=4, num_groups=8, topk_groups=4, sel_bias=torch.zeros(64))
+    assert ids.shape == w.shape == (0, 4)
+    loss, load = gtr.balance_loss(z(), ids)
+    assert loss.shape == () and load.shape == (64,) and not loss.any() and not load.any()
+    for kw in (dict(grad_topk_w=w), dict(grad_topk_w=w, load=load),
+               dict(grad_topk_w=None, load=load, grad_loss=torch.ones(()))):
+        assert gtr.select_backward(z(), ids, **kw).shape == (0, 64)
+    ids, w, logits = gtr.route_select(torch.zeros(0, 256, dtype=torch.bfloat16),
+                                      torch.zeros(256, 256), return_logits=True)
+    assert ids.shape == w.shape == (0, 8) and logits.shape == (0, 256)
+
+
+@pytest.mark.parametrize("kw", [dict(topk=100), dict(topk=0), dict(topk=9, num_groups=8),
+                                dict(num_groups=7), dict(num_groups=4, topk_groups=5),
+                                dict(group_best=3), dict(num_groups=0)])
+def test_empty_batches_are_refused_what_others_are(on_cpu, kw):
+    with pytest.raises(gtr.MoeError):
+        gtr.select(z(), **kw)
+    with pytest.raises(gtr.MoeError):
+        gtr.route_select(torch.zeros(0, 256, dtype=torch.bfloat16), torch.zeros(256, 256),
+                         **({**kw, "topk": 33} if kw.get("topk") == 9 else kw))
+
+
+def test_empty_batches_of_the_gradient_and_the_loss_are_refused_too(on_cpu):
+    ids = lambda k: torch.zeros(0, k, dtype=I32)
+    for E, k in ((64, 0), (64, 33), (2000, 8)):
+        with pytest.raises(gtr.MoeError):
+            gtr.select_backward(z(E), ids(k), torch.zeros(0, k))
+        with pytest.raises(gtr.MoeError):
+            gtr.balance_loss(z(E), ids(k))
+    for coef in (float("nan"), float("inf")):
+        with pytest.raises(gtr.MoeError):
+            gtr.balance_loss(z(), ids(2), coef=coef)
