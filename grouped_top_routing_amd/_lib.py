@@ -861,9 +861,9 @@ def expert_ffn_fp4(x, perm_src, offsets, w: Fp4Weights, *, topk=8, out=None, wor
         out = torch.empty(T * topk, H, dtype=torch.bfloat16, device=x.device)
     else:
         _check(out, "out", torch.bfloat16, (T * topk, H), x.device)
+    nb = workspace_bytes(cfg, ENTRY_EXPERT_FFN)  # checks an empty batch's sizes too
     if T == 0:
         return out
-    nb = workspace_bytes(cfg, ENTRY_EXPERT_FFN)
     ws = _ws(workspace, x.device).get(nb, x.device)
     _call("moe_expert_ffn_fp4", lib().moe_expert_ffn_fp4(
         ctypes.byref(cfg), _ptr(x), _ptr(perm_src), _ptr(offsets), _ptr(w.q_gate_up),
@@ -883,9 +883,9 @@ def expert_gate_up_fp4(x, perm_src, offsets, w: Fp4Weights, *, topk=8, workspace
     _check(offsets, "offsets", torch.int32, (E + 1,), x.device)
     cfg = _fp4_config(T, w, topk)
     h = torch.empty(T * topk, I, dtype=torch.bfloat16, device=x.device)
+    nb = workspace_bytes(cfg, ENTRY_EXPERT_STAGE)  # checks an empty batch's sizes too
     if T == 0:
         return h
-    nb = workspace_bytes(cfg, ENTRY_EXPERT_STAGE)
     ws = _ws(workspace, x.device).get(nb, x.device)
     _call("moe_expert_gate_up_fp4", lib().moe_expert_gate_up_fp4(
         ctypes.byref(cfg), _ptr(x), _ptr(perm_src), _ptr(offsets), _ptr(w.q_gate_up),
@@ -904,9 +904,9 @@ def expert_down_fp4(h, offsets, w: Fp4Weights, *, topk=8, workspace=None):
     _check(offsets, "offsets", torch.int32, (E + 1,), h.device)
     cfg = _fp4_config(T, w, topk)
     y = torch.empty(T * topk, H, dtype=torch.bfloat16, device=h.device)
+    nb = workspace_bytes(cfg, ENTRY_EXPERT_STAGE)  # checks an empty batch's sizes too
     if T == 0:
         return y
-    nb = workspace_bytes(cfg, ENTRY_EXPERT_STAGE)
     ws = _ws(workspace, h.device).get(nb, h.device)
     _call("moe_expert_down_fp4", lib().moe_expert_down_fp4(
         ctypes.byref(cfg), _ptr(h), _ptr(offsets), _ptr(w.q_down), _ptr(w.s_down), _ptr(y),
@@ -937,8 +937,8 @@ def layer_forward_fp4(x, w_router, w: Fp4Weights, *, sel_bias=None, num_groups=8
     if return_routing:
         ids = torch.empty(T, topk, dtype=torch.int32, device=x.device)
         tw = torch.empty(T, topk, dtype=torch.float32, device=x.device)
+    nb = workspace_bytes(cfg, ENTRY_LAYER)  # checks an empty batch's sizes too
     if T:
-        nb = workspace_bytes(cfg, ENTRY_LAYER)
         ws = _ws(workspace, x.device).get(nb, x.device)
         _call("moe_layer_forward_fp4", lib().moe_layer_forward_fp4(
             ctypes.byref(cfg), _ptr(x), _ptr(w_router), _ptr(sel_bias), _ptr(w.q_gate_up),

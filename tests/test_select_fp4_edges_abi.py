@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import grouped_top_routing_amd as gtr
+from grouped_top_routing_amd import _lib as L
 from grouped_top_routing_amd import _select as S
 
 F, I32 = torch.float32, torch.int32
@@ -63,3 +64,35 @@ def test_empty_batches_of_the_gradient_and_the_loss_are_refused_too(on_cpu):
     for coef in (float("nan"), float("inf")):
         with pytest.raises(gtr.MoeError):
             gtr.balance_loss(z(), ids(2), coef=coef)
+
+
+# ---------------------------------------------------------------------------
+def fp4_call(name, topk, groups=8, kept=4):
+    """`name` of no tokens on 4-bit experts, hidden 256, intermediate 128."""
+    E, H, I = 256, 256, 128
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    w = gtr.Fp4Weights(u8(E, 2 * I, H // 2), u8(E, 2 * I, H // 32), u8(E, H, I // 2),
+                       u8(E, H, I // 32))
+    x, h = torch.zeros(0, H, dtype=torch.bfloat16), torch.zeros(0, I, dtype=torch.bfloat16)
+    src, off = torch.zeros(0, dtype=I32), torch.zeros(E + 1, dtype=I32)
+    if name == "layer_forward_fp4":
+        return gtr.layer_forward_fp4(x, torch.zeros(E, H), w, topk=topk, num_groups=groups,
+                                     topk_groups=kept)
+    if name == "expert_down_fp4":
+        return gtr.expert_down_fp4(h, off, w, topk=topk)
+    return getattr(gtr, name)(x, src, off, w, topk=topk)
+
+
+@pytest.mark.parametrize("name,width", [("expert_ffn_fp4", 256), ("expert_gate_up_fp4", 128),
+                                        ("expert_down_fp4", 256), ("layer_forward_fp4", 256)])
+def test_empty_batches_of_4_bit_experts(monkeypatch, name, width):
+    monkeypatch.setattr(L, "_check", lambda *a: None)
+    assert fp4_call(name, 8).shape == (0, width)
+    with pytest.raises(gtr.MoeError):
+        fp4_call(name, 9)  # at most 8 slots
+    with pytest.raises(gtr.MoeError):
+        fp4_call(name, 300)
+    if name == "layer_forward_fp4":
+        for groups, kept in ((7, 4), (8, 9), (0, 0)):
+            with pytest.raises(gtr.MoeError):
+                fp4_call(name, 8, groups, kept)
