@@ -46,6 +46,9 @@ __device__ __forceinline__ uint32_t e8m0_of(float most) {
   return (uint32_t)(c < 1 ? 1 : c);
 }
 
+// The float whose exponent field is the code, which is all that the conversion
+// takes of its scale: 0 stands for 2^-127 (codes .5, 1 and 1.5 of it are subnormal
+// in bf16, and the MFMA keeps them) and infinity for NaN.
 __device__ __forceinline__ float e8m0_value(uint32_t code) { return __uint_as_float(code << 23); }
 
 }  // namespace

@@ -297,7 +297,9 @@ int moe_layer_forward_fp8(const moe_config_t* cfg, const uint16_t* x, const floa
  * Each expert matrix row n (output channel) has E2M1 codes q[n, k] (1 sign, 2
  * exponent, 1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6) and one E8M0 scale s[n,
  * k / 32]; the matrix the GEMMs use is w[n, k] = 2^(s - 127) * q[n, k], exact
- * in bf16 (s = 255 is NaN; a value past the largest bf16 is infinite).
+ * in bf16 for every s but 255, subnormal values (s of 0 and 1) included; s = 255
+ * is NaN with every code, and a value past the largest bf16 (s of 253 and 254) is
+ * infinite.
  * Activations stay bf16, accumulation fp32.  The router, selection, permutation
  * and combine are the bf16 path's.
  *
@@ -322,7 +324,8 @@ int moe_layer_forward_fp8(const moe_config_t* cfg, const uint16_t* x, const floa
  * group is the least power of two, at least 2^-126, by which its largest
  * magnitude is at most 7 (so that no weight is off by more than half a step);
  * codes are to the nearest, ties to the even code, magnitudes above 6 to 6.  A
- * group with an infinity or a NaN gets the scale NaN.
+ * group with an infinity or a NaN gets the scale NaN; a weight past 7 * 2^125
+ * (2.98e38) rounds to 4 * 2^126, which bf16 holds as infinity.
  *   w_gate_up, w_down  row-major bf16 inputs [E, 2I, H], [E, H, I]
  *   q_*, s_*           outputs as above; must not overlap the inputs or each other
  * Either set (w, q, s) may be all NULL to skip it.  num_tokens and
