@@ -685,7 +685,8 @@ hipError_t launch_grouped_gemm_fp4(int mb, bool swiglu, const uint16_t* A, const
   // A token's few items: two waves share each one's k.  In us, one wave / two: 1 token
   // of 5120 x 2560 (720 items) 42.5 / 38.7, 4 of 1024 x 512 15.8 / 15.2, but 2 of 5120
   // x 2560 (1360 items, the CUs hold 1024 pairs) 66.8 / 70.9, 100 of 1024 x 512 42.8 /
-  // 49.0; four waves 38.6, 13.7, 73.7, 55.5.
+  // 49.0; four waves 38.6, 13.7, 73.7, 55.5.  The order of a row's sums, and so its last
+  // bits, go by this choice, that is by the pairs of the whole call.
   if (mb == 1 && (int64_t)max_tiles * (n_out / (swiglu ? 32 : 64)) <= 1024)
     return swiglu ? launch_fp4<1, 1, 1, 4, 2, true>(args, stream)
                   : launch_fp4<1, 1, 1, 4, 2, false>(args, stream);

@@ -342,7 +342,10 @@ int moe_pack_fp4(const moe_config_t* cfg, const uint8_t* c_gate_up, const uint8_
 
 /* moe_expert_ffn, moe_expert_gate_up, moe_expert_down and moe_layer_forward
  * with 4-bit expert weights (arguments as in those calls; the expert calls
- * refuse outputs or a workspace that overlap another argument). */
+ * refuse outputs or a workspace that overlap another argument).  A call repeated
+ * gives the same bits.  Calls of different sizes may not for the same row: where a
+ * call has few pairs a row is summed over the two halves of k, in others over all of
+ * it in order. */
 int moe_expert_ffn_fp4(const moe_config_t* cfg, const uint16_t* x, const int32_t* perm_src,
                        const int32_t* offsets, const uint8_t* q_gate_up, const uint8_t* s_gate_up,
                        const uint8_t* q_down, const uint8_t* s_down, uint16_t* y_perm,

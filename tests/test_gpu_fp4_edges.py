@@ -1,4 +1,5 @@
-"""4-bit expert weights on the GPU at their edges: every code under every scale."""
+"""4-bit expert weights on the GPU at their edges: every code under every scale,
+and the rows of a call beside those of another."""
 import numpy as np
 import pytest
 import torch
@@ -9,6 +10,7 @@ from parity_util import say
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda", 0)
+U, UB = 2.0 ** -24, 2.0 ** -8
 BF = torch.bfloat16
 E = 256
 
@@ -93,3 +95,55 @@ def test_the_largest_weights(all_scales):
     y = n64(gtr.expert_down_fp4(h, off, w, topk=1)[:2])
     assert (y[:, 0] == 6 * 2.0 ** 25).all() and (y[:, 1] == np.inf).all()
     assert (y[:, 2] == -np.inf).all() and not y[:, 3:].any()
+
+
+def silu(g):
+    return g / (1 + np.exp(-g))
+
+
+@pytest.mark.parametrize("H,I", [(1024, 512), (2560, 1280)])
+def test_rows_alone_and_among_others(H, I):
+    """The pairs of a call choose its tiles, and up to 1024 items of 16 rows two
+    waves that take half of k each: a token's outputs may differ in their last bits
+    from one call to another.  Each call is within the bound of H, then I, roundings
+    (U per addition, in any order) and one of each output to bf16; calls that take
+    k in one chain agree bit for bit."""
+    say(f"[expert_ffn_fp4] rows alone and among others, H={H} I={I}")
+    g = torch.Generator(device=DEV).manual_seed(H)
+    r = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, device=DEV, dtype=torch.uint8)
+    arrays = (r(0, 256, E, 2 * I, H // 2), r(118, 122, E, 2 * I, H // 32),
+              r(0, 256, E, H, I // 2), r(118, 122, E, H, I // 32))
+    w = gtr.pack_fp4(*arrays)
+    k, T = 4, 4000
+    x = torch.randn(T, H, generator=g, device=DEV).to(BF)
+    ids = torch.rand(T, E, generator=g, device=DEV).topk(k, 1).indices.to(torch.int32)
+    gate_up, down = {}, {}
+    for n in (1, 3, 40, 300, 2000, T):
+        _, off, src, dst = gtr.permute(ids[:n].contiguous())
+        h = gtr.expert_gate_up_fp4(x[:n], src, off, w, topk=k)
+        y = gtr.expert_down_fp4(h, off, w, topk=k)
+        assert torch.equal(y, gtr.expert_ffn_fp4(x[:n], src, off, w, topk=k))
+        first = dst[:k].long()  # the rows of token 0
+        gate_up[n], down[n] = h[first], y[first]
+    items = lambda n: (n * k // 16 + min(n * k, E) + 1)
+    split = [n for n in gate_up if items(n) * (I // 32) <= 1024 and n * k <= E // 4]
+    chain = [n for n in gate_up if items(n) * (I // 32) > 1024 and items(n) * (H // 64) > 1024]
+    assert 1 in split and T in chain and 300 in chain
+    for n in chain:
+        assert torch.equal(gate_up[n], gate_up[T])
+    dense = lambda q, s, e: fp4.dequantize(
+        np.stack((q[e].cpu().numpy() & 15, q[e].cpu().numpy() >> 4), -1).reshape(q.shape[1], -1),
+        s[e].cpu().numpy())
+    X = n64(x[0])
+    for j, e in enumerate(ids[0].tolist()):
+        W, D = dense(*arrays[:2], e), dense(*arrays[2:], e)
+        s, mag = W @ X, np.abs(W) @ np.abs(X) * (H * U)
+        a, u, da, du = s[:I], s[I:], mag[:I], mag[I:]
+        want = silu(a) * u
+        bound = 1.1 * np.abs(u) * da + np.abs(a) * du + 1.1 * da * du + (8 * U + UB) * np.abs(want)
+        for n in gate_up:
+            h = n64(gate_up[n][j])
+            assert (np.abs(h - want) <= bound).all(), (n, j)
+            y = D @ h
+            assert (np.abs(n64(down[n][j]) - y)
+                    <= I * U * (np.abs(D) @ np.abs(h)) + UB * np.abs(y)).all(), (n, j)
