@@ -96,3 +96,34 @@ def test_empty_batches_of_4_bit_experts(monkeypatch, name, width):
         for groups, kept in ((7, 4), (8, 9), (0, 0)):
             with pytest.raises(gtr.MoeError):
                 fp4_call(name, 8, groups, kept)
+
+
+def tile_rows(pairs, weights):
+    """Rows per tile of a call of this many pairs on experts of hidden *
+    intermediate weights."""
+    if pairs <= 64 or pairs <= 1024 and min(pairs, 256) * weights <= 1 << 28:
+        return 16
+    return 64 if pairs // 256 <= 50 else 96 if pairs // 256 <= 80 else 192
+
+
+@pytest.mark.parametrize("H,I", [(5120, 2560), (256, 128)])
+@pytest.mark.parametrize("k", [1, 8])
+def test_fp4_plans_hold_the_worst_split_of_the_pairs(H, I, k):
+    """The most tiles that T * k pairs make are one ragged tile for each expert in
+    use and whole ones of the rest: the plan has a count (and three words beside
+    it) and five words per tile."""
+    for T in (0, 1, 2, 7, 8, 9, 31, 64, 128, 129, 1000, 1631, 1632, 2592, 4096, 100000, 1 << 24,
+              (1 << 28) - 1):
+        n = T * k
+        rows = tile_rows(n, H * I)
+        # 1 pair each to all experts but one, the rest to that one, or a row more
+        # than whole tiles to each
+        tiles = [n] if n <= 256 else [255 + -(-(n - 255) // rows)]
+        if n > 256:
+            each = (n // 256 - 1) // rows * rows + 1
+            tiles.append(255 * -(-each // rows) + -(-(n - 255 * each) // rows))
+        cfg = gtr.make_config(T, H, I, topk=k, num_groups=1, topk_groups=1,
+                              weight_layout=gtr.LAYOUT_FP4_PACKED)
+        need = 4 * (4 + 5 * max(tiles))
+        assert gtr.workspace_bytes(cfg, gtr.ENTRY_EXPERT_STAGE) >= need, (T, k)
+        assert gtr.workspace_bytes(cfg, gtr.ENTRY_EXPERT_FFN) >= need + 2 * n * I, (T, k)
