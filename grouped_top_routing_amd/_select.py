@@ -95,7 +95,11 @@ def route_select(x, w_router, *, score="softmax", sel_bias=None, num_groups=1, t
     """select on the logits of the block's router (as route computes them in
     FP32 from x bf16 [T, H] and w_router fp32 [256, H]): (topk_ids, topk_w), and
     with return_logits all logits too (fp32 [T, E], for select_backward and
-    balance_loss)."""
+    balance_loss).
+
+    route and layer_forward compare scores in fp32: with sigmoids and groups the
+    choice is theirs but where values are nearer than that (scores of 1, say), so
+    a router that they are to serve is trained on the ids of route."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise TypeError("x must be a torch.Tensor [T, H]")
     if not isinstance(w_router, torch.Tensor) or w_router.dim() != 2:

@@ -616,6 +616,10 @@ int moe_select(const moe_select_config_t* cfg, const void* logits, const float* 
  * logits.
  *   logits  [T, E] fp32 out or NULL: what moe_select_backward starts from
  * Workspace MOE_ENTRY_ROUTE of cfg.
+ * By the block's rule (sigmoids, groups by two best) the choice is moe_route's but
+ * where values are as near as fp32 roundings: moe_route and moe_layer_forward compare
+ * fp32 scores, also without a bias, and take the lower index where all are 1.  A
+ * router that those are to serve is trained on the ids of moe_route.
  */
 int moe_route_select(const moe_config_t* cfg, const moe_select_config_t* sel, const uint16_t* x,
                      const float* w_router, const float* sel_bias, int32_t* topk_ids,

@@ -57,3 +57,66 @@ def test_balance_loss_of_many_live_tokens(T, E, score, dt):
     D = float((z.amax(1) - z.amin(1)).max())
     assert abs(float(loss) - want) <= (47 + 2 * D) * U * want
     assert (np.abs(n64(load) - want_load) <= 2 * U * want_load).all()
+
+
+# ---------------------------------------------------------------------------
+RULE = dict(num_groups=8, topk_groups=4, topk=8)
+
+
+def order_gaps(z, bias):
+    """By how much the order that the block's rule makes of scores in 64 bits is the
+    nearest one, [T]: the smallest gap between neighbours among the nine best experts
+    of the kept groups, and between the last kept group and the first that is not."""
+    v = ref.scores(z, "sigmoid") + (0.0 if bias is None else bias)
+    groups = np.sort(v.reshape(len(v), 8, 32), 2)[:, :, -2:].sum(2)
+    rank = np.argsort(-groups, 1, kind="stable")
+    total = np.take_along_axis(groups, rank, 1)
+    keep = np.zeros_like(groups, bool)
+    np.put_along_axis(keep, rank[:, :4], True, 1)
+    best = -np.sort(-np.where(np.repeat(keep, 32, 1), v, -np.inf), 1)[:, :9]
+    return np.minimum(-np.diff(best, axis=1).max(1), total[:, 3] - total[:, 4])
+
+
+@pytest.mark.parametrize("T,H", [(1, 256), (37, 512), (700, 1280)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_route_select_by_the_blocks_rule(T, H, biased):
+    """Sigmoids, groups and a bias behind the router GEMM: the reference's choice
+    from the call's own logits; route's too, but where scores are nearer than fp32
+    tells apart (a sigmoid within 4 U, with a bias 5 U of the value, twice that for
+    a pair and again for a group's sum; values below 4 here: 80 U)."""
+    say(f"[route_select] T={T} H={H} bias={biased}")
+    g = torch.Generator().manual_seed(T)
+    x = torch.randn(T, H, generator=g).to(torch.bfloat16).to(DEV)
+    W = (torch.randn(256, H, generator=g) * 0.05).to(DEV)
+    bias = (torch.randn(256, generator=g) * 0.2).to(DEV) if biased else None
+    for renormalize in (True, False):
+        kw = dict(sel_bias=bias, renormalize=renormalize, **RULE)
+        ids, w, z = gtr.route_select(x, W, score="sigmoid", group_best=2, return_logits=True, **kw)
+        want, want_w = ref.select(n64(z), score="sigmoid", group_best=2,
+                                  **{**kw, "sel_bias": None if bias is None else n64(bias)})
+        assert np.array_equal(ids.cpu().numpy(), want)
+        # logits of the chosen are above -8 here: as a renormalised weight of select,
+        # (40 + 8 * 8 + 2 * 8) U
+        assert np.abs(ref.log_scores(n64(z), "sigmoid")[np.arange(T)[:, None], want]).max() < 8
+        assert (np.abs(n64(w) - want_w) <= 120 * U * want_w).all()
+        rid, rw = gtr.route(x, W, **kw)
+        sure = order_gaps(n64(z), None if bias is None else n64(bias)) > 80 * U
+        assert sure.mean() > 0.9
+        assert np.array_equal(rid.cpu().numpy()[sure], want[sure])
+        assert (np.abs(n64(rw)[sure] - want_w[sure]) <= 120 * U * want_w[sure]).all()
+
+
+def test_route_and_route_select_at_scores_of_one():
+    """Logits from 30 up: every sigmoid is 1 in fp32, by which route orders experts;
+    route_select tells groups apart in 64 bits, and experts by their logits."""
+    say("[route_select] saturated scores")
+    x = torch.zeros(3, 256, dtype=torch.bfloat16, device=DEV)
+    x[:, 0] = 1
+    W = torch.zeros(256, 256, device=DEV)
+    W[:, 0] = 30 + torch.arange(256, device=DEV) / 8
+    rid, _ = gtr.route(x, W, **RULE)
+    assert (rid.cpu() == torch.arange(8)).all()
+    ids, w, z = gtr.route_select(x, W, score="sigmoid", return_logits=True, **RULE)
+    want, _ = ref.select(n64(z), score="sigmoid", **RULE)
+    assert np.array_equal(ids.cpu().numpy(), want) and want[0].min() > 31
+    assert torch.equal(w, torch.full_like(w, 0.125))
