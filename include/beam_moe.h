@@ -583,7 +583,9 @@ int moe_adamw_step(const moe_adamw_t* opt, const moe_adamw_tensor_t* tensors, in
  * its row's weights, and its row's part of the gradient and of the loss, NaN.
  *
  * Limits: num_experts <= 1024, num_groups <= 64 (a divisor of num_experts),
- * topk <= 32, num_tokens < 2^26; others return MOE_ERR_UNSUPPORTED.  Logits and
+ * topk <= 32, num_tokens < 2^26; others return MOE_ERR_UNSUPPORTED.  (The calls
+ * that take the ids on, moe_permute and the expert calls, have 256 experts and topk
+ * <= 8; other counts are for experts of the caller's own.)  Logits and
  * their gradient are dense [T, E] of logits_dtype and need only the alignment
  * of their elements.  Outputs that overlap an input or each other are refused.
  */
