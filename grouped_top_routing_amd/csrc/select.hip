@@ -233,9 +233,17 @@ __device__ __forceinline__ int choose(const T (&order)[V], int topk, int lane, f
 // Selection.  Two experts (or groups) whose values differ by less than an fp32
 // rounding are ordered by the values, not by the roundings: values are compared
 // in fp32, and a token whose order has a gap within their errors is done again in
-// 64 bits (of random logits one in 240 with sigmoids, a bias and groups, one in 1250
-// with softmax).  Without a bias experts are ordered by their logits, and only groups
-// need scores.
+// 64 bits.  Without a bias experts are ordered by their logits, and only groups need
+// scores.
+//
+// How many are done again goes by the logits.  Of normal ones over 256 experts in 8
+// groups, 4 kept, 8 chosen, at standard deviations of 1.5 / 3 / 5: sigmoids with a
+// bias of deviation 0.3 0.1 % / 0.2 % / 0.2 % of the tokens, without one 0.04 / 0.3 /
+// 6, with a bias of zeros 0.7 / 8 / 93 (saturated scores lie close together, and the
+// bound is that of the row's largest score); softmax 0.02-0.2 / 0.02-0.5 / 0.5-5.
+// Equal logits under equal biases count as near too: bf16 logits and a bias of zeros
+// 30-37 % from 1.5 on.  16384 tokens take 26-29 us where few are, 48 where all are;
+// 32 tokens 8.0 and 11.5 (calls from Python).
 //
 // Bound by the instructions of topk dependent rounds: 16384 tokens of 256 experts,
 // 8 chosen, take 12.7 us (1.4 TB/s; their bytes would take 3.4).  Keys are integers
