@@ -139,7 +139,7 @@ def balance_loss(logits, topk_ids, *, score="softmax", coef=1e-2, workspace=None
     load = new(E, dtype=torch.float32, device=dev)
     ws = _scratch(nb, dev, workspace)
     _launch("moe_balance_loss", dev, ctypes.byref(cfg), _at(logits), _at(topk_ids), float(coef),
-            _at(loss), _at(load), _at(ws), nb)
+            loss.data_ptr(), load.data_ptr(), _at(ws), nb)
     return loss, load
 
 

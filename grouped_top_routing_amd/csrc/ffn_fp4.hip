@@ -53,7 +53,9 @@ __device__ __forceinline__ float e8m0_value(uint32_t code) { return __uint_as_fl
 
 }  // namespace
 
-// One thread per 32 consecutive weights of a row.  Load time only; bound by HBM.
+// One thread per 32 consecutive weights of a row.  Load time only: gate/up of 256
+// experts of 5120 x 2560 (13.4 GB read, 3.6 written) take 5.96 ms, 2.9 TB/s, since
+// codes are stored four bytes at a time, in fragment order.
 __global__ __launch_bounds__(256) void quantize_fp4_kernel(const uint16_t* __restrict__ w,
                                                            uint8_t* __restrict__ q,
                                                            uint8_t* __restrict__ s, int K,
@@ -160,13 +162,13 @@ __global__ __launch_bounds__(256) void pack_fp4_kernel(const uint8_t* __restrict
 // workgroup issues its next item's first S stages before the current item's outputs
 // are written.
 //
-// Measured at 256 experts of 5120 x 2560, gate/up and down in us: 1 token 23 and 12
-// (4.7 TB/s of codes and scales: launch and first latencies), 32 tokens 350 and 178
-// (6.5 TB/s: bound by HBM; a copy of the loop that only loads takes 0.96 of it), 512
-// tokens 605 and 348 (5.8 and 5.2 TB/s, HBM), 4096 tokens 1550 and 800 (1.1
-// PFLOP/s; MFMAs take 52 % of the cycles, load issue and LDS reads do not hide behind
-// them: without the loads 1244, without the MFMAs 960, without the widening no
-// change).
+// Measured at 256 experts of 5120 x 2560, gate/up and down in us, medians: 1 token 23
+// and 13 (4.8 and 4.3 TB/s of codes and scales: launch and first latencies), 32 tokens
+// 349 and 181 (6.6 and 6.3 TB/s: bound by HBM; a copy of the loop that only loads takes
+// 0.96 of it), 512 tokens 604 and 348 (6.0 and 5.1 TB/s, HBM), 4096 tokens 1604 and 826
+// (1.07 and 1.04 PFLOP/s; MFMAs take 52 % of the cycles, load issue and LDS reads do
+// not hide behind them: of 1549 in the fastest runs 1244 without the loads, 960 without
+// the MFMAs, no change without the widening).
 constexpr int kCols = 4;         // column blocks per wave
 constexpr int kHalfB = kCodeB / 2;  // codes of a block's 64 k
 constexpr int kBlockA = 2048;    // bytes of 64 k of a row block

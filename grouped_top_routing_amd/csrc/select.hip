@@ -246,9 +246,10 @@ __device__ __forceinline__ int choose(const T (&order)[V], int topk, int lane, f
 // 32 tokens 8.0 and 11.5 (calls from Python).
 //
 // Bound by the instructions of topk dependent rounds: 16384 tokens of 256 experts,
-// 8 chosen, take 12.7 us (1.4 TB/s; their bytes would take 3.4).  Keys are integers
-// because a float maximum takes two instructions per DPP step (14.4 us).  32 tokens
-// are one chain of latencies, 7.7 us with sigmoids, bias and groups.
+// 8 chosen, take 13.6 us (12.4 the fastest; their bytes would take 3.4).  Keys are integers
+// because a float maximum takes two instructions per DPP step (14.4 us a call, 12.7 with
+// keys).  32 tokens are one chain of latencies, 6.6 us at the fastest with sigmoids, bias
+// and groups, 10.8 where the GPU idles between.
 //
 // Bound: with s_max the row's largest score, a score carries at most 48 U s_max
 // (U = 2^-24; exponential 2 U, its argument's rounding U |d| at exp(-|d|), a sum
@@ -382,7 +383,7 @@ __global__ __launch_bounds__(64 * kWaves) void select_experts_kernel(
 //   ... renormalised:     dz_e = sum_{j of e} w_j (g_j - sum_C g_i w_i)
 //   balance:              + gl q_e (load_e - sum_i load_i q_i) [(1 - s_e) for the sigmoid]
 // in rows with a slot in C; other rows get zeros.  One read of the logits, one write;
-// 4096 tokens of 256 experts with the balance loss take 6.7 us (1.3 TB/s), 509 of 60
+// 4096 tokens of 256 experts with the balance loss take 6.6 us (1.3 TB/s), 509 of 60
 // experts 3.6: the latencies of a wave's loads (logits, ids, the chosen logits) and
 // sums.
 template <class Z, int V>
@@ -498,7 +499,7 @@ __global__ __launch_bounds__(64 * kWaves) void select_backward_kernel(
 // would drift by up to half a step per token where a router's scores are alike
 // (5e-5 of the loss at 4096 tokens a wave).  part: [blocks][E]
 // sums, [blocks][E] counts, [blocks] rows with an expert.  At most 128 workgroups,
-// so that the second pass stays short: 4096 tokens of 256 experts take 5.5 us here and
+// so that the second pass stays short: 4096 tokens of 256 experts take 5.7 us here and
 // 6.3 there, both latencies of dependent loads rather than their bytes (4.3 MB).
 template <class Z, int V>
 __global__ __launch_bounds__(64 * kBalanceWaves) void balance_part_kernel(
